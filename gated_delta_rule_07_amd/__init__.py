@@ -12,6 +12,10 @@ fallback: without the library or a GPU these functions raise.
     Phi, Psi = segment_map(q, k, v, alpha, b, w)  # per-sequence state maps
     S_in, S_final = segment_combine(Phi, Psi, S0) # entering state of each segment
 
+and, for the attention layers of a hybrid stack (see ``attention``),
+``qk_norm_rope``, ``qk_norm_rope_bwd``, ``rope_frequencies``, ``attn_fwd``,
+``attn_bwd``, ``attn_paged``, ``kv_cache_write`` and ``kv_cache_read``.
+
 Shapes: q, k, alpha, b [B, T, H, dk]; v, w [B, T, H, dv] (packed sequences:
 B = 1 and ``cu_seqlens`` int32 [N + 1] on the device); states [N, H, dk, dv]
 float32.  Inputs are float32 or bfloat16 and must all have the same dtype.
@@ -76,6 +80,28 @@ def configure(L: ctypes.CDLL) -> ctypes.CDLL:
     L.gdn2_segment_combine.argtypes = [vp] * 3 + [i] * 4 + [vp, vp, vp]
     L.gdn2_decode_step.restype = i
     L.gdn2_decode_step.argtypes = [vp] * 8 + [i] * 5 + [vp]
+    f = ctypes.c_float
+    rope = [vp] * 6
+    L.gdn2_qk_norm_rope_fwd.restype = i
+    L.gdn2_qk_norm_rope_fwd.argtypes = rope + [i] * 6 + [f, i, u32, vp, vp, vp]
+    L.gdn2_qk_norm_rope_bwd_workspace_bytes.restype = sz
+    L.gdn2_qk_norm_rope_bwd_workspace_bytes.argtypes = [i] * 5
+    L.gdn2_qk_norm_rope_bwd.restype = i
+    L.gdn2_qk_norm_rope_bwd.argtypes = rope + [vp, vp] + [i] * 6 + [f, i, u32] + [vp] * 4 + [vp, sz, vp]
+    L.gdn2_attn_fwd.restype = i
+    L.gdn2_attn_fwd.argtypes = [vp] * 4 + [i] * 7 + [f, i, vp, vp, vp]
+    L.gdn2_attn_bwd_workspace_bytes.restype = sz
+    L.gdn2_attn_bwd_workspace_bytes.argtypes = [i] * 5
+    L.gdn2_attn_bwd.restype = i
+    L.gdn2_attn_bwd.argtypes = [vp] * 7 + [i] * 7 + [f, i, vp, vp, vp, vp, sz, vp]
+    L.gdn2_attn_paged_workspace_bytes.restype = sz
+    L.gdn2_attn_paged_workspace_bytes.argtypes = [i] * 9
+    L.gdn2_attn_paged.restype = i
+    L.gdn2_attn_paged.argtypes = [vp] * 8 + [i] * 10 + [f, i, i, vp, vp, vp, sz, vp]
+    L.gdn2_kv_cache_write.restype = i
+    L.gdn2_kv_cache_write.argtypes = [vp] * 3 + [i] * 7 + [vp] * 5
+    L.gdn2_kv_cache_read.restype = i
+    L.gdn2_kv_cache_read.argtypes = [vp] + [i] * 7 + [vp] * 7
     L.gdn2_status_string.restype = ctypes.c_char_p
     L.gdn2_status_string.argtypes = [i]
     L.gdn2_last_error.restype = ctypes.c_char_p
@@ -389,9 +415,14 @@ def profile_enable(on: bool = True) -> None:
 def profile_read(reset: bool = True) -> dict:
     """{kernel name: (total ms, launches)} since the last reset."""
     n = ctypes.c_int(0)
-    cap = 16
+    cap = 32
     names = (ctypes.c_char_p * cap)()
     ms = (ctypes.c_double * cap)()
     cnt = (ctypes.c_int * cap)()
     _check(lib().gdn2_profile_read(cap, names, ms, cnt, ctypes.byref(n), 1 if reset else 0))
     return {names[i].decode(): (ms[i], cnt[i]) for i in range(min(n.value, cap))}
+
+
+from .attention import (attn_bwd, attn_bwd_workspace_bytes, attn_fwd, attn_paged,  # noqa: E402,F401
+                        attn_paged_workspace_bytes, kv_cache_read, kv_cache_write, qk_norm_rope, qk_norm_rope_bwd,
+                        rope_frequencies)

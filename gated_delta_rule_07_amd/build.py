@@ -7,7 +7,7 @@ gated_delta_rule_07_amd/libgdn2.so.  Packed-FP32 instruction selection is
 switched off for device code (the flag is harmless for the host pass).
 
 It also links libgdn2_hostcheck.so: the same kernels with the host side of
-gdn2_api.cpp (argument checks, workspace planning, launch set-up) built with
+the C-ABI files (gdn2_api.cpp, gdn2_attn_api.cpp: argument checks, workspace planning, launch set-up) built with
 undefined-behaviour checks that trap (signed overflow, shifts, array bounds,
 misaligned or null accesses), for the host-side tests.  The product binding
 never loads it.
@@ -27,7 +27,8 @@ BUILD = os.path.join(HERE, "_build")
 ARCH = os.environ.get("GDN2_OFFLOAD_ARCH", "gfx950")
 
 SOURCES = ["gdn2_api.cpp", "gdn2_recurrent.hip", "gdn2_chunk.hip", "gdn2_fused.hip", "gdn2_bwd.hip", "gdn2_segment.hip",
-           "gdn2_rule_r1.hip", "gdn2_pad.hip"]
+           "gdn2_rule_r1.hip", "gdn2_pad.hip", "gdn2_attn_api.cpp", "gdn2_qkrope.hip", "gdn2_attn_fwd.hip",
+           "gdn2_attn_bwd.hip", "gdn2_kvcache.hip"]
 COMMON = ["-O3", "-fPIC", "-std=c++17", f"--offload-arch={ARCH}",
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
           "-Wall", "-Wno-unused-command-line-argument"]
@@ -36,7 +37,7 @@ COMMON = ["-O3", "-fPIC", "-std=c++17", f"--offload-arch={ARCH}",
 # default the compiler keeps them in AGPRs and copies them to VGPRs and back
 # every chunk, which the VGPR form of the products avoids.
 EXTRA = {"gdn2_segment.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
-# Host-only undefined-behaviour traps for the checked build of gdn2_api.cpp
+# Host-only undefined-behaviour traps for the checked build of the C-ABI files
 # (each flag after -Xarch_host: device code is compiled as in the product).
 HOSTCHECK = [f for x in ("-fsanitize=undefined", "-fsanitize-trap=undefined", "-fsanitize=bounds",
                          "-fno-sanitize-recover=all") for f in ("-Xarch_host", x)]
@@ -72,13 +73,14 @@ def _link(objs: list[str], out: str) -> None:
 
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+    checked = [src for src in SOURCES if src.endswith(".cpp")]
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + len(checked)) as ex:
         futs = [ex.submit(_compile, src) for src in SOURCES]
-        checked_api = ex.submit(_compile, "gdn2_api.cpp", True)
+        checked_futs = {src: ex.submit(_compile, src, True) for src in checked}
         objs = [f.result() for f in futs]
-        api_checked = checked_api.result()
+        checked_objs = {src: f.result() for src, f in checked_futs.items()}
     _link(objs, OUT)
-    _link([api_checked if o.endswith("gdn2_api.o") else o for o in objs], OUT_HOSTCHECK)
+    _link([checked_objs.get(src, obj) for src, obj in zip(SOURCES, objs)], OUT_HOSTCHECK)
     if verbose:
         print(f"built {OUT} and {OUT_HOSTCHECK}")
     return OUT

@@ -5,82 +5,19 @@
 
 #include <hip/hip_runtime.h>
 
-#include <cstdarg>
-#include <cstdio>
 #include <mutex>
-#include <string>
 #include <utility>
 #include <vector>
 
+#include "gdn2_host.hpp"
 #include "gdn2_kernels.hpp"
+
+using namespace gdn2::host;
 
 namespace {
 
-thread_local std::string g_last_error;
-
-gdn2_status_t fail(gdn2_status_t st, const char *fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  g_last_error = buf;
-  return st;
-}
-
-gdn2_status_t ok() {
-  g_last_error.clear();
-  return GDN2_OK;
-}
-
 bool supported_dim(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
 bool supported_chunk(int c) { return c == 16 || c == 64; }
-
-size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-
-// ------------------------------------------------------------- profiling --
-// Kernel names are string literals of this file, so the pointers handed out
-// by gdn2_profile_read stay valid for the life of the library.
-struct prof_rec {
-  const char *name;
-  hipEvent_t start, stop;
-};
-std::mutex g_prof_mu;
-bool g_prof_on = false;
-std::vector<prof_rec> g_prof_pending;
-std::vector<std::pair<const char *, std::pair<double, int>>> g_prof_total;
-
-struct prof_scope {
-  hipStream_t st;
-  bool on;
-  prof_rec rec;
-  prof_scope(const char *name, hipStream_t s) : st(s), on(false) {
-    std::lock_guard<std::mutex> lk(g_prof_mu);
-    if (!g_prof_on)
-      return;
-    // no system-scope fence: a fenced event would write back the L2 between
-    // the two passes and slow down the very launches being timed
-    if (hipEventCreateWithFlags(&rec.start, hipEventDisableSystemFence) != hipSuccess)
-      return;
-    if (hipEventCreateWithFlags(&rec.stop, hipEventDisableSystemFence) != hipSuccess) {
-      (void)hipEventDestroy(rec.start);
-      return;
-    }
-    rec.name = name;
-    on = hipEventRecord(rec.start, st) == hipSuccess;
-    if (!on) {
-      (void)hipEventDestroy(rec.start);
-      (void)hipEventDestroy(rec.stop);
-    }
-  }
-  ~prof_scope() {
-    if (!on)
-      return;
-    (void)hipEventRecord(rec.stop, st);
-    std::lock_guard<std::mutex> lk(g_prof_mu);
-    g_prof_pending.push_back(rec);
-  }
-};
 
 // --------------------------------------------------------------- dispatch --
 template <typename IO, int D, int C> size_t block_bytes() { return gdn2::chunk_block_bytes<IO, D, C>(); }
@@ -552,7 +489,6 @@ bwd_plan plan_bwd(gdn2_dtype_t dt, int B, int T, int H, int d, int N, int chunk,
 }
 
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // ------------------------------------------------------------ segment maps --
 template <typename IO, int D, int C>

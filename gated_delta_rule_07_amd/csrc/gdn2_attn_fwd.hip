@@ -1,0 +1,590 @@
+// gdn2_attn_fwd.hip -- causal attention with grouped heads, for gfx950: over
+// whole packed sequences, and over a paged cache.
+//
+//   s_ij = scale q_i . k_j for the visible keys j (j <= pos(i), and with a
+//   window W, j > pos(i) - W);  o_i = sum_j softmax(s_i)_j v_j;
+//   lse_i = ln sum_j exp(s_ij).  A row that sees no key gives o = 0, lse = -inf.
+//
+// One pass over the keys with the running maximum m and sum l of each row
+// (kept in float32, in base 2: p = 2^(s c - m) with c = scale log2 e).
+// Both products are formed transposed, S^T = K Q^T and O^T = V^T P^T, so that
+// an accumulator's column is a query row: the row's statistics are a lane's
+// own (plus one exchange between the wave's halves), rescaling O is a lane
+// multiply, and P^T leaves the first product in the operand layout of the
+// second.  V^T's fragments come from row-major tiles through the transposing
+// LDS read.
+//
+// WM waves share key tiles of 32 KT keys along 32-row blocks; WN waves split
+// the tile's keys (each keeps its own m, l, O, joined at the end).
+#include "gdn2_attn.hpp"
+
+namespace gdn2 {
+namespace attn {
+
+struct fwd_args {
+  const void *q, *k, *v;
+  void *o;
+  float *lse;
+  const int32_t *cu;         // packed queries, or nullptr: N sequences of T tokens
+  const int32_t *table;      // paged: [N, max_pages]
+  const int32_t *seq_lens;   // paged: keys of each sequence
+  const uint8_t *ks, *vs;    // paged e4m3: [pages, Hk, page] exponent bytes
+  float *part_o, *part_lse;  // splits > 1: [splits, T total, Hq(, D)]
+  int N, T, Hq, Hk, G;
+  int Ttot;                  // tokens of q in all
+  int max_pages, num_pages, page_shift;
+  int window, splits;
+  float c;                   // scale log2 e
+  order od;
+};
+
+// Infinities and NaN of an operand set to zero; whether there were any.
+__device__ __forceinline__ bool drop_nonfinite(frag8<bf16_t> &x) {
+  u32x4 w = __builtin_bit_cast(u32x4, x.v);
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool lo = (w[i] & 0x7f80u) == 0x7f80u, hi = (w[i] & 0x7f800000u) == 0x7f800000u;
+    any |= lo | hi;
+    w[i] &= (lo ? 0xffff0000u : 0xffffffffu) & (hi ? 0x0000ffffu : 0xffffffffu);
+  }
+  x.v = __builtin_bit_cast(bf16x8, w);
+  return any;
+}
+__device__ __forceinline__ bool drop_nonfinite(frag8<float> &x) {
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool lo = !(fabsf(x.lo[i]) <= 3.4028234663852886e38f), hi = !(fabsf(x.hi[i]) <= 3.4028234663852886e38f);
+    any |= lo | hi;
+    x.lo[i] = lo ? 0.f : x.lo[i];
+    x.hi[i] = hi ? 0.f : x.hi[i];
+  }
+  return any;
+}
+
+// Four channels of a row: its output, or with split keys its float32 part.
+template <typename IO, int D>
+__device__ __forceinline__ void store_row(const fwd_args &a, f32x4 x, float l, size_t qrow, int split, bool ok, int ch) {
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  x *= inv;
+  if (!ok)
+    return;
+  if (a.splits > 1)
+    io<float>::store4(a.part_o + (static_cast<size_t>(split) * a.Ttot * a.Hq + qrow) * D + ch, x);
+  else
+    io<IO>::store4(static_cast<IO *>(a.o) + qrow * D + ch, x);
+}
+// ln of the row's sum (with split keys: of the part's, in base 2)
+__device__ __forceinline__ void store_lse(const fwd_args &a, float m, float l, size_t qrow, int split) {
+  const float x = m + log2f(l);
+  if (a.splits > 1)
+    a.part_lse[static_cast<size_t>(split) * a.Ttot * a.Hq + qrow] = x;
+  else if (a.lse)
+    a.lse[qrow] = x * LN2;
+}
+
+template <typename IO, typename CT, int D, int WM, int WN, int KT, bool PAGED>
+__global__ void __launch_bounds__(64 * WM * WN, (WN == 1 && D * sizeof(IO) <= 256 ? 2 : 1))
+    gdn2_attn_fwd_kernel(fwd_args a) {
+  typedef tile<IO, D> TL;
+  typedef chunk_src<IO, CT> CS;
+  constexpr int NT = 64 * WM * WN, BM = 32 * WM, BN = 32 * KT * WN;
+  constexpr int CPR = TL::CPR, CH = BN * CPR / NT;  // chunks a thread stages of K (and of V)
+  constexpr int TILEB = BN * TL::ROWB;
+  constexpr bool F8 = sizeof(CT) == 1;
+  static_assert(BN * CPR % NT == 0 && NT % CPR == 0, "staging split");
+  constexpr int ROWS_PER_I = NT / CPR;
+  __shared__ __align__(16) char lds[4 * TILEB];  // K and V tiles, double-buffered
+  __shared__ float kscale[F8 ? 2 * BN : 1], vscale[F8 ? 2 * BN : 1];
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int r = lane & 31, h = lane >> 5;
+  const int wm = WN == 1 ? wave : 0, wn = WN == 1 ? 0 : wave;
+
+  // ---- which rows
+  const int id = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
+  int unit, slot;
+  if (!place(a.od, id, unit, slot))
+    return;
+  span sq;
+  int hk, row0;
+  if (a.cu) {
+    hk = unit;
+    const int n = find_seq(a.cu, a.N, a.G, BM, slot, lane);
+    sq = packed_span(a.cu, n, a.T);
+    row0 = static_cast<int>((slot - (static_cast<long>(a.cu[n]) * a.G / BM + n)) * BM);
+  } else {
+    sq.n = unit / a.Hk;
+    hk = unit % a.Hk;
+    sq.start = sq.n * a.T;
+    sq.len = a.T;
+    row0 = slot * BM;
+  }
+  const int rows = sq.len * a.G;
+  if (row0 < 0 || row0 >= rows)
+    return;
+  int kv_len = sq.len;
+  if constexpr (PAGED) {
+    kv_len = a.seq_lens[sq.n];
+    const int cap = a.max_pages << a.page_shift;
+    kv_len = kv_len < 0 ? 0 : (kv_len > cap ? cap : kv_len);
+  }
+  const int shift = kv_len - sq.len;  // position of the sequence's first query
+
+  // ---- visible keys of the workgroup, and this split's part
+  const int t_lo = row0 / a.G;
+  const int last_row = row0 + BM - 1 < rows - 1 ? row0 + BM - 1 : rows - 1;
+  const int t_hi = last_row / a.G;
+  int k_hi = shift + t_hi + 1;
+  k_hi = k_hi < 0 ? 0 : k_hi;
+  int k_lo = 0;
+  if (a.window > 0) {
+    k_lo = shift + t_lo - a.window + 1;
+    k_lo = k_lo < 0 ? 0 : k_lo;
+  }
+  int k0 = k_lo, k1 = k_hi;
+  if (a.splits > 1) {
+    const int nt = k_hi > k_lo ? (k_hi - k_lo + BN - 1) / BN : 0;
+    const int per = (nt + a.splits - 1) / a.splits;
+    k0 = k_lo + split * per * BN;
+    k1 = k0 + per * BN < k_hi ? k0 + per * BN : k_hi;
+  }
+  const int ntiles = k1 > k0 ? (k1 - k0 + BN - 1) / BN : 0;
+
+  // ---- this lane's row
+  const int my_row = row0 + 32 * wm + r;
+  const bool row_ok = my_row < rows;
+  const int cl_row = row_ok ? my_row : rows - 1;
+  const int tok = cl_row / a.G, head = hk * a.G + cl_row % a.G;
+  const int pos = shift + tok;
+  const size_t qrow = static_cast<size_t>(sq.start + tok) * a.Hq + head;
+  // positions of the wave's first and last row
+  const int wr0 = row0 + 32 * wm < rows ? row0 + 32 * wm : rows - 1;
+  const int wr1 = row0 + 32 * wm + 31 < rows ? row0 + 32 * wm + 31 : rows - 1;
+  const int pos_lo = shift + wr0 / a.G, pos_hi = shift + wr1 / a.G;
+
+  frag8<IO> q[D / 16];
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk)
+    q[kk] = load8<IO>(static_cast<const IO *>(a.q) + qrow * D + 16 * kk + 8 * h);
+
+  // ---- staging: thread's chunk c of rows sr0 + ROWS_PER_I i
+  const int sc = tid % CPR, sr0 = tid / CPR;
+  typename CS::raw rk[CH], rv[CH];
+  int ent[CH];
+  uint8_t bk = 127, bv = 127;
+  int ent_b = 0;
+  const int32_t *table = PAGED ? a.table + static_cast<size_t>(sq.n) * a.max_pages : nullptr;
+  const int pmask = (1 << a.page_shift) - 1;
+  // page-table entries of the tile at key kb (-1: row not staged)
+  auto load_entries = [&](int kb) {
+    if constexpr (PAGED) {
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int j = kb + sr0 + ROWS_PER_I * i;
+        int e = j < k1 ? table[j >> a.page_shift] : -1;
+        ent[i] = e < a.num_pages ? e : -1;
+      }
+      if constexpr (F8) {
+        const int j = kb + tid;
+        int e = tid < BN && j < k1 ? table[j >> a.page_shift] : -1;
+        ent_b = e < a.num_pages ? e : -1;
+      }
+    }
+  };
+  auto load_tile = [&](int kb) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int j = kb + sr0 + ROWS_PER_I * i;
+      size_t off;
+      bool ok;
+      if constexpr (PAGED) {
+        ok = ent[i] >= 0;
+        off = (((static_cast<size_t>(ok ? ent[i] : 0) * a.Hk + hk) << a.page_shift) + (j & pmask)) * D;
+      } else {
+        ok = j < k1;
+        off = (static_cast<size_t>(sq.start + (ok ? j : 0)) * a.Hk + hk) * D;
+      }
+      off += sc * TL::VPC;
+      rk[i] = ok ? CS::load(static_cast<const CT *>(a.k) + off) : CS::zero();
+      rv[i] = ok ? CS::load(static_cast<const CT *>(a.v) + off) : CS::zero();
+    }
+    if constexpr (F8) {
+      bk = bv = 127;
+      if (ent_b >= 0 && tid < BN) {
+        const size_t off = ((static_cast<size_t>(ent_b) * a.Hk + hk) << a.page_shift) + ((kb + tid) & pmask);
+        bk = a.ks[off];
+        bv = a.vs[off];
+      }
+    }
+  };
+  auto store_tile = [&](int buf) {
+    char *kt = lds + buf * 2 * TILEB, *vt = kt + TILEB;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int at = TL::at(sr0 + ROWS_PER_I * i, sc);
+      *reinterpret_cast<u32x4 *>(kt + at) = CS::widen(rk[i]);
+      *reinterpret_cast<u32x4 *>(vt + at) = CS::widen(rv[i]);
+    }
+    if constexpr (F8) {
+      if (tid < BN) {
+        kscale[buf * BN + tid] = scale_of(bk);
+        vscale[buf * BN + tid] = scale_of(bv);
+      }
+    }
+  };
+
+  f32x16 o[D / 32];
+#pragma unroll
+  for (int n = 0; n < D / 32; ++n)
+    o[n] = zero16();
+  float m = neg_inf(), l = 0.f;  // l: this half's part of the sum
+
+  if (ntiles > 0) {
+    load_entries(k0);
+    load_tile(k0);
+    load_entries(k0 + BN);
+  }
+  for (int it = 0; it < ntiles; ++it) {
+    const int kb = k0 + it * BN, buf = it & 1;
+    store_tile(buf);
+    __syncthreads();
+    if (it + 1 < ntiles) {
+      load_tile(kb + BN);
+      load_entries(kb + 2 * BN);
+    }
+    const char *kt = lds + buf * 2 * TILEB, *vt = kt + TILEB;
+    const int wk = kb + 32 * KT * wn;  // the wave's first key
+    // nothing of the tile is visible to the wave
+    if (wk > pos_hi || wk >= k1 || (a.window > 0 && wk + 32 * KT - 1 <= pos_lo - a.window))
+      continue;
+    const bool masked = wk + 32 * KT - 1 > pos_lo || wk + 32 * KT > k1 ||
+                        (a.window > 0 && wk <= pos_hi - a.window);
+
+    f32x16 s[KT];
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+      s[t] = zero16();
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+        mma(s[t], TL::row(kt, 32 * (KT * wn + t) + r, kk, h), q[kk]);
+    }
+    if constexpr (F8) {
+#pragma unroll
+      for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const f32x4 sc4 = *reinterpret_cast<const f32x4 *>(&kscale[buf * BN + 32 * (KT * wn + t) + 8 * g + 4 * h]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            s[t][4 * g + i] *= sc4[i];
+        }
+    }
+    // key of register i: wk + 32 t + 8 (i / 4) + 4 h + i % 4; visible when
+    // j <= pos, j > pos - W and j < k1
+    const int hi_rel = (pos < k1 - 1 ? pos : k1 - 1) - wk - 4 * h;
+    const int lo_rel = (a.window > 0 ? pos - a.window : -0x40000000) - wk - 4 * h;
+    if (masked) {
+#pragma unroll
+      for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int j = 32 * t + 8 * (i >> 2) + (i & 3);
+          s[t][i] = (j <= hi_rel && j > lo_rel) ? s[t][i] : neg_inf();
+        }
+    }
+    float mx = s[0][0];
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        mx = fmaxf(mx, s[t][i]);
+    mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+    const float m_new = fmaxf(m, mx * a.c);
+    const float base = m_new == neg_inf() ? 0.f : m_new;  // a row without keys yet
+    const float alpha = fast_exp2(m - base);
+    m = m_new;
+    float sum = 0.f;
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float p = fast_exp2(s[t][i] * a.c - base);
+        s[t][i] = p;
+        sum += p;
+      }
+    l = l * alpha + sum;
+#pragma unroll
+    for (int n = 0; n < D / 32; ++n)
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        o[n][i] *= alpha;
+    if constexpr (F8) {
+      // the values' scales go to the weights (a masked weight stays 0
+      // whatever its row's scale holds)
+#pragma unroll
+      for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const f32x4 sc4 = *reinterpret_cast<const f32x4 *>(&vscale[buf * BN + 32 * (KT * wn + t) + 8 * g + 4 * h]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int j = 32 * t + 8 * g + i;
+            s[t][4 * g + i] = (!masked || (j <= hi_rel && j > lo_rel)) ? s[t][4 * g + i] * sc4[i] : 0.f;
+          }
+        }
+    }
+    bool odd = false;  // infinities or NaN among the values of a masked tile
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+      for (int jj = 0; jj < 2; ++jj) {
+        const frag8<IO> p = pack8<IO>(s[t], jj);
+        const int kr = 32 * (KT * wn + t) + 16 * jj;
+#pragma unroll
+        for (int n = 0; n < D / 32; ++n) {
+          frag8<IO> v = TL::col(vt, kr, n, lane);
+          if (masked)
+            odd |= drop_nonfinite(v);
+          mma(o[n], v, p);
+        }
+      }
+    // 0 times an infinity would reach rows that do not see its key: in a
+    // masked tile such values are left out of the product above and added
+    // here for the rows that do see them.
+    if (masked && __any(odd)) {
+      for (int j = 0; j < 32 * KT; ++j) {
+        float p = 0.f;  // weight of key j, kept by half (j / 4) % 2
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            p = (32 * t + 8 * (i >> 2) + (i & 3)) == j - 4 * ((j >> 2) & 1) ? s[t][i] : p;
+        p = __shfl(p, r + 32 * ((j >> 2) & 1), 64);
+        const int jr = j - 4 * h;
+        const bool vis = jr <= hi_rel && jr > lo_rel;
+#pragma unroll
+        for (int n = 0; n < D / 32; ++n)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float x = TL::one(vt, 32 * KT * wn + j, 32 * n + 8 * (i >> 2) + 4 * h + (i & 3));
+            if (vis && !(fabsf(x) <= 3.4028234663852886e38f))
+              o[n][i] += p * x;
+          }
+      }
+    }
+  }
+
+  l += __shfl_xor(l, 32, 64);
+
+  if constexpr (WN > 1) {
+    // join the waves' parts: weights 2^(m_w - M)
+    static_assert(WM == 1, "one row block");
+    constexpr int OLD = D + 4;
+    static_assert(WN * 32 * OLD * 4 + WN * 32 * 8 <= 4 * TILEB, "join space");
+    float *jo = reinterpret_cast<float *>(lds);                 // [WN][32][OLD]
+    float *jm = jo + WN * 32 * OLD, *jl = jm + WN * 32;
+    __syncthreads();
+    if (h == 0) {
+      jm[wn * 32 + r] = m;
+      jl[wn * 32 + r] = l;
+    }
+    __syncthreads();
+    float M = neg_inf();
+#pragma unroll
+    for (int w = 0; w < WN; ++w)
+      M = fmaxf(M, jm[w * 32 + r]);
+    const float base = M == neg_inf() ? 0.f : M;
+    float L = 0.f;
+#pragma unroll
+    for (int w = 0; w < WN; ++w)
+      L += jl[w * 32 + r] * fast_exp2(jm[w * 32 + r] - base);
+    const float f = fast_exp2(m - base);
+#pragma unroll
+    for (int n = 0; n < D / 32; ++n)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        f32x4 x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          x[i] = o[n][4 * g + i] * f;
+        *reinterpret_cast<f32x4 *>(&jo[(wn * 32 + r) * OLD + 32 * n + 8 * g + 4 * h]) = x;
+      }
+    __syncthreads();
+    // wave w sums the waves' parts of channel block w of every row
+    m = M;
+    l = L;
+    for (int n = wn; n < D / 32; n += WN)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        f32x4 x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < WN; ++w)
+          x += *reinterpret_cast<const f32x4 *>(&jo[(w * 32 + r) * OLD + 32 * n + 8 * g + 4 * h]);
+        store_row<IO, D>(a, x, l, qrow, split, row_ok, 32 * n + 8 * g + 4 * h);
+      }
+    if (wn == 0 && h == 0 && row_ok)
+      store_lse(a, m, l, qrow, split);
+  } else {
+#pragma unroll
+    for (int n = 0; n < D / 32; ++n)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        f32x4 x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          x[i] = o[n][4 * g + i];
+        store_row<IO, D>(a, x, l, qrow, split, row_ok, 32 * n + 8 * g + 4 * h);
+      }
+    if (h == 0 && row_ok)
+      store_lse(a, m, l, qrow, split);
+  }
+}
+
+// Joins the parts of split keys: one wave per (token, query head), weights
+// 2^(lse_s - max lse); the order of the sum is fixed.
+template <typename IO, int D>
+__global__ void __launch_bounds__(256) gdn2_attn_join_kernel(fwd_args a) {
+  const int lane = threadIdx.x & 63;
+  const size_t rows = static_cast<size_t>(a.Ttot) * a.Hq;
+  const size_t row = static_cast<size_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (row >= rows)
+    return;
+  if (a.cu && row >= static_cast<size_t>(a.cu[a.N] < 0 ? 0 : a.cu[a.N]) * a.Hq)
+    return;  // behind the last sequence
+  float M = neg_inf();
+  for (int s = lane; s < a.splits; s += 64)
+    M = fmaxf(M, a.part_lse[s * rows + row]);
+#pragma unroll
+  for (int x = 1; x < 64; x <<= 1)
+    M = fmaxf(M, __shfl_xor(M, x, 64));
+  const float base = M == neg_inf() ? 0.f : M;
+  constexpr int V = D / 64;
+  float acc[V], L = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    acc[i] = 0.f;
+  for (int s = 0; s < a.splits; ++s) {
+    const float ls = a.part_lse[s * rows + row];
+    const float w = fast_exp2(ls - base);  // NaN stays NaN
+    L += w;
+    if (ls == neg_inf())
+      continue;
+    const float *p = a.part_o + (s * rows + row) * D + V * lane;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      acc[i] += w * p[i];
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  IO *o = static_cast<IO *>(a.o) + row * D + V * lane;
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    o[i] = io<IO>::from_f(acc[i] * inv);
+  if (a.lse && lane == 0)
+    a.lse[row] = (base + log2f(L)) * LN2;
+}
+
+// ------------------------------------------------------------- launchers --
+// The kernel's shape for a call: 32-row blocks with the keys split over 4
+// waves where a sequence brings few rows (decode), else 128 rows and shared
+// key tiles.
+static bool few_rows(const attn_sizes &z) {
+  return static_cast<long long>(z.Ttot) * (z.Hq / z.Hk) <= 32LL * z.N;
+}
+// Parts along the keys of a paged call: enough workgroups for two rounds of
+// the 256 CUs, no part under 256 keys of the longest possible sequence.
+int attn_paged_splits(const attn_sizes &z) {
+  order od;
+  plan_tiles(z, z.Hq / z.Hk, few_rows(z) ? 32 : 128, od);
+  const long long blocks = static_cast<long long>(od.units) * od.tiles;
+  long long keys = z.max_keys;
+  if (z.window > 0 && keys > z.window + 128LL)
+    keys = z.window + 128LL;
+  long long s = (512 + blocks - 1) / blocks;
+  if (s > keys / 256)
+    s = keys / 256;
+  return s < 1 ? 1 : (s > 64 ? 64 : static_cast<int>(s));
+}
+
+template <typename IO, typename CT, int D, int WM, int WN, int KT, bool PAGED>
+static hipError_t go(fwd_args &a, const attn_sizes &z, hipStream_t st) {
+  const unsigned blocks = plan_tiles(z, a.G, 32 * WM, a.od) * a.splits;
+  hipLaunchKernelGGL((gdn2_attn_fwd_kernel<IO, CT, D, WM, WN, KT, PAGED>), dim3(blocks), dim3(64 * WM * WN), 0, st, a);
+  return hipGetLastError();
+}
+
+static void fill(fwd_args &a, const attn_sizes &z, const attn_ptrs &p) {
+  a.q = p.q;
+  a.k = p.k;
+  a.v = p.v;
+  a.o = p.o;
+  a.lse = p.lse;
+  a.cu = p.cu;
+  a.table = p.table;
+  a.seq_lens = p.seq_lens;
+  a.ks = p.ks;
+  a.vs = p.vs;
+  a.part_o = a.part_lse = nullptr;
+  a.N = z.N;
+  a.T = z.T;
+  a.Ttot = z.Ttot;
+  a.Hq = z.Hq;
+  a.Hk = z.Hk;
+  a.G = z.Hq / z.Hk;
+  a.max_pages = z.max_pages;
+  a.num_pages = z.num_pages;
+  a.page_shift = z.page_shift;
+  a.window = z.window;
+  a.splits = 1;
+  a.c = z.scale * LOG2E;
+}
+
+template <typename IO, int D> hipError_t launch_attn_fwd(const attn_sizes &z, const attn_ptrs &p, hipStream_t st) {
+  fwd_args a;
+  fill(a, z, p);
+  constexpr int KT = sizeof(IO) == 2 ? 2 : 1;
+  return go<IO, IO, D, 4, 1, KT, false>(a, z, st);
+}
+
+template <typename IO, typename CT, int D>
+hipError_t launch_attn_paged(const attn_sizes &z, const attn_ptrs &p, int splits, void *ws, hipStream_t st) {
+  fwd_args a;
+  fill(a, z, p);
+  a.splits = splits;
+  constexpr int KT = sizeof(IO) == 2 ? 2 : 1;
+  if (splits > 1) {
+    const size_t rows = static_cast<size_t>(z.Ttot) * z.Hq;
+    a.part_o = static_cast<float *>(ws);
+    a.part_lse = a.part_o + rows * D * splits;
+  }
+  constexpr int WN = sizeof(IO) == 2 ? 4 : 2;
+  return few_rows(z) ? go<IO, CT, D, 1, WN, 1, true>(a, z, st) : go<IO, CT, D, 4, 1, KT, true>(a, z, st);
+}
+
+template <typename IO, int D>
+hipError_t launch_attn_join(const attn_sizes &z, const attn_ptrs &p, int splits, void *ws, hipStream_t st) {
+  fwd_args a;
+  fill(a, z, p);
+  a.splits = splits;
+  const size_t rows = static_cast<size_t>(z.Ttot) * z.Hq;
+  a.part_o = static_cast<float *>(ws);
+  a.part_lse = a.part_o + rows * D * splits;
+  hipLaunchKernelGGL((gdn2_attn_join_kernel<IO, D>), dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(256), 0, st, a);
+  return hipGetLastError();
+}
+
+#define GDN2_INST_ATTN(IO, D)                                                                              \
+  template hipError_t launch_attn_fwd<IO, D>(const attn_sizes &, const attn_ptrs &, hipStream_t);          \
+  template hipError_t launch_attn_paged<IO, IO, D>(const attn_sizes &, const attn_ptrs &, int, void *,     \
+                                                   hipStream_t);                                           \
+  template hipError_t launch_attn_paged<IO, f8_t, D>(const attn_sizes &, const attn_ptrs &, int, void *,   \
+                                                     hipStream_t);                                         \
+  template hipError_t launch_attn_join<IO, D>(const attn_sizes &, const attn_ptrs &, int, void *, hipStream_t);
+GDN2_INST_ATTN(float, 64)
+GDN2_INST_ATTN(float, 128)
+GDN2_INST_ATTN(bf16_t, 64)
+GDN2_INST_ATTN(bf16_t, 128)
+
+}  // namespace attn
+}  // namespace gdn2

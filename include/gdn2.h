@@ -77,7 +77,10 @@ extern "C" {
 
 #define GDN2_ABI_VERSION 1
 
-/* The *_MAX_ENUM values are never returned or accepted: they give both
+/* GDN2_F8E4M3 (8-bit floating point, 4 exponent and 3 fraction bits, largest
+ * value 448, no infinity) is a cache element type only: every other dtype
+ * argument refuses it.
+ * The *_MAX_ENUM values are never returned or accepted: they give both
  * enums the range of a non-negative int, so that any such value a caller
  * passes (an unknown status or dtype) is a valid value of the type and is
  * refused by the library, not undefined. */
@@ -90,7 +93,7 @@ typedef enum {
     GDN2_STATUS_MAX_ENUM = 0x7FFFFFFF
 } gdn2_status_t;
 
-typedef enum { GDN2_F32 = 0, GDN2_BF16 = 1, GDN2_DTYPE_MAX_ENUM = 0x7FFFFFFF } gdn2_dtype_t;
+typedef enum { GDN2_F32 = 0, GDN2_BF16 = 1, GDN2_F8E4M3 = 2, GDN2_DTYPE_MAX_ENUM = 0x7FFFFFFF } gdn2_dtype_t;
 
 /* flags of gdn2_chunk_fwd */
 #define GDN2_FLAG_RECURRENT (1u << 1) /* token-by-token kernel instead of the
@@ -385,6 +388,150 @@ gdn2_status_t gdn2_segment_combine(const float *Phi, const float *Psi, const flo
 gdn2_status_t gdn2_decode_step(const void *q, const void *k, const void *v, const void *alpha,
                                const void *b, const void *w, float *S, void *o, int N, int H,
                                int dk, int dv, gdn2_dtype_t dt, void *stream);
+
+/* ------------------------------------------ attention layers of a hybrid stack
+ *
+ * A hybrid interleaves GDN-2 layers with causal sliding-window attention
+ * (aixai.ru blog and aiexpert.news/pt: 2K windows).  These entry points are
+ * the attention layer's operators, next to the recurrence's:
+ *   gdn2_qk_norm_rope_fwd / _bwd   per-head norm of q and k, and the rotation
+ *                                  by position, in one pass
+ *   gdn2_attn_fwd / _bwd           attention over whole sequences (training,
+ *                                  prompts), next to gdn2_chunk_fwd / _bwd
+ *   gdn2_kv_cache_write / _read    the paged cache, its values as they are or
+ *                                  quantised to 8 bits
+ *   gdn2_attn_paged                new tokens over the paged cache (decode,
+ *                                  chunks of a prompt), next to
+ *                                  gdn2_decode_step
+ * The conventions at the top hold: contiguous token-major device tensors of
+ * dtype dt (16-byte aligned), packed sequences by cu_seqlens with B = 1, all
+ * work enqueued on `stream`, nothing allocated.  q and o are [B, T, Hq, d],
+ * k and v [B, T, Hk, d]; Hq is a multiple of Hk, and query head h uses kv
+ * head h / (Hq / Hk).  d is 64 or 128.  Sums, softmax statistics and
+ * accumulators are float32; with bfloat16 tensors the softmax weights (and
+ * the backward's score gradients) are rounded to bfloat16 as operands of
+ * their matrix products.  Every sum has a fixed order: the same call gives
+ * the same bits.  Outputs may not alias inputs, except where said.
+ * Limits: at most 2^26 - 1 (token, query head) rows a call, and 2^20 - 1
+ * (sequence, kv head) pairs.  Rows of the tensors behind cu_seqlens[N] are
+ * neither read nor written. */
+
+/* flags of gdn2_qk_norm_rope_fwd / _bwd */
+#define GDN2_ROPE_INTERLEAVED (1u << 0) /* pairs are channels (2j, 2j + 1); without
+                                           it (j, j + rotary_dim / 2) */
+#define GDN2_ROPE_NO_NORM (1u << 1)     /* the rotation alone */
+
+/* Per-head norm and rotation of queries and keys:
+ *   y = x / sqrt(mean(x^2) + eps) (.) w, then channel pair j (of the first
+ *   rotary_dim channels) turned by the angle position * freqs[j]; the other
+ *   channels pass.
+ *   q, k      : [B, T, Hq, d] and [B, T, Hk, d] (here Hq need not be a
+ *               multiple of Hk).
+ *   wq, wk    : [d] float32 weights, either or both NULL for ones (NULL with
+ *               GDN2_ROPE_NO_NORM).
+ *   freqs     : [rotary_dim / 2] float64, radians per position; NULL exactly
+ *               when rotary_dim is 0 (no rotation).  Angles are formed and
+ *               reduced in 64 bits, so far positions keep their precision.
+ *   positions : [B, T] int32, any values, or NULL for 0 .. T-1 in every row.
+ *   rotary_dim: a multiple of 8, 0 .. d.
+ *   eps       : >= 0 (a row of zeros with eps = 0 gives NaN).
+ *   q_out, k_out : outputs; may be q and k themselves. */
+gdn2_status_t gdn2_qk_norm_rope_fwd(const void *q, const void *k, const float *wq, const float *wk,
+                                    const double *freqs, const int32_t *positions, int B, int T, int Hq, int Hk, int d,
+                                    int rotary_dim, float eps, gdn2_dtype_t dt, uint32_t flags, void *q_out,
+                                    void *k_out, void *stream);
+
+/* Bytes of workspace the weight gradients need (0 for unsupported sizes). */
+size_t gdn2_qk_norm_rope_bwd_workspace_bytes(int B, int T, int Hq, int Hk, int d);
+
+/* Its backward.  dq_out, dk_out: dL/dq_out and dL/dk_out.  Outputs dq, dk
+ * (like q, k; each may be the gradient buffer it comes from) and dwq, dwk
+ * ([d] float32, either or both NULL; summed over all tokens and heads).  q
+ * and k are the forward's inputs (not read, and may be NULL, with
+ * GDN2_ROPE_NO_NORM).  The workspace may be NULL when no weight gradient is
+ * asked for.  T == 0 writes zeros to dwq and dwk. */
+gdn2_status_t gdn2_qk_norm_rope_bwd(const void *q, const void *k, const float *wq, const float *wk,
+                                    const double *freqs, const int32_t *positions, const void *dq_out,
+                                    const void *dk_out, int B, int T, int Hq, int Hk, int d, int rotary_dim, float eps,
+                                    gdn2_dtype_t dt, uint32_t flags, void *dq, void *dk, float *dwq, float *dwk,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+
+/* Causal attention over whole sequences.
+ *   o_i = sum_j softmax_j(scale q_i . k_j) v_j over the keys j <= i of the same
+ *   sequence, with window > 0 only those with j > i - window.
+ *   cu_seqlens, B, T, num_seqs : as for gdn2_chunk_fwd.
+ *   window    : 0 for none.
+ *   scale     : positive and finite.
+ *   lse       : [B, T, Hq] float32, ln sum_j exp(scale q_i . k_j), or NULL.
+ * An infinity or NaN in a token's key or value reaches the rows that see it
+ * and no others. */
+gdn2_status_t gdn2_attn_fwd(const void *q, const void *k, const void *v, const int32_t *cu_seqlens, int B, int T,
+                            int Hq, int Hk, int d, int num_seqs, int window, float scale, gdn2_dtype_t dt, void *o,
+                            float *lse, void *stream);
+
+/* Bytes of workspace gdn2_attn_bwd needs (B = 1 and the total T when packed;
+ * 0 for unsupported sizes). */
+size_t gdn2_attn_bwd_workspace_bytes(int B, int T, int Hq, int Hk, int d);
+
+/* Its backward: dq, dk, dv (like q, k, v) from dout = dL/do and the forward's
+ * o and lse on the same inputs; a kv head's gradients are the sums over the
+ * query heads that share it.  An infinity or NaN in q, k, v or dout may reach
+ * any gradient of its sequence and kv head. */
+gdn2_status_t gdn2_attn_bwd(const void *q, const void *k, const void *v, const void *o, const float *lse,
+                            const void *dout, const int32_t *cu_seqlens, int B, int T, int Hq, int Hk, int d,
+                            int num_seqs, int window, float scale, gdn2_dtype_t dt, void *dq, void *dk, void *dv,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/* The paged cache.  k_cache and v_cache are [num_pages, Hk, page_size, d],
+ * page_size 16, 32, 64, 128 or 256, num_pages * page_size < 2^31; slot
+ * p * page_size + r is row r of page p.  cache_dt is dt (values as they are;
+ * scales NULL) or GDN2_F8E4M3: then k_scale and v_scale, [num_pages, Hk,
+ * page_size] bytes, hold for every row (token, kv head) the byte e + 127 of
+ * its scale 2^e, e the smallest integer >= -126 with max |x| <= 448 * 2^e
+ * (127 for a row of zeros), and the codes are x * 2^-e rounded to nearest
+ * even: code * 2^e is exact in float32 and bfloat16.  A row holding an
+ * infinity or NaN gets the byte 255 and stands for NaN throughout.
+ *
+ * gdn2_kv_cache_write stores n tokens' keys and values, [n, Hk, d], into
+ * slots[0 .. n-1] (int64); a slot outside the cache is skipped (a padded
+ * batch marks its padding with -1).  Two tokens of one call may not share a
+ * slot (which one a row would keep is not defined). */
+gdn2_status_t gdn2_kv_cache_write(const void *k, const void *v, const int64_t *slots, int n, int Hk, int d,
+                                  int num_pages, int page_size, gdn2_dtype_t dt, gdn2_dtype_t cache_dt, void *k_cache,
+                                  void *v_cache, uint8_t *k_scale, uint8_t *v_scale, void *stream);
+
+/* Reads n slots back into k and v, [n, Hk, d] of dtype dt (zeros for a slot
+ * outside the cache; a slot may be read more than once). */
+gdn2_status_t gdn2_kv_cache_read(const int64_t *slots, int n, int Hk, int d, int num_pages, int page_size,
+                                 gdn2_dtype_t dt, gdn2_dtype_t cache_dt, const void *k_cache, const void *v_cache,
+                                 const uint8_t *k_scale, const uint8_t *v_scale, void *k, void *v, void *stream);
+
+/* Bytes of workspace gdn2_attn_paged needs: B sequences of T new tokens
+ * (num_seqs 0), or num_seqs packed sequences of T new tokens in all (B = 1).
+ * 0 when none is needed, and for unsupported sizes. */
+size_t gdn2_attn_paged_workspace_bytes(int B, int T, int Hq, int Hk, int d, int num_seqs, int page_size, int max_pages,
+                                       int window);
+
+/* Attention of new tokens over the paged cache, which already holds their own
+ * keys and values.  Sequence n has seq_lens[n] keys (int32 [N], the new ones
+ * included; clamped to 0 .. max_pages * page_size), key j in row
+ * j % page_size of page block_table[n][j / page_size] (int32 [N, max_pages]);
+ * its L new queries stand at the positions seq_lens[n] - L .. seq_lens[n] - 1
+ * and see keys as in gdn2_attn_fwd.  q and o are [B, T, Hq, d] (T new tokens
+ * for each of B sequences; decode is T = 1) or packed by cu_seqlens
+ * [1, T, Hq, d].  A query at a negative position sees nothing: o = 0,
+ * lse = -inf.  A table entry outside the cache stands for a page of zeros;
+ * entries that no query sees (behind seq_lens, before the window) are not
+ * read.  lse [B, T, Hq] float32 or NULL.  max_pages * page_size <= 2^28.
+ * Where the call has too few rows to fill the GPU, its keys are split into
+ * parts (their number depends on the sizes alone) that a second kernel joins
+ * from the workspace. */
+gdn2_status_t gdn2_attn_paged(const void *q, const void *k_cache, const void *v_cache, const uint8_t *k_scale,
+                              const uint8_t *v_scale, const int32_t *block_table, const int32_t *seq_lens,
+                              const int32_t *cu_seqlens, int B, int T, int Hq, int Hk, int d, int num_seqs,
+                              int num_pages, int page_size, int max_pages, int window, float scale, gdn2_dtype_t dt,
+                              gdn2_dtype_t cache_dt, void *o, float *lse, void *workspace, size_t workspace_bytes,
+                              void *stream);
 
 /* Static text of a status code. */
 const char *gdn2_status_string(gdn2_status_t status);
