@@ -35,8 +35,12 @@ COMMON = ["-O3", "-fPIC", "-std=c++17", f"--offload-arch={ARCH}",
 # Per-file flags.  The segment map's state loop carries its matrix-core
 # accumulators from chunk to chunk and scales them on the vector ALU; by
 # default the compiler keeps them in AGPRs and copies them to VGPRs and back
-# every chunk, which the VGPR form of the products avoids.
-EXTRA = {"gdn2_segment.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+# every chunk, which the VGPR form of the products avoids; so the
+# attention kernels carry up to 128 accumulator registers beside 64 of operands and
+# exchange them with the vector ALU every tile.
+EXTRA = {"gdn2_segment.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+         "gdn2_attn_fwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+         "gdn2_attn_bwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 # Host-only undefined-behaviour traps for the checked build of the C-ABI files
 # (each flag after -Xarch_host: device code is compiled as in the product).
 HOSTCHECK = [f for x in ("-fsanitize=undefined", "-fsanitize-trap=undefined", "-fsanitize=bounds",

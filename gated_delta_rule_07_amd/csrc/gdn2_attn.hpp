@@ -117,46 +117,62 @@ template <typename T, int D> struct tile {
   }
   __device__ static __forceinline__ int at(int r, int c) { return r * ROWB + ((c ^ f(r)) << 4); }
 
-  // row fragment: values 16 kk + 8h .. + 7 of row r
-  __device__ static __forceinline__ frag8<T> row(const char *t, int r, int kk, int h) {
-    if constexpr (sizeof(T) == 2) {
-      frag8<T> x;
-      x.v = *reinterpret_cast<const bf16x8 *>(t + at(r, 2 * kk + h));
-      return x;
-    } else {
-      frag8<T> x;
-      x.lo = *reinterpret_cast<const f32x4 *>(t + at(r, 4 * kk + 2 * h));
-      x.hi = *reinterpret_cast<const f32x4 *>(t + at(r, 4 * kk + 2 * h + 1));
-      return x;
-    }
+  // at(sr + RPI i, c), b = at(sr, c)
+  template <int RPI> __device__ static __forceinline__ int step(int b, int sr, int c, int i) {
+    return RPI % 16 == 0 ? b + RPI * i * ROWB : at(sr + RPI * i, c);
   }
-  // column fragment of the transposed tile: channel 32 n + lane % 32, tile
-  // rows r0 + 8 (e / 4) + 4h + e % 4 (acc order)
-  __device__ static __forceinline__ frag8<T> col(const char *t, int r0, int n, int lane) {
+
+  // A fragment's place in a tile is a lane's own base, XORed with the part
+  // of the chunk number that k or n gives (rows are whole multiples of the
+  // permutation's span, so adding rows and XORing chunks commute): one base a
+  // lane instead of an address per fragment.
+  //
+  // Row fragments: values 16 kk + 8h .. + 7 of row r.
+  __device__ static __forceinline__ int row_base(int r, int h) {
+    return r * ROWB + ((f(r) ^ (sizeof(T) == 2 ? h : 2 * h)) << 4);
+  }
+  __device__ static __forceinline__ frag8<T> row(const char *t, int base, int kk) {
+    frag8<T> x;
+    if constexpr (sizeof(T) == 2) {
+      x.v = *reinterpret_cast<const bf16x8 *>(t + (base ^ (kk << 5)));
+    } else {
+      x.lo = *reinterpret_cast<const f32x4 *>(t + (base ^ (kk << 6)));
+      x.hi = *reinterpret_cast<const f32x4 *>(t + (base ^ (kk << 6) ^ 16));
+    }
+    return x;
+  }
+  // Column fragments, of the transposed tile: channel 32 n + lane % 32, tile
+  // rows r0 + 8 (e / 4) + 4h + e % 4 (acc order), r0 a multiple of 16.
+  __device__ static __forceinline__ int col_base(int lane) {
     const int h = lane >> 5;
     if constexpr (sizeof(T) == 2) {
       // a transposing read hands lane i of 16 the values of column i of a
       // 4 x 16 block whose row j / 4, values 4 (j % 4) .. + 3 lane j points at
-      typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-      const int j = lane & 15, ch = (lane >> 4) & 1;
-      const int c = 4 * n + 2 * ch + ((j & 3) >> 1), sub = (j & 1) << 3;
-      const int ra = r0 + 4 * h + (j >> 2);
-      const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(t + at(ra, c) + sub));
-      const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(t + at(ra + 8, c) + sub));
-      frag8<T> x;
-      x.v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
-      return x;
+      const int j = lane & 15, ch = (lane >> 4) & 1, ra = 4 * h + (j >> 2);
+      return ra * ROWB + (((2 * ch + ((j & 3) >> 1)) ^ f(ra)) << 4) + ((j & 1) << 3);
     } else {
-      const int ch = 32 * n + (lane & 31);
-      frag8<T> x;
+      return 4 * h * ROWB + ((((lane & 31) >> 2) ^ f(4 * h)) << 4) + ((lane & 3) << 2);
+    }
+  }
+  __device__ static __forceinline__ frag8<T> col(const char *t, int base, int r0, int n) {
+    frag8<T> x;
+    if constexpr (sizeof(T) == 2) {
+      // f(r + 8) = f(r) ^ 2
+      typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+      const char *p = t + r0 * ROWB;
+      const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + (base ^ (n << 6))));
+      const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 8 * ROWB + (base ^ (n << 6) ^ 32)));
+      x.v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      // f(4h + e) = f(4h) ^ 2e, f(r + 8) = f(r) ^ 1
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int ra = r0 + 4 * h + e;
-        x.lo[e] = *reinterpret_cast<const float *>(t + at(ra, ch >> 2) + ((ch & 3) << 2));
-        x.hi[e] = *reinterpret_cast<const float *>(t + at(ra + 8, ch >> 2) + ((ch & 3) << 2));
+        const char *p = t + (r0 + e) * ROWB;
+        x.lo[e] = *reinterpret_cast<const float *>(p + (base ^ (n << 7) ^ (e << 5)));
+        x.hi[e] = *reinterpret_cast<const float *>(p + 8 * ROWB + (base ^ (n << 7) ^ (e << 5) ^ 16));
       }
-      return x;
     }
+    return x;
   }
   // one value
   __device__ static __forceinline__ float one(const char *t, int r, int ch) {
@@ -164,33 +180,61 @@ template <typename T, int D> struct tile {
   }
 };
 
-// One 16-byte chunk (VPC values of IO) of a tensor row of element type CT:
-// e4m3 codes become the values they stand for (the row's scale is applied
-// to the scores and weights, in float32), which both formats hold exactly.
+// Between groups of products: LDS reads and products keep their groups, so
+// that a group's operands are read while the group before is multiplied.
+__device__ __forceinline__ void group_fence() {
+  __builtin_amdgcn_sched_barrier(0x6);  // vector and scalar ALU may move across
+}
+
+// Hides a value's origin, so that what depends on it is formed where it is
+// used and not kept in registers across a loop.
+__device__ __forceinline__ int fresh(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
+// max over the two halves of a wave (lanes l and l ^ 32).  The swap puts the
+// lower halves of both registers into the first and the upper halves into the
+// second; the no-op covers the two wait states it needs behind the write of
+// its operands.  (The builtin's two results were taken for equal and the max
+// dropped.)
+__device__ __forceinline__ float half_max(float x) {
+  float y = x;
+  asm("s_nop 1\n\tv_permlane32_swap_b32 %0, %1" : "+v"(x), "+v"(y));
+  return fmaxf(x, y);
+}
+
+// What a thread stages at once of a cache's rows (element type CT) into a
+// tile of IO: N chunks of 16 bytes of the tile.  e4m3 codes become the values
+// they stand for (the row's scale is applied to the scores and weights, in
+// float32), which both formats hold exactly.
 template <typename IO, typename CT> struct chunk_src {
   typedef u32x4 raw;
+  static constexpr int N = 1;
   __device__ static __forceinline__ raw load(const CT *p) { return *reinterpret_cast<const u32x4 *>(p); }
   __device__ static __forceinline__ raw zero() { return u32x4{0u, 0u, 0u, 0u}; }
-  __device__ static __forceinline__ u32x4 widen(raw x) { return x; }
+  __device__ static __forceinline__ u32x4 widen(raw x, int) { return x; }
 };
 template <> struct chunk_src<bf16_t, f8_t> {
-  typedef u32x2 raw;
-  __device__ static __forceinline__ raw load(const f8_t *p) { return *reinterpret_cast<const u32x2 *>(p); }
-  __device__ static __forceinline__ raw zero() { return u32x2{0u, 0u}; }
-  __device__ static __forceinline__ u32x4 widen(raw x) {
+  typedef u32x4 raw;
+  static constexpr int N = 2;
+  __device__ static __forceinline__ raw load(const f8_t *p) { return *reinterpret_cast<const u32x4 *>(p); }
+  __device__ static __forceinline__ raw zero() { return u32x4{0u, 0u, 0u, 0u}; }
+  __device__ static __forceinline__ u32x4 widen(raw x, int i) {
     u32x4 y;
-    y[0] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[0], 1.0f, false));
-    y[1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[0], 1.0f, true));
-    y[2] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[1], 1.0f, false));
-    y[3] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[1], 1.0f, true));
+    y[0] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * i], 1.0f, false));
+    y[1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * i], 1.0f, true));
+    y[2] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * i + 1], 1.0f, false));
+    y[3] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * i + 1], 1.0f, true));
     return y;
   }
 };
 template <> struct chunk_src<float, f8_t> {
   typedef unsigned raw;
+  static constexpr int N = 1;
   __device__ static __forceinline__ raw load(const f8_t *p) { return *reinterpret_cast<const unsigned *>(p); }
   __device__ static __forceinline__ raw zero() { return 0u; }
-  __device__ static __forceinline__ u32x4 widen(raw x) {
+  __device__ static __forceinline__ u32x4 widen(raw x, int) {
     const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(x, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(x, true);
     const f32x4 y = {a[0], a[1], b[0], b[1]};
     return __builtin_bit_cast(u32x4, y);

@@ -25,33 +25,36 @@ struct bwd_args {
   const int32_t *cu;
   int N, T, Ttot, Hq, Hk, G, window;
   float c, scale;
+  int gs;   // heads of a row tile of the dk, dv kernel
   order od;
 };
 
-// delta and the base-2 lse of every row, in row-tile order.  A wave takes
-// one row at a time, D / 64 channels a lane.
+// delta and the base-2 lse of every row, in row-tile order: D / 8 lanes a
+// row, 8 channels each.
 template <typename IO, int D> __global__ void __launch_bounds__(256) gdn2_attn_stat_kernel(bwd_args a) {
-  const int lane = threadIdx.x & 63;
+  constexpr int LPR = D / 8, RPB = 256 / LPR;
+  const int j = threadIdx.x % LPR;
   const size_t rows = static_cast<size_t>(a.Ttot) * a.Hq;
-  const size_t row = static_cast<size_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const size_t row = static_cast<size_t>(blockIdx.x) * RPB + threadIdx.x / LPR;
   if (row >= rows)
     return;
-  const size_t tok = row / a.Hq;
-  const int head = static_cast<int>(row % a.Hq), hk = head / a.G, g = head % a.G;
+  const size_t tok = row / static_cast<unsigned>(a.Hq);
   if (a.cu && static_cast<long>(tok) >= a.cu[a.N])
     return;  // behind the last sequence
-  constexpr int V = D / 64;
-  const IO *o = static_cast<const IO *>(a.o) + row * D + V * lane;
-  const IO *d = static_cast<const IO *>(a.dout) + row * D + V * lane;
+  const IO *o = static_cast<const IO *>(a.o) + row * D + 8 * j;
+  const IO *d = static_cast<const IO *>(a.dout) + row * D + 8 * j;
+  const f32x4 o0 = io<IO>::load4(o), o1 = io<IO>::load4(o + 4), d0 = io<IO>::load4(d), d1 = io<IO>::load4(d + 4);
   float x = 0.f;
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-    x += io<IO>::to_f(o[i]) * io<IO>::to_f(d[i]);
+  for (int i = 0; i < 4; ++i)
+    x += o0[i] * d0[i] + o1[i] * d1[i];
 #pragma unroll
-  for (int s = 1; s < 64; s <<= 1)
+  for (int s = 1; s < LPR; s <<= 1)
     x += __shfl_xor(x, s, 64);
-  if (lane == 0)
+  if (j == 0) {
+    const int head = static_cast<int>(row - tok * a.Hq), hk = head / a.G, g = head % a.G;
     a.stat[(static_cast<size_t>(hk) * a.Ttot + tok) * a.G + g] = f32x2{a.lse[row] * LOG2E, x};
+  }
 }
 
 // The sequence of a workgroup's tile and the tile's first row in it (rows:
@@ -112,15 +115,19 @@ __global__ void __launch_bounds__(256, (D * sizeof(IO) <= 256 ? 2 : 1)) gdn2_att
     d[kk] = load8<IO>(static_cast<const IO *>(a.dout) + qrow * D + 16 * kk + 8 * h);
   }
   const int sc = tid % CPR, sr0 = tid / CPR;
+  const int row_b = TL::row_base(r, h), col_b = TL::col_base(lane), st_b = TL::at(sr0, sc);
+  const unsigned kstep = static_cast<unsigned>(a.Hk) * D;  // values of a token
   u32x4 rk[CH], rv[CH];
   auto load_tile = [&](int kb) {
+    const size_t base = (static_cast<size_t>(sq.start + kb) * a.Hk + hk) * D;
+    const IO *const kp = static_cast<const IO *>(a.k) + base, *const vp = static_cast<const IO *>(a.v) + base;
+    const int left = k1 - 1 - kb;  // (a key behind the last: any, its score is masked)
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      int j = kb + sr0 + RPI * i;
-      j = j < k1 ? j : k1 - 1;
-      const size_t off = (static_cast<size_t>(sq.start + j) * a.Hk + hk) * D + sc * TL::VPC;
-      rk[i] = *reinterpret_cast<const u32x4 *>(static_cast<const IO *>(a.k) + off);
-      rv[i] = *reinterpret_cast<const u32x4 *>(static_cast<const IO *>(a.v) + off);
+      const int x = sr0 + RPI * i;
+      const unsigned off = (x < left ? x : left) * kstep + sc * TL::VPC;
+      rk[i] = *reinterpret_cast<const u32x4 *>(kp + off);
+      rv[i] = *reinterpret_cast<const u32x4 *>(vp + off);
     }
   };
   f32x16 dq[D / 32];
@@ -129,17 +136,18 @@ __global__ void __launch_bounds__(256, (D * sizeof(IO) <= 256 ? 2 : 1)) gdn2_att
     dq[n] = zero16();
   load_tile(k0);
   for (int it = 0; it < ntiles; ++it) {
-    const int kb = k0 + it * BN;
-    char *kt = lds + (it & 1) * 2 * TILEB, *vt = kt + TILEB;
+    const int kb = k0 + it * BN, bo = (it & 1) * 2 * TILEB;
+    char *const kt = lds, *const vt = lds + TILEB;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int at = TL::at(sr0 + RPI * i, sc);
+      const int at = bo + TL::template step<RPI>(st_b, sr0, sc, i);
       *reinterpret_cast<u32x4 *>(kt + at) = rk[i];
       *reinterpret_cast<u32x4 *>(vt + at) = rv[i];
     }
     __syncthreads();
     if (it + 1 < ntiles)
       load_tile(kb + BN);
+    const int rb = row_b + bo, cb = col_b + bo;
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
       const int wk = kb + 32 * t;
@@ -149,8 +157,8 @@ __global__ void __launch_bounds__(256, (D * sizeof(IO) <= 256 ? 2 : 1)) gdn2_att
       f32x16 s = zero16(), dp = zero16();
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
-        mma(s, TL::row(kt, 32 * t + r, kk, h), q[kk]);
-        mma(dp, TL::row(vt, 32 * t + r, kk, h), d[kk]);
+        mma(s, TL::row(kt + 32 * t * TL::ROWB, rb, kk), q[kk]);
+        mma(dp, TL::row(vt + 32 * t * TL::ROWB, rb, kk), d[kk]);
       }
 #pragma unroll
       for (int i = 0; i < 16; ++i)
@@ -168,7 +176,7 @@ __global__ void __launch_bounds__(256, (D * sizeof(IO) <= 256 ? 2 : 1)) gdn2_att
         const frag8<IO> x = pack8<IO>(s, jj);
 #pragma unroll
         for (int n = 0; n < D / 32; ++n)
-          mma(dq[n], TL::col(kt, 32 * t + 16 * jj, n, lane), x);
+          mma(dq[n], TL::col(kt, cb, 32 * t + 16 * jj, n), x);
       }
     }
   }
@@ -187,82 +195,118 @@ __global__ void __launch_bounds__(256, (D * sizeof(IO) <= 256 ? 2 : 1)) gdn2_att
 }
 
 // --------------------------------------------------------------- dk, dv --
-// A workgroup owns 32 keys per wave (K and V in registers) and walks the
-// rows that see any of them, 32 at a time through shared memory.
-template <typename IO, int D, int W>
-__global__ void __launch_bounds__(64 * W, 1) gdn2_attn_dkv_kernel(bwd_args a) {
+// A workgroup owns 32 WK keys and walks the rows that see any of them, 32 WR
+// at a time: wave (wk, wr) takes keys 32 wk .. + 31 and of every tile the rows
+// 32 wr .. + 31; the row parts' sums are joined at the end.  K, V and the
+// tile of Q and dO are read from shared memory: K and V in registers would
+// leave one wave a SIMD (their 64 registers beside the 128 of the sums).
+template <typename IO, int D, int WK, int WR>
+__global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1)) gdn2_attn_dkv_kernel(bwd_args a) {
   typedef tile<IO, D> TL;
-  constexpr int NT = 64 * W, BK = 32 * W, BQ = 32, CPR = TL::CPR, CH = BQ * CPR / NT, RPI = NT / CPR;
-  constexpr int TILEB = BQ * TL::ROWB;
-  static_assert(BQ * CPR % NT == 0, "staging split");
-  __shared__ __align__(16) char lds[4 * TILEB];
-  __shared__ __align__(16) float s_lse[2][BQ], s_delta[2][BQ];
-  __shared__ __align__(16) int s_pos[2][BQ];
+  constexpr int NT = 64 * WK * WR, BK = 32 * WK, BQ = 32 * WR, CPR = TL::CPR, CH = BQ * CPR / NT, RPI = NT / CPR;
+  constexpr int TILEB = BQ * TL::ROWB, KTB = BK * TL::ROWB, KCH = BK * CPR / NT;
+  // a second buffer for the tile where it does not cost a workgroup a CU
+  constexpr int NB = 2 * KTB + 4 * TILEB <= 80000 || (2 * KTB + 2 * TILEB > 80000 && 2 * KTB + 4 * TILEB <= 150000) ? 2 : 1;
+  static_assert(BQ * CPR % NT == 0 && BK * CPR % NT == 0, "staging split");
+  // K, V, Q and dO; in the end the room in which the sums are joined
+  constexpr int TILES = 2 * KTB + NB * 2 * TILEB, JOIN = WK * WR * 32 * D * 4;
+  __shared__ __align__(16) char lds[TILES > JOIN ? TILES : JOIN];
+  __shared__ __align__(16) float s_lse[NB][BQ], s_delta[NB][BQ];
+  __shared__ __align__(16) int s_pos[NB][BQ];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 31, h = lane >> 5;
+  const int wkey = wave % WK, wrow = wave / WK;
   int unit, slot, hk, key0;
   span sq;
   if (!place(a.od, blockIdx.x, unit, slot) || !locate(a, unit, a.od.tiles - 1 - slot, 1, BK, lane, sq, hk, key0))
     return;
   const int key_end = key0 + BK < sq.len ? key0 + BK : sq.len;
-  // rows (token, head of the group) that see a key of the workgroup
-  const int row0 = key0 * a.G;
+  // Tokens whose rows see a key of the workgroup.  A tile is TB whole tokens
+  // of GS heads (GS: the largest divisor of G up to 32; its TB GS rows come
+  // first, the rest of the tile's are no rows), so that a thread's rows keep
+  // their places in it and only the tile's base moves; G / GS turns over the
+  // tokens take all heads.
   int tok_end = sq.len;
   if (a.window > 0 && key_end - 1 + static_cast<long>(a.window) < tok_end)
     tok_end = key_end - 1 + a.window;
-  const int row1 = tok_end * a.G;
-  const int wk = key0 + 32 * wave;        // the wave's first key
-  const int key = wk + r;                 // the lane's
-  const bool key_ok = key < sq.len;
-  const size_t krow = static_cast<size_t>(sq.start + (key_ok ? key : sq.len - 1)) * a.Hk + hk;
+  const int GS = a.gs, TB = BQ / GS, nrows = TB * GS;
+  const int wk = key0 + 32 * wkey;  // the wave's first key
+  const int key = wk + r;           // the lane's
   const int wk_hi = wk + 31 < sq.len - 1 ? wk + 31 : sq.len - 1;
 
-  frag8<IO> k[D / 16], v[D / 16];
-#pragma unroll
-  for (int kk = 0; kk < D / 16; ++kk) {
-    k[kk] = load8<IO>(static_cast<const IO *>(a.k) + krow * D + 16 * kk + 8 * h);
-    v[kk] = load8<IO>(static_cast<const IO *>(a.v) + krow * D + 16 * kk + 8 * h);
-  }
   const int sc = tid % CPR, sr0 = tid / CPR;
+  const int row_b = TL::row_base(r, h), col_b = TL::col_base(lane), st_b = TL::at(sr0, sc);
+  char *const kt = lds, *const vt = lds + KTB, *const qt = lds + 2 * KTB, *const dt = qt + TILEB;
+#pragma unroll
+  for (int i = 0; i < KCH; ++i) {
+    // (a key behind the last: any row, it is not stored)
+    const int x = sr0 + RPI * i, j = key0 + x < sq.len ? key0 + x : sq.len - 1;
+    const size_t off = (static_cast<size_t>(sq.start + j) * a.Hk + hk) * D + sc * TL::VPC;
+    *reinterpret_cast<u32x4 *>(lds + TL::at(x, sc)) =
+        *reinterpret_cast<const u32x4 *>(static_cast<const IO *>(a.k) + off);
+    *reinterpret_cast<u32x4 *>(lds + KTB + TL::at(x, sc)) =
+        *reinterpret_cast<const u32x4 *>(static_cast<const IO *>(a.v) + off);
+  }
   u32x4 rq[CH], rd[CH];
   f32x2 rs = {0.f, 0.f};
   int rp = 0;
-  auto load_tile = [&](int rb) {
+  int tok_of[CH];  // token of a thread's row in the tile, and its values' place
+  unsigned at_of[CH];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    int x = sr0 + RPI * i;
+    x = x < nrows ? x : nrows - 1;
+    tok_of[i] = x / GS;
+    at_of[i] = static_cast<unsigned>(x % GS * D + sc * TL::VPC);
+  }
+  const int my_x = tid < nrows ? tid : nrows - 1, my_tok = my_x / GS, my_g = my_x % GS;
+  const bool my_ok = tid < nrows;
+  const unsigned tstep = static_cast<unsigned>(a.Hq) * D;  // values of a token
+  const int ntok = (tok_end - key0 + TB - 1) / TB, ntiles = ntok * (a.G / GS);
+  // Order of the tiles: a sequence's workgroups run side by side on one die,
+  // whose L2 holds a part of its rows, so they walk the tokens in step: without
+  // a window from the end down, where all have rows; with one from the first
+  // tile whose index is a multiple of the window's tiles.
+  int turn = 0;
+  if (a.window > 0) {
+    const int period = static_cast<int>((static_cast<long>(a.window) + BK - 1) / TB) + 1;
+    turn = (period - key0 / TB % period) % period;
+    turn = turn < ntok ? turn : 0;
+  }
+  auto load_tile = [&](int it) {
+    const int sub = it / ntok;
+    int x = it - sub * ntok;
+    x = a.window > 0 ? (x + turn < ntok ? x + turn : x + turn - ntok) : ntok - 1 - x;
+    const int t0 = key0 + x * TB;
+    const size_t base = (static_cast<size_t>(sq.start + t0) * a.Hq + hk * a.G + sub * GS) * D;
+    const IO *const qb = static_cast<const IO *>(a.q) + base, *const db = static_cast<const IO *>(a.dout) + base;
+    const int left = tok_end - 1 - t0;  // (a token behind the last: any, its weight is 0)
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int row = rb + sr0 + RPI * i;
-      if (row < row1) {
-        const int tok = row / a.G;
-        const size_t off =
-            (static_cast<size_t>(sq.start + tok) * a.Hq + hk * a.G + (row - tok * a.G)) * D + sc * TL::VPC;
-        rq[i] = *reinterpret_cast<const u32x4 *>(static_cast<const IO *>(a.q) + off);
-        rd[i] = *reinterpret_cast<const u32x4 *>(static_cast<const IO *>(a.dout) + off);
-      } else {
-        rq[i] = rd[i] = u32x4{0u, 0u, 0u, 0u};
-      }
+      const unsigned off = (tok_of[i] < left ? tok_of[i] : left) * tstep + at_of[i];
+      rq[i] = *reinterpret_cast<const u32x4 *>(qb + off);
+      rd[i] = *reinterpret_cast<const u32x4 *>(db + off);
     }
     if (tid < BQ) {
-      const int row = rb + tid;
-      // a row behind the last: weight 2^(0 - inf) = 0
-      rs = f32x2{__builtin_inff(), 0.f};
-      rp = 0x3fffffff;
-      if (row < row1) {
-        rs = a.stat[(static_cast<size_t>(hk) * a.Ttot + sq.start) * a.G + row];
-        rp = row / a.G;
-      }
+      const bool ok = my_ok && my_tok <= left;
+      const f32x2 x = a.stat[(static_cast<size_t>(hk) * a.Ttot + sq.start + t0 + (ok ? my_tok : 0)) * a.G + sub * GS + my_g];
+      // no row: weight 2^(0 - inf) = 0
+      rs = f32x2{ok ? x[0] : __builtin_inff(), ok ? x[1] : 0.f};
+      rp = t0 + my_tok;
     }
   };
   f32x16 dk[D / 32], dv[D / 32];
 #pragma unroll
   for (int n = 0; n < D / 32; ++n)
     dk[n] = dv[n] = zero16();
-  const int ntiles = (row1 - row0 + BQ - 1) / BQ;
-  load_tile(row0);
+  load_tile(0);
   for (int it = 0; it < ntiles; ++it) {
-    const int rb = row0 + it * BQ, buf = it & 1;
-    char *qt = lds + buf * 2 * TILEB, *dt = qt + TILEB;
+    const int buf = NB == 2 ? it & 1 : 0;
+    const int bo = buf * 2 * TILEB;
+    if (NB == 1 && it > 0)
+      __syncthreads();  // the tile before is read
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int at = TL::at(sr0 + RPI * i, sc);
+      const int at = bo + TL::template step<RPI>(st_b, sr0, sc, i);
       *reinterpret_cast<u32x4 *>(qt + at) = rq[i];
       *reinterpret_cast<u32x4 *>(dt + at) = rd[i];
     }
@@ -273,22 +317,27 @@ __global__ void __launch_bounds__(64 * W, 1) gdn2_attn_dkv_kernel(bwd_args a) {
     }
     __syncthreads();
     if (it + 1 < ntiles)
-      load_tile(rb + BQ);
-    const int lr = rb + BQ - 1 < row1 - 1 ? rb + BQ - 1 : row1 - 1;
-    const int p_lo = rb / a.G, p_hi = lr / a.G;
-    if (wk > p_hi || wk >= sq.len || (a.window > 0 && wk_hi <= p_lo - a.window))
+      load_tile(it + 1);
+    const int u0 = 32 * wrow;
+    if (u0 >= nrows)
+      continue;
+    const int p_lo = __builtin_amdgcn_readfirstlane(s_pos[buf][u0]);
+    const int p_hi = __builtin_amdgcn_readfirstlane(s_pos[buf][u0 + 31]);
+    if (p_lo >= tok_end || wk > p_hi || wk >= sq.len || (a.window > 0 && wk_hi <= p_lo - a.window))
       continue;  // no row sees a key of the wave
     const bool masked = wk_hi > p_lo || (a.window > 0 && wk <= p_hi - a.window);
+    const int rb = row_b + bo + u0 * TL::ROWB, cb = col_b + bo + u0 * TL::ROWB;
+    const int kb = fresh(row_b + 32 * wkey * TL::ROWB);
     f32x16 s = zero16(), dp = zero16();
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
-      mma(s, TL::row(qt, r, kk, h), k[kk]);
-      mma(dp, TL::row(dt, r, kk, h), v[kk]);
+      mma(s, TL::row(qt, rb, kk), TL::row(kt, kb, kk));
+      mma(dp, TL::row(dt, rb, kk), TL::row(vt, kb, kk));
     }
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      const f32x4 ls = *reinterpret_cast<const f32x4 *>(&s_lse[buf][8 * g + 4 * h]);
-      const f32x4 de = *reinterpret_cast<const f32x4 *>(&s_delta[buf][8 * g + 4 * h]);
+      const f32x4 ls = *reinterpret_cast<const f32x4 *>(&s_lse[buf][u0 + 8 * g + 4 * h]);
+      const f32x4 de = *reinterpret_cast<const f32x4 *>(&s_delta[buf][u0 + 8 * g + 4 * h]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float p = fast_exp2(s[4 * g + i] * a.c - ls[i]);
@@ -300,7 +349,7 @@ __global__ void __launch_bounds__(64 * W, 1) gdn2_attn_dkv_kernel(bwd_args a) {
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         typedef __attribute__((ext_vector_type(4))) int i32x4;
-        const i32x4 ps = *reinterpret_cast<const i32x4 *>(&s_pos[buf][8 * g + 4 * h]);
+        const i32x4 ps = *reinterpret_cast<const i32x4 *>(&s_pos[buf][u0 + 8 * g + 4 * h]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const bool vis = key <= ps[i] && (a.window <= 0 || key > ps[i] - a.window);
@@ -314,26 +363,75 @@ __global__ void __launch_bounds__(64 * W, 1) gdn2_attn_dkv_kernel(bwd_args a) {
       const frag8<IO> p = pack8<IO>(s, jj), ds = pack8<IO>(dp, jj);
 #pragma unroll
       for (int n = 0; n < D / 32; ++n) {
-        mma(dv[n], TL::col(dt, 16 * jj, n, lane), p);
-        mma(dk[n], TL::col(qt, 16 * jj, n, lane), ds);
+        mma(dv[n], TL::col(dt, cb, 16 * jj, n), p);
+        mma(dk[n], TL::col(qt, cb, 16 * jj, n), ds);
       }
     }
   }
-  if (!key_ok)
-    return;
+  // The row parts joined: halves until two are left; of those, wave (wk, 1)
+  // leaves dk and takes dv, wave (wk, 0) the other way round.
+  constexpr int PART = 32 * D;  // floats
+  auto slot_of = [&](int x) { return reinterpret_cast<float *>(lds) + (x * WK + wkey) * PART + 4 * lane; };
+  auto leave = [&](const f32x16(&x)[D / 32], float *to) {
 #pragma unroll
-  for (int n = 0; n < D / 32; ++n)
+    for (int n = 0; n < D / 32; ++n)
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      f32x4 x, y;
+      for (int g = 0; g < 4; ++g)
+        *reinterpret_cast<f32x4 *>(to + (4 * n + g) * 256) =
+            f32x4{x[n][4 * g], x[n][4 * g + 1], x[n][4 * g + 2], x[n][4 * g + 3]};
+  };
+  auto take = [&](f32x16(&x)[D / 32], const float *from) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[i] = dk[n][4 * g + i] * a.scale;
-        y[i] = dv[n][4 * g + i];
+    for (int n = 0; n < D / 32; ++n)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x4 y = *reinterpret_cast<const f32x4 *>(from + (4 * n + g) * 256);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          x[n][4 * g + i] += y[i];
       }
-      io<IO>::store4(static_cast<IO *>(a.dk) + krow * D + 32 * n + 8 * g + 4 * h, x);
-      io<IO>::store4(static_cast<IO *>(a.dv) + krow * D + 32 * n + 8 * g + 4 * h, y);
+  };
+  auto store = [&](const f32x16(&x)[D / 32], float scale, IO *out) {
+    if (key >= sq.len)
+      return;
+    IO *row = out + (static_cast<size_t>(sq.start + key) * a.Hk + hk) * D + 4 * h;
+#pragma unroll
+    for (int n = 0; n < D / 32; ++n)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        f32x4 z;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          z[i] = x[n][4 * g + i] * scale;
+        io<IO>::store4(row + 32 * n + 8 * g, z);
+      }
+  };
+#pragma unroll
+  for (int half = WR / 2; half > 1; half /= 2) {
+    __syncthreads();
+    if (wrow >= half && wrow < 2 * half) {
+      leave(dk, slot_of(wrow - half));
+      leave(dv, slot_of(wrow));
     }
+    __syncthreads();
+    if (wrow < half) {
+      take(dk, slot_of(wrow));
+      take(dv, slot_of(wrow + half));
+    }
+  }
+  __syncthreads();
+  if (wrow == 0)
+    leave(dv, slot_of(0));
+  else if (wrow == 1)
+    leave(dk, slot_of(1));
+  __syncthreads();
+  if (wrow == 0) {
+    take(dk, slot_of(1));
+    store(dk, a.scale, static_cast<IO *>(a.dk));
+  } else if (wrow == 1) {
+    take(dv, slot_of(0));
+    store(dv, 1.f, static_cast<IO *>(a.dv));
+  }
 }
 
 // ------------------------------------------------------------- launchers --
@@ -358,6 +456,9 @@ static void fill(bwd_args &a, const attn_sizes &z, const attn_ptrs &p, void *ws)
   a.window = z.window;
   a.c = z.scale * LOG2E;
   a.scale = z.scale;
+  a.gs = a.G < 32 ? a.G : 32;
+  while (a.G % a.gs)
+    --a.gs;
 }
 
 template <typename IO, int D>
@@ -365,7 +466,9 @@ hipError_t launch_attn_bwd_stat(const attn_sizes &z, const attn_ptrs &p, void *w
   bwd_args a;
   fill(a, z, p, ws);
   const size_t rows = static_cast<size_t>(z.Ttot) * z.Hq;
-  hipLaunchKernelGGL((gdn2_attn_stat_kernel<IO, D>), dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(256), 0, st, a);
+  constexpr int RPB = 256 / (D / 8);
+  hipLaunchKernelGGL((gdn2_attn_stat_kernel<IO, D>), dim3(static_cast<unsigned>((rows + RPB - 1) / RPB)), dim3(256), 0,
+                     st, a);
   return hipGetLastError();
 }
 template <typename IO, int D>
@@ -381,9 +484,19 @@ template <typename IO, int D>
 hipError_t launch_attn_bwd_dkv(const attn_sizes &z, const attn_ptrs &p, void *ws, hipStream_t st) {
   bwd_args a;
   fill(a, z, p, ws);
-  constexpr int W = 4;
-  const unsigned blocks = plan_tiles(z, 1, 32 * W, a.od);
-  hipLaunchKernelGGL((gdn2_attn_dkv_kernel<IO, D, W>), dim3(blocks), dim3(64 * W), 0, st, a);
+  // Where the tiles do not give every CU two, the longest sequence's first
+  // keys, which every row sees, take as long as the call: half as many keys
+  // and twice the row parts a workgroup.  (bfloat16, 11 packed sequences of up
+  // to 3167 tokens x 4 kv heads, d = 64: 356 tiles, 157 against 200 us; 8 x
+  // 4096 x 4, d = 128, window 2048: 1024 tiles, 1321 against 985 us.)
+  constexpr int WK = sizeof(IO) == 2 ? 4 : 2, WR4 = D * sizeof(IO) <= 256 ? 4 : 2;
+  unsigned blocks = plan_tiles(z, 1, 32 * WK, a.od);
+  if (static_cast<long long>(a.od.units) * a.od.tiles >= 512) {
+    hipLaunchKernelGGL((gdn2_attn_dkv_kernel<IO, D, WK, 2>), dim3(blocks), dim3(128 * WK), 0, st, a);
+  } else {
+    blocks = plan_tiles(z, 1, 16 * WK, a.od);
+    hipLaunchKernelGGL((gdn2_attn_dkv_kernel<IO, D, WK / 2, WR4>), dim3(blocks), dim3(32 * WK * WR4), 0, st, a);
+  }
   return hipGetLastError();
 }
 

@@ -17,6 +17,7 @@
 // WM waves share key tiles of 32 KT keys along 32-row blocks; WN waves split
 // the tile's keys (each keeps its own m, l, O, joined at the end).
 #include "gdn2_attn.hpp"
+#include <type_traits>
 
 namespace gdn2 {
 namespace attn {
@@ -63,6 +64,14 @@ __device__ __forceinline__ bool drop_nonfinite(frag8<float> &x) {
   return any;
 }
 
+// The wave's LDS accesses before and after, by any of its lanes, keep their
+// order (the hardware keeps it; this keeps the compiler to it).
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Four channels of a row: its output, or with split keys its float32 part.
 template <typename IO, int D>
 __device__ __forceinline__ void store_row(const fwd_args &a, f32x4 x, float l, size_t qrow, int split, bool ok, int ch) {
@@ -85,18 +94,32 @@ __device__ __forceinline__ void store_lse(const fwd_args &a, float m, float l, s
 }
 
 template <typename IO, typename CT, int D, int WM, int WN, int KT, bool PAGED>
-__global__ void __launch_bounds__(64 * WM * WN, (WN == 1 && D * sizeof(IO) <= 256 ? 2 : 1))
+__global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
     gdn2_attn_fwd_kernel(fwd_args a) {
   typedef tile<IO, D> TL;
   typedef chunk_src<IO, CT> CS;
-  constexpr int NT = 64 * WM * WN, BM = 32 * WM, BN = 32 * KT * WN;
-  constexpr int CPR = TL::CPR, CH = BN * CPR / NT;  // chunks a thread stages of K (and of V)
-  constexpr int TILEB = BN * TL::ROWB;
+  // SHARED: the workgroup's waves share a tile, double-buffered, with one
+  // barrier a tile.  Else every wave stages the keys it alone reads (single
+  // buffer, no barrier: a wave's LDS accesses stay in order).
+  constexpr bool SHARED = WN == 1;
+  constexpr int NT = SHARED ? 64 * WM : 64, BM = 32 * WM, BN = 32 * KT * WN, SN = 32 * KT, NB = SHARED ? 2 : 1;
+  constexpr int RPC = CS::N, CPR = TL::CPR / RPC;  // loads per row
+  constexpr int CH = SN * CPR / NT;                 // loads a thread stages of K (and of V)
+  constexpr int TILEB = SN * TL::ROWB;
   constexpr bool F8 = sizeof(CT) == 1;
-  static_assert(BN * CPR % NT == 0 && NT % CPR == 0, "staging split");
+  // Tiles under way from memory: a wave of its own stages little of e4m3
+  // (8 KB a tile), so it keeps two.
+  constexpr int DEPTH = !SHARED && F8 ? 2 : 1;
+  static_assert(SN * CPR % NT == 0 && NT % CPR == 0, "staging split");
   constexpr int ROWS_PER_I = NT / CPR;
-  __shared__ __align__(16) char lds[4 * TILEB];  // K and V tiles, double-buffered
-  __shared__ float kscale[F8 ? 2 * BN : 1], vscale[F8 ? 2 * BN : 1];
+  // K and V tiles; with split keys also the room in which the waves join
+  constexpr int JOIN = SHARED ? 0 : WN * 32 * ((D + 4) * 4 + 8);
+  constexpr int LDSB = 2 * NB * WN * TILEB > JOIN ? 2 * NB * WN * TILEB : JOIN;
+  __shared__ __align__(16) char lds[LDSB];
+  // waves of their own keep the queries, the same for all of them, here
+  // rather than in 32 registers
+  __shared__ __align__(16) char lq[SHARED ? 16 : 32 * TL::ROWB];
+  __shared__ __align__(16) float scales[F8 ? 2 * NB * WN * SN : 1];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int r = lane & 31, h = lane >> 5;
@@ -164,73 +187,93 @@ __global__ void __launch_bounds__(64 * WM * WN, (WN == 1 && D * sizeof(IO) <= 25
   const int wr1 = row0 + 32 * wm + 31 < rows ? row0 + 32 * wm + 31 : rows - 1;
   const int pos_lo = shift + wr0 / a.G, pos_hi = shift + wr1 / a.G;
 
-  frag8<IO> q[D / 16];
+  frag8<IO> q[SHARED ? D / 16 : 1];
+  const IO *const qp = static_cast<const IO *>(a.q) + qrow * D;
+  if constexpr (SHARED) {
 #pragma unroll
-  for (int kk = 0; kk < D / 16; ++kk)
-    q[kk] = load8<IO>(static_cast<const IO *>(a.q) + qrow * D + 16 * kk + 8 * h);
+    for (int kk = 0; kk < D / 16; ++kk)
+      q[kk] = load8<IO>(qp + 16 * kk + 8 * h);
+  } else {
+    // every wave has the same rows: wave w brings every WN-th chunk pair
+    for (int c = 2 * wn + h; c < TL::CPR; c += 2 * WN)
+      *reinterpret_cast<u32x4 *>(lq + TL::at(r, c)) = *reinterpret_cast<const u32x4 *>(qp + c * TL::VPC);
+    __syncthreads();
+  }
 
   // ---- staging: thread's chunk c of rows sr0 + ROWS_PER_I i
-  const int sc = tid % CPR, sr0 = tid / CPR;
-  typename CS::raw rk[CH], rv[CH];
+  const int st = SHARED ? tid : lane;
+  const int sc = st % CPR, sr0 = st / CPR + (SHARED ? 0 : SN * wn);
+  const int wave_b = wn * 2 * TILEB;  // the wave's tiles
+  const int row_b = TL::row_base(r, h) + wave_b, col_b = TL::col_base(lane) + wave_b;
+  char *const kt = lds, *const vt = lds + TILEB;
+  float *const kscale = scales + wn * 2 * SN, *const vscale = kscale + SN;
+  typename CS::raw rk[DEPTH][CH], rv[DEPTH][CH];
   int ent[CH];
-  uint8_t bk = 127, bv = 127;
+  uint8_t bk[DEPTH], bv[DEPTH];
   int ent_b = 0;
   const int32_t *table = PAGED ? a.table + static_cast<size_t>(sq.n) * a.max_pages : nullptr;
   const int pmask = (1 << a.page_shift) - 1;
-  // page-table entries of the tile at key kb (-1: row not staged)
+  // Rows of the tile at key kb; one behind the last key stands for that key's
+  // row (its score is masked).  Paged: the table's entries are fetched a tile
+  // ahead of the rows they lead to.
   auto load_entries = [&](int kb) {
     if constexpr (PAGED) {
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
         const int j = kb + sr0 + ROWS_PER_I * i;
-        int e = j < k1 ? table[j >> a.page_shift] : -1;
-        ent[i] = e < a.num_pages ? e : -1;
+        ent[i] = table[(j < k1 ? j : k1 - 1) >> a.page_shift];
       }
       if constexpr (F8) {
-        const int j = kb + tid;
-        int e = tid < BN && j < k1 ? table[j >> a.page_shift] : -1;
-        ent_b = e < a.num_pages ? e : -1;
+        const int j = kb + SN * wn + st % SN;
+        ent_b = table[(j < k1 ? j : k1 - 1) >> a.page_shift];
       }
     }
   };
-  auto load_tile = [&](int kb) {
+  const unsigned kstep = static_cast<unsigned>(a.Hk) * D;  // values of a token
+  auto load_tile = [&](int kb, int set) {
+    const size_t base = PAGED ? 0 : (static_cast<size_t>(sq.start + kb) * a.Hk + hk) * D;
+    const CT *const kp = static_cast<const CT *>(a.k) + base, *const vp = static_cast<const CT *>(a.v) + base;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int j = kb + sr0 + ROWS_PER_I * i;
-      size_t off;
-      bool ok;
+      int j = kb + sr0 + ROWS_PER_I * i;
+      j = j < k1 ? j : k1 - 1;
       if constexpr (PAGED) {
-        ok = ent[i] >= 0;
-        off = (((static_cast<size_t>(ok ? ent[i] : 0) * a.Hk + hk) << a.page_shift) + (j & pmask)) * D;
+        // an entry outside the cache stands for zeros
+        const bool ok = static_cast<unsigned>(ent[i]) < static_cast<unsigned>(a.num_pages);
+        const size_t off = (((static_cast<size_t>(ok ? ent[i] : 0) * a.Hk + hk) << a.page_shift) + (j & pmask)) * D +
+                           sc * (RPC * TL::VPC);
+        rk[set][i] = CS::load(kp + off);
+        rv[set][i] = CS::load(vp + off);
+        if (!ok)
+          rk[set][i] = rv[set][i] = CS::zero();
       } else {
-        ok = j < k1;
-        off = (static_cast<size_t>(sq.start + (ok ? j : 0)) * a.Hk + hk) * D;
+        const unsigned off = static_cast<unsigned>(j - kb) * kstep + sc * TL::VPC;
+        rk[set][i] = CS::load(kp + off);
+        rv[set][i] = CS::load(vp + off);
       }
-      off += sc * TL::VPC;
-      rk[i] = ok ? CS::load(static_cast<const CT *>(a.k) + off) : CS::zero();
-      rv[i] = ok ? CS::load(static_cast<const CT *>(a.v) + off) : CS::zero();
     }
     if constexpr (F8) {
-      bk = bv = 127;
-      if (ent_b >= 0 && tid < BN) {
-        const size_t off = ((static_cast<size_t>(ent_b) * a.Hk + hk) << a.page_shift) + ((kb + tid) & pmask);
-        bk = a.ks[off];
-        bv = a.vs[off];
-      }
+      int j = kb + SN * wn + st % SN;
+      j = j < k1 ? j : k1 - 1;
+      const bool ok = static_cast<unsigned>(ent_b) < static_cast<unsigned>(a.num_pages);
+      const size_t off = ((static_cast<size_t>(ok ? ent_b : 0) * a.Hk + hk) << a.page_shift) + (j & pmask);
+      bk[set] = a.ks[off];
+      bv[set] = a.vs[off];
     }
   };
-  auto store_tile = [&](int buf) {
-    char *kt = lds + buf * 2 * TILEB, *vt = kt + TILEB;
+  auto store_tile = [&](int buf, int set) {
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int at = TL::at(sr0 + ROWS_PER_I * i, sc);
-      *reinterpret_cast<u32x4 *>(kt + at) = CS::widen(rk[i]);
-      *reinterpret_cast<u32x4 *>(vt + at) = CS::widen(rv[i]);
-    }
+    for (int i = 0; i < CH; ++i)
+#pragma unroll
+      for (int x = 0; x < RPC; ++x) {
+        const int at = wave_b + buf * 2 * TILEB + TL::at(st / CPR + ROWS_PER_I * i, RPC * sc + x);
+        *reinterpret_cast<u32x4 *>(kt + at) = CS::widen(rk[set][i], x);
+        *reinterpret_cast<u32x4 *>(vt + at) = CS::widen(rv[set][i], x);
+      }
     if constexpr (F8) {
-      if (tid < BN) {
-        kscale[buf * BN + tid] = scale_of(bk);
-        vscale[buf * BN + tid] = scale_of(bv);
+      if (st < SN) {
+        kscale[buf * 2 * SN + st] = scale_of(bk[set]);
+        vscale[buf * 2 * SN + st] = scale_of(bv[set]);
       }
     }
   };
@@ -241,41 +284,70 @@ __global__ void __launch_bounds__(64 * WM * WN, (WN == 1 && D * sizeof(IO) <= 25
     o[n] = zero16();
   float m = neg_inf(), l = 0.f;  // l: this half's part of the sum
 
-  if (ntiles > 0) {
-    load_entries(k0);
-    load_tile(k0);
-    load_entries(k0 + BN);
-  }
-  for (int it = 0; it < ntiles; ++it) {
-    const int kb = k0 + it * BN, buf = it & 1;
-    store_tile(buf);
-    __syncthreads();
-    if (it + 1 < ntiles) {
-      load_tile(kb + BN);
-      load_entries(kb + 2 * BN);
+  auto tile_step = [&](int it, auto set) {
+    const int kb = k0 + it * BN, buf = SHARED ? it & 1 : 0;
+    if constexpr (SHARED) {
+      store_tile(buf, set);
+      __syncthreads();
+    } else {
+      // the lanes' reads of the tile before come first, their writes before
+      // the reads below
+      wave_order();
+      store_tile(buf, set);
+      wave_order();
     }
-    const char *kt = lds + buf * 2 * TILEB, *vt = kt + TILEB;
-    const int wk = kb + 32 * KT * wn;  // the wave's first key
-    // nothing of the tile is visible to the wave
-    if (wk > pos_hi || wk >= k1 || (a.window > 0 && wk + 32 * KT - 1 <= pos_lo - a.window))
-      continue;
+    if (it + DEPTH < ntiles) {
+      load_tile(kb + DEPTH * BN, set);
+      load_entries(kb + (DEPTH + 1) * BN);
+    }
+    const int rb = row_b + buf * 2 * TILEB, cb = col_b + buf * 2 * TILEB;
+    const float *const ksc = kscale + buf * 2 * SN, *const vsc = vscale + buf * 2 * SN;
+    const int wk = kb + SN * wn;  // the wave's first key
+    // no rows, or nothing of the tile is visible to the wave
+    if (row0 + 32 * wm >= rows || wk > pos_hi || wk >= k1 || (a.window > 0 && wk + 32 * KT - 1 <= pos_lo - a.window))
+      return;
     const bool masked = wk + 32 * KT - 1 > pos_lo || wk + 32 * KT > k1 ||
                         (a.window > 0 && wk <= pos_hi - a.window);
 
+    // S^T, and further down O^T, in groups of GR products whose operands are
+    // read a group ahead
+    constexpr int GR = sizeof(IO) == 2 && !PAGED ? 4 : 2, NS = KT * (D / 16);
+    const int qb = fresh(TL::row_base(r, h));
     f32x16 s[KT];
 #pragma unroll
-    for (int t = 0; t < KT; ++t) {
+    for (int t = 0; t < KT; ++t)
       s[t] = zero16();
+    {
+      frag8<IO> kf[2][GR], qf[2][SHARED ? 1 : GR];
+      auto fetch = [&](int g) {
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-        mma(s[t], TL::row(kt, 32 * (KT * wn + t) + r, kk, h), q[kk]);
+        for (int x = 0; x < GR; ++x) {
+          const int y = g * GR + x;
+          if constexpr (!SHARED)
+            qf[g & 1][x] = TL::row(lq, qb, y % (D / 16));
+          kf[g & 1][x] = TL::row(kt + 32 * (y / (D / 16)) * TL::ROWB, rb, y % (D / 16));
+        }
+      };
+      fetch(0);
+#pragma unroll
+      for (int g = 0; g < NS / GR; ++g) {
+        if (g + 1 < NS / GR)
+          fetch(g + 1);
+        group_fence();
+#pragma unroll
+        for (int x = 0; x < GR; ++x) {
+          const int y = g * GR + x;
+          mma(s[y / (D / 16)], kf[g & 1][x], SHARED ? q[SHARED ? y % (D / 16) : 0] : qf[g & 1][SHARED ? 0 : x]);
+        }
+        group_fence();
+      }
     }
     if constexpr (F8) {
 #pragma unroll
       for (int t = 0; t < KT; ++t)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const f32x4 sc4 = *reinterpret_cast<const f32x4 *>(&kscale[buf * BN + 32 * (KT * wn + t) + 8 * g + 4 * h]);
+          const f32x4 sc4 = *reinterpret_cast<const f32x4 *>(&ksc[32 * t + 8 * g + 4 * h]);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             s[t][4 * g + i] *= sc4[i];
@@ -300,26 +372,34 @@ __global__ void __launch_bounds__(64 * WM * WN, (WN == 1 && D * sizeof(IO) <= 25
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         mx = fmaxf(mx, s[t][i]);
-    mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-    const float m_new = fmaxf(m, mx * a.c);
-    const float base = m_new == neg_inf() ? 0.f : m_new;  // a row without keys yet
-    const float alpha = fast_exp2(m - base);
-    m = m_new;
-    float sum = 0.f;
+    mx = half_max(mx) * a.c;
+    // The reference of a row's exponents stays while its maximum is not more
+    // than 8 above it (weights up to 2^8: no loss, they are floating point),
+    // so that most tiles rescale nothing.
+    const bool up = mx > m + 8.f;
+    if (__any(up)) {
+      const float m_new = up ? mx : m;
+      const float alpha = fast_exp2(m - (m_new == neg_inf() ? 0.f : m_new));
+      m = m_new;
+      l *= alpha;
 #pragma unroll
-    for (int t = 0; t < KT; ++t)
+      for (int n = 0; n < D / 32; ++n)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          o[n][i] *= alpha;
+    }
+    const float base = m == neg_inf() ? 0.f : m;  // a row without keys yet
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const float p = fast_exp2(s[t][i] * a.c - base);
         s[t][i] = p;
-        sum += p;
+        sum[i & 3] += p;
       }
-    l = l * alpha + sum;
-#pragma unroll
-    for (int n = 0; n < D / 32; ++n)
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        o[n][i] *= alpha;
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    }
     if constexpr (F8) {
       // the values' scales go to the weights (a masked weight stays 0
       // whatever its row's scale holds)
@@ -327,7 +407,7 @@ __global__ void __launch_bounds__(64 * WM * WN, (WN == 1 && D * sizeof(IO) <= 25
       for (int t = 0; t < KT; ++t)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const f32x4 sc4 = *reinterpret_cast<const f32x4 *>(&vscale[buf * BN + 32 * (KT * wn + t) + 8 * g + 4 * h]);
+          const f32x4 sc4 = *reinterpret_cast<const f32x4 *>(&vsc[32 * t + 8 * g + 4 * h]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int j = 32 * t + 8 * g + i;
@@ -336,20 +416,30 @@ __global__ void __launch_bounds__(64 * WM * WN, (WN == 1 && D * sizeof(IO) <= 25
         }
     }
     bool odd = false;  // infinities or NaN among the values of a masked tile
+    {
+      constexpr int NN = D / 32, GV = NN < GR ? NN : GR, PER = NN / GV;
+      frag8<IO> vf[2][GV];
+      auto fetch = [&](int g) {
 #pragma unroll
-    for (int t = 0; t < KT; ++t)
+        for (int x = 0; x < GV; ++x)
+          vf[g & 1][x] = TL::col(vt, cb, 16 * (g / PER), g % PER * GV + x);
+      };
+      fetch(0);
 #pragma unroll
-      for (int jj = 0; jj < 2; ++jj) {
-        const frag8<IO> p = pack8<IO>(s[t], jj);
-        const int kr = 32 * (KT * wn + t) + 16 * jj;
+      for (int g = 0; g < 2 * KT * PER; ++g) {
+        if (g + 1 < 2 * KT * PER)
+          fetch(g + 1);
+        group_fence();
+        const frag8<IO> p = pack8<IO>(s[g / PER / 2], g / PER & 1);
 #pragma unroll
-        for (int n = 0; n < D / 32; ++n) {
-          frag8<IO> v = TL::col(vt, kr, n, lane);
+        for (int x = 0; x < GV; ++x) {
           if (masked)
-            odd |= drop_nonfinite(v);
-          mma(o[n], v, p);
+            odd |= drop_nonfinite(vf[g & 1][x]);
+          mma(o[g % PER * GV + x], vf[g & 1][x], p);
         }
+        group_fence();
       }
+    }
     // 0 times an infinity would reach rows that do not see its key: in a
     // masked tile such values are left out of the product above and added
     // here for the rows that do see them.
@@ -368,11 +458,27 @@ __global__ void __launch_bounds__(64 * WM * WN, (WN == 1 && D * sizeof(IO) <= 25
         for (int n = 0; n < D / 32; ++n)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float x = TL::one(vt, 32 * KT * wn + j, 32 * n + 8 * (i >> 2) + 4 * h + (i & 3));
+            const float x = TL::one(vt + wave_b + buf * 2 * TILEB, j, 32 * n + 8 * (i >> 2) + 4 * h + (i & 3));
             if (vis && !(fabsf(x) <= 3.4028234663852886e38f))
               o[n][i] += p * x;
           }
       }
+    }
+  };
+  if (ntiles > 0) {
+    load_entries(k0);
+#pragma unroll
+    for (int x = 0; x < DEPTH; ++x)
+      if (x == 0 || x < ntiles) {
+        load_tile(k0 + x * BN, x);
+        load_entries(k0 + (x + 1) * BN);
+      }
+  }
+  for (int it = 0; it < ntiles; it += DEPTH) {
+    tile_step(it, std::integral_constant<int, 0>());
+    if constexpr (DEPTH == 2) {
+      if (it + 1 < ntiles)
+        tile_step(it + 1, std::integral_constant<int, 1>());
     }
   }
 
@@ -382,7 +488,6 @@ __global__ void __launch_bounds__(64 * WM * WN, (WN == 1 && D * sizeof(IO) <= 25
     // join the waves' parts: weights 2^(m_w - M)
     static_assert(WM == 1, "one row block");
     constexpr int OLD = D + 4;
-    static_assert(WN * 32 * OLD * 4 + WN * 32 * 8 <= 4 * TILEB, "join space");
     float *jo = reinterpret_cast<float *>(lds);                 // [WN][32][OLD]
     float *jm = jo + WN * 32 * OLD, *jl = jm + WN * 32;
     __syncthreads();
@@ -442,15 +547,13 @@ __global__ void __launch_bounds__(64 * WM * WN, (WN == 1 && D * sizeof(IO) <= 25
   }
 }
 
-// Joins the parts of split keys: one wave per (token, query head), weights
-// 2^(lse_s - max lse); the order of the sum is fixed.
-template <typename IO, int D>
-__global__ void __launch_bounds__(256) gdn2_attn_join_kernel(fwd_args a) {
-  const int lane = threadIdx.x & 63;
-  const size_t rows = static_cast<size_t>(a.Ttot) * a.Hq;
-  const size_t row = static_cast<size_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  if (row >= rows)
-    return;
+// Joins the parts of split keys: a workgroup per (token, query head), wave w
+// takes the parts w, w + 4, ..; weights 2^(lse_s - max lse); the order of the
+// sums is fixed.
+template <typename IO, int D> __global__ void __launch_bounds__(256) gdn2_attn_join_kernel(fwd_args a) {
+  __shared__ float red[4][D + 1];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const size_t rows = static_cast<size_t>(a.Ttot) * a.Hq, row = blockIdx.x;
   if (a.cu && row >= static_cast<size_t>(a.cu[a.N] < 0 ? 0 : a.cu[a.N]) * a.Hq)
     return;  // behind the last sequence
   float M = neg_inf();
@@ -465,23 +568,29 @@ __global__ void __launch_bounds__(256) gdn2_attn_join_kernel(fwd_args a) {
 #pragma unroll
   for (int i = 0; i < V; ++i)
     acc[i] = 0.f;
-  for (int s = 0; s < a.splits; ++s) {
-    const float ls = a.part_lse[s * rows + row];
-    const float w = fast_exp2(ls - base);  // NaN stays NaN
-    L += w;
-    if (ls == neg_inf())
-      continue;
+#pragma unroll 4
+  for (int s = wave; s < a.splits; s += 4) {
+    // (a part without keys: weight 0 and zeros; NaN stays NaN)
+    const float w = fast_exp2(a.part_lse[s * rows + row] - base);
     const float *p = a.part_o + (s * rows + row) * D + V * lane;
+    L += w;
 #pragma unroll
     for (int i = 0; i < V; ++i)
       acc[i] += w * p[i];
   }
-  const float inv = L == 0.f ? 0.f : 1.f / L;
-  IO *o = static_cast<IO *>(a.o) + row * D + V * lane;
 #pragma unroll
   for (int i = 0; i < V; ++i)
-    o[i] = io<IO>::from_f(acc[i] * inv);
-  if (a.lse && lane == 0)
+    red[wave][V * lane + i] = acc[i];
+  if (lane == 0)
+    red[wave][D] = L;
+  __syncthreads();
+  L = (red[0][D] + red[1][D]) + (red[2][D] + red[3][D]);
+  const int c = threadIdx.x;
+  if (c < D) {
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    static_cast<IO *>(a.o)[row * D + c] = io<IO>::from_f(((red[0][c] + red[1][c]) + (red[2][c] + red[3][c])) * inv);
+  }
+  if (a.lse && c == 0)
     a.lse[row] = (base + log2f(L)) * LN2;
 }
 
@@ -492,19 +601,21 @@ __global__ void __launch_bounds__(256) gdn2_attn_join_kernel(fwd_args a) {
 static bool few_rows(const attn_sizes &z) {
   return static_cast<long long>(z.Ttot) * (z.Hq / z.Hk) <= 32LL * z.N;
 }
-// Parts along the keys of a paged call: enough workgroups for two rounds of
-// the 256 CUs, no part under 256 keys of the longest possible sequence.
+// Parts along the keys of a paged call: enough workgroups for several rounds
+// of the chip's 512 (sequences differ in length), no part of the longest
+// possible sequence under 128 keys, at most 128 parts.
 int attn_paged_splits(const attn_sizes &z) {
   order od;
-  plan_tiles(z, z.Hq / z.Hk, few_rows(z) ? 32 : 128, od);
+  const bool few = few_rows(z);
+  plan_tiles(z, z.Hq / z.Hk, few ? 32 : 128, od);
   const long long blocks = static_cast<long long>(od.units) * od.tiles;
   long long keys = z.max_keys;
   if (z.window > 0 && keys > z.window + 128LL)
     keys = z.window + 128LL;
-  long long s = (512 + blocks - 1) / blocks;
-  if (s > keys / 256)
-    s = keys / 256;
-  return s < 1 ? 1 : (s > 64 ? 64 : static_cast<int>(s));
+  long long s = ((few ? 2048 : 1024) + blocks - 1) / blocks;
+  if (s > keys / 128)
+    s = keys / 128;
+  return s < 1 ? 1 : (s > 128 ? 128 : static_cast<int>(s));
 }
 
 template <typename IO, typename CT, int D, int WM, int WN, int KT, bool PAGED>
@@ -570,7 +681,7 @@ hipError_t launch_attn_join(const attn_sizes &z, const attn_ptrs &p, int splits,
   const size_t rows = static_cast<size_t>(z.Ttot) * z.Hq;
   a.part_o = static_cast<float *>(ws);
   a.part_lse = a.part_o + rows * D * splits;
-  hipLaunchKernelGGL((gdn2_attn_join_kernel<IO, D>), dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(256), 0, st, a);
+  hipLaunchKernelGGL((gdn2_attn_join_kernel<IO, D>), dim3(static_cast<unsigned>(rows)), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 
