@@ -204,6 +204,15 @@ __device__ __forceinline__ float half_max(float x) {
   return fmaxf(x, y);
 }
 
+// 16 bytes a lane from global memory straight into shared memory, lane i's at
+// lds + 16 i (lds: one address for the wave); there after dma_wait() and a
+// barrier.
+__device__ __forceinline__ void dma16(const void *src, char *lds) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
+                                   (__attribute__((address_space(3))) void *)lds, 16, 0, 0);
+}
+__device__ __forceinline__ void dma_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
 // What a thread stages at once of a cache's rows (element type CT) into a
 // tile of IO: N chunks of 16 bytes of the tile.  e4m3 codes become the values
 // they stand for (the row's scale is applied to the scores and weights, in
@@ -317,6 +326,9 @@ inline unsigned plan_tiles(const attn_sizes &z, int GR, int BM, order &od) {
   od.tpr = (od.tiles + r - 1) / r;
   return 8u * static_cast<unsigned>(od.units / od.g) * static_cast<unsigned>(od.tpr);
 }
+// Fewer 128-row tiles than CUs: such calls take 32-row tiles whose keys the
+// waves split.
+inline bool few_tiles(const order &od) { return static_cast<long long>(od.units) * od.tiles < 256; }
 
 }  // namespace attn
 }  // namespace gdn2

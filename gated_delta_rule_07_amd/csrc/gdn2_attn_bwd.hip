@@ -77,14 +77,18 @@ __device__ __forceinline__ bool locate(const bwd_args &a, int unit, int slot, in
 }
 
 // ------------------------------------------------------------------- dq --
-template <typename IO, int D, int KT>
-__global__ void __launch_bounds__(256, (D * sizeof(IO) <= 256 ? 2 : 1)) gdn2_attn_dq_kernel(bwd_args a) {
+// WM waves of 32 rows each share key tiles; WN waves split a tile's keys and
+// join their sums at the end.  Wave (wm, wn) multiplies 32 KT keys of a tile.
+template <typename IO, int D, int WM, int WN, int KT>
+__global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1)) gdn2_attn_dq_kernel(bwd_args a) {
   typedef tile<IO, D> TL;
-  constexpr int BM = 128, BN = 32 * KT, CPR = TL::CPR, CH = BN * CPR / 256, RPI = 256 / CPR;
+  constexpr int NT = 64 * WM * WN, BM = 32 * WM, BN = 32 * KT * WN, CPR = TL::CPR, CH = BN * CPR / NT, RPI = NT / CPR;
   constexpr int TILEB = BN * TL::ROWB;
-  static_assert(BN * CPR % 256 == 0, "staging split");
-  __shared__ __align__(16) char lds[4 * TILEB];
+  static_assert(BN * CPR % NT == 0, "staging split");
+  static_assert(WN == 1 || WN * 32 * D * 4 <= 4 * TILEB, "join space");
+  __shared__ __align__(16) char lds[4 * TILEB];  // K and V tiles, double-buffered
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 31, h = lane >> 5;
+  const int wm = WN == 1 ? wave : 0, wn = WN == 1 ? 0 : wave;
   int unit, slot, hk, row0;
   span sq;
   if (!place(a.od, blockIdx.x, unit, slot) || !locate(a, unit, slot, a.G, BM, lane, sq, hk, row0))
@@ -98,13 +102,13 @@ __global__ void __launch_bounds__(256, (D * sizeof(IO) <= 256 ? 2 : 1)) gdn2_att
     k0 = k0 < 0 ? 0 : k0;
   }
   const int ntiles = (k1 - k0 + BN - 1) / BN;
-  const int my_row = row0 + 32 * wave + r;
+  const int my_row = row0 + 32 * wm + r;
   const bool row_ok = my_row < rows;
   const int cl_row = row_ok ? my_row : rows - 1;
   const int pos = cl_row / a.G, g = cl_row % a.G;
   const size_t qrow = static_cast<size_t>(sq.start + pos) * a.Hq + hk * a.G + g;
-  const int wr0 = row0 + 32 * wave < rows ? row0 + 32 * wave : rows - 1;
-  const int wr1 = row0 + 32 * wave + 31 < rows ? row0 + 32 * wave + 31 : rows - 1;
+  const int wr0 = row0 + 32 * wm < rows ? row0 + 32 * wm : rows - 1;
+  const int wr1 = row0 + 32 * wm + 31 < rows ? row0 + 32 * wm + 31 : rows - 1;
   const int pos_lo = wr0 / a.G, pos_hi = wr1 / a.G;
   const f32x2 st = a.stat[(static_cast<size_t>(hk) * a.Ttot + sq.start) * a.G + cl_row];
 
@@ -114,51 +118,68 @@ __global__ void __launch_bounds__(256, (D * sizeof(IO) <= 256 ? 2 : 1)) gdn2_att
     q[kk] = load8<IO>(static_cast<const IO *>(a.q) + qrow * D + 16 * kk + 8 * h);
     d[kk] = load8<IO>(static_cast<const IO *>(a.dout) + qrow * D + 16 * kk + 8 * h);
   }
-  const int sc = tid % CPR, sr0 = tid / CPR;
-  const int row_b = TL::row_base(r, h), col_b = TL::col_base(lane), st_b = TL::at(sr0, sc);
+  // Tiles come straight from memory: position p of one is chunk (p % CPR) ^ f
+  // of row p / CPR.
+  const int sc = tid % CPR, sr0 = tid / CPR, wv = __builtin_amdgcn_readfirstlane(wave);
+  const int row_b = TL::row_base(r, h), col_b = TL::col_base(lane);
   const unsigned kstep = static_cast<unsigned>(a.Hk) * D;  // values of a token
-  u32x4 rk[CH], rv[CH];
-  auto load_tile = [&](int kb) {
+  char *const kt = lds, *const vt = lds + TILEB;
+  auto load_tile = [&](int kb, int buf) {
     const size_t base = (static_cast<size_t>(sq.start + kb) * a.Hk + hk) * D;
     const IO *const kp = static_cast<const IO *>(a.k) + base, *const vp = static_cast<const IO *>(a.v) + base;
     const int left = k1 - 1 - kb;  // (a key behind the last: any, its score is masked)
+    char *const to = lds + buf * 2 * TILEB + 1024 * wv;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int x = sr0 + RPI * i;
-      const unsigned off = (x < left ? x : left) * kstep + sc * TL::VPC;
-      rk[i] = *reinterpret_cast<const u32x4 *>(kp + off);
-      rv[i] = *reinterpret_cast<const u32x4 *>(vp + off);
+      const unsigned off = (x < left ? x : left) * kstep + (sc ^ TL::f(x)) * TL::VPC;
+      dma16(kp + off, to + 16 * NT * i);
+      dma16(vp + off, to + TILEB + 16 * NT * i);
     }
   };
   f32x16 dq[D / 32];
 #pragma unroll
   for (int n = 0; n < D / 32; ++n)
     dq[n] = zero16();
-  load_tile(k0);
+  load_tile(k0, 0);
   for (int it = 0; it < ntiles; ++it) {
     const int kb = k0 + it * BN, bo = (it & 1) * 2 * TILEB;
-    char *const kt = lds, *const vt = lds + TILEB;
-#pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int at = bo + TL::template step<RPI>(st_b, sr0, sc, i);
-      *reinterpret_cast<u32x4 *>(kt + at) = rk[i];
-      *reinterpret_cast<u32x4 *>(vt + at) = rv[i];
-    }
+    dma_wait();
     __syncthreads();
     if (it + 1 < ntiles)
-      load_tile(kb + BN);
-    const int rb = row_b + bo, cb = col_b + bo;
+      load_tile(kb + BN, (it + 1) & 1);
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
-      const int wk = kb + 32 * t;
+      const int wk = kb + 32 * (KT * wn + t);
       if (wk > pos_hi || (a.window > 0 && wk + 31 <= pos_lo - a.window))
         continue;  // nothing visible to the wave
       const bool masked = wk + 31 > pos_lo || (a.window > 0 && wk <= pos_hi - a.window);
+      const int rb = row_b + bo + 32 * KT * wn * TL::ROWB, cb = col_b + bo + 32 * KT * wn * TL::ROWB;
       f32x16 s = zero16(), dp = zero16();
+      {
+        // operands read a group of products ahead
+        constexpr int GR = 2, NK = D / 16, NG = 2 * NK / GR;
+        frag8<IO> fa[2][GR];
+        auto fetch = [&](int x0) {
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        mma(s, TL::row(kt + 32 * t * TL::ROWB, rb, kk), q[kk]);
-        mma(dp, TL::row(vt + 32 * t * TL::ROWB, rb, kk), d[kk]);
+          for (int x = 0; x < GR; ++x) {
+            const int y = x0 * GR + x;
+            fa[x0 & 1][x] = TL::row((y < NK ? kt : vt) + 32 * t * TL::ROWB, rb, y % NK);
+          }
+        };
+        fetch(0);
+#pragma unroll
+        for (int x0 = 0; x0 < NG; ++x0) {
+          if (x0 + 1 < NG)
+            fetch(x0 + 1);
+          group_fence();
+#pragma unroll
+          for (int x = 0; x < GR; ++x) {
+            const int y = x0 * GR + x;
+            mma(y < NK ? s : dp, fa[x0 & 1][x], y < NK ? q[y % NK] : d[y % NK]);
+          }
+          group_fence();
+        }
       }
 #pragma unroll
       for (int i = 0; i < 16; ++i)
@@ -180,6 +201,31 @@ __global__ void __launch_bounds__(256, (D * sizeof(IO) <= 256 ? 2 : 1)) gdn2_att
       }
     }
   }
+  IO *const out = static_cast<IO *>(a.dq) + qrow * D + 4 * h;
+  if constexpr (WN > 1) {
+    // wave w sums the waves' parts of channel blocks w, w + WN, ..
+    float *const j = reinterpret_cast<float *>(lds) + 4 * lane;  // [wave][n, gg][lane]
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < D / 32; ++n)
+#pragma unroll
+      for (int gg = 0; gg < 4; ++gg)
+        *reinterpret_cast<f32x4 *>(j + (wn * (D / 8) + 4 * n + gg) * 256) =
+            f32x4{dq[n][4 * gg], dq[n][4 * gg + 1], dq[n][4 * gg + 2], dq[n][4 * gg + 3]};
+    __syncthreads();
+    if (!row_ok)
+      return;
+    for (int n = wn; n < D / 32; n += WN)
+#pragma unroll
+      for (int gg = 0; gg < 4; ++gg) {
+        f32x4 x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < WN; ++w)
+          x += *reinterpret_cast<const f32x4 *>(j + (w * (D / 8) + 4 * n + gg) * 256);
+        io<IO>::store4(out + 32 * n + 8 * gg, x * a.scale);
+      }
+    return;
+  }
   if (!row_ok)
     return;
 #pragma unroll
@@ -190,7 +236,7 @@ __global__ void __launch_bounds__(256, (D * sizeof(IO) <= 256 ? 2 : 1)) gdn2_att
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         x[i] = dq[n][4 * gg + i] * a.scale;
-      io<IO>::store4(static_cast<IO *>(a.dq) + qrow * D + 32 * n + 8 * gg + 4 * h, x);
+      io<IO>::store4(out + 32 * n + 8 * gg, x);
     }
 }
 
@@ -246,7 +292,10 @@ __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1))
     *reinterpret_cast<u32x4 *>(lds + KTB + TL::at(x, sc)) =
         *reinterpret_cast<const u32x4 *>(static_cast<const IO *>(a.v) + off);
   }
-  u32x4 rq[CH], rd[CH];
+  // With two buffers a tile comes straight from memory: position p of it is
+  // chunk (p % CPR) ^ f of row p / CPR.  With one it passes through registers.
+  const int wv = __builtin_amdgcn_readfirstlane(wave);
+  u32x4 rq[NB == 2 ? 1 : CH], rd[NB == 2 ? 1 : CH];
   f32x2 rs = {0.f, 0.f};
   int rp = 0;
   int tok_of[CH];  // token of a thread's row in the tile, and its values' place
@@ -256,7 +305,7 @@ __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1))
     int x = sr0 + RPI * i;
     x = x < nrows ? x : nrows - 1;
     tok_of[i] = x / GS;
-    at_of[i] = static_cast<unsigned>(x % GS * D + sc * TL::VPC);
+    at_of[i] = static_cast<unsigned>(x % GS * D + (NB == 2 ? sc ^ TL::f(sr0 + RPI * i) : sc) * TL::VPC);
   }
   const int my_x = tid < nrows ? tid : nrows - 1, my_tok = my_x / GS, my_g = my_x % GS;
   const bool my_ok = tid < nrows;
@@ -283,8 +332,14 @@ __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1))
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const unsigned off = (tok_of[i] < left ? tok_of[i] : left) * tstep + at_of[i];
-      rq[i] = *reinterpret_cast<const u32x4 *>(qb + off);
-      rd[i] = *reinterpret_cast<const u32x4 *>(db + off);
+      if constexpr (NB == 2) {
+        char *const to = qt + (it & 1) * 2 * TILEB + 1024 * wv + 16 * NT * i;
+        dma16(qb + off, to);
+        dma16(db + off, to + TILEB);
+      } else {
+        rq[i] = *reinterpret_cast<const u32x4 *>(qb + off);
+        rd[i] = *reinterpret_cast<const u32x4 *>(db + off);
+      }
     }
     if (tid < BQ) {
       const bool ok = my_ok && my_tok <= left;
@@ -304,11 +359,15 @@ __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1))
     const int bo = buf * 2 * TILEB;
     if (NB == 1 && it > 0)
       __syncthreads();  // the tile before is read
+    if constexpr (NB == 2) {
+      dma_wait();
+    } else {
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int at = bo + TL::template step<RPI>(st_b, sr0, sc, i);
-      *reinterpret_cast<u32x4 *>(qt + at) = rq[i];
-      *reinterpret_cast<u32x4 *>(dt + at) = rd[i];
+      for (int i = 0; i < CH; ++i) {
+        const int at = TL::template step<RPI>(st_b, sr0, sc, i);
+        *reinterpret_cast<u32x4 *>(qt + at) = rq[i];
+        *reinterpret_cast<u32x4 *>(dt + at) = rd[i];
+      }
     }
     if (tid < BQ) {
       s_lse[buf][tid] = rs[0];
@@ -329,10 +388,29 @@ __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1))
     const int rb = row_b + bo + u0 * TL::ROWB, cb = col_b + bo + u0 * TL::ROWB;
     const int kb = fresh(row_b + 32 * wkey * TL::ROWB);
     f32x16 s = zero16(), dp = zero16();
+    {
+      // operands read a group of products ahead
+      constexpr int GR = 2, NK = D / 16, NG = 2 * NK / GR;
+      frag8<IO> fa[2][GR], fb[2][GR];
+      auto fetch = [&](int g) {
 #pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
-      mma(s, TL::row(qt, rb, kk), TL::row(kt, kb, kk));
-      mma(dp, TL::row(dt, rb, kk), TL::row(vt, kb, kk));
+        for (int x = 0; x < GR; ++x) {
+          const int y = g * GR + x;
+          fa[g & 1][x] = TL::row(y < NK ? qt : dt, rb, y % NK);
+          fb[g & 1][x] = TL::row(y < NK ? kt : vt, kb, y % NK);
+        }
+      };
+      fetch(0);
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        if (g + 1 < NG)
+          fetch(g + 1);
+        group_fence();
+#pragma unroll
+        for (int x = 0; x < GR; ++x)
+          mma(g * GR + x < NK ? s : dp, fa[g & 1][x], fb[g & 1][x]);
+        group_fence();
+      }
     }
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
@@ -475,9 +553,14 @@ template <typename IO, int D>
 hipError_t launch_attn_bwd_dq(const attn_sizes &z, const attn_ptrs &p, void *ws, hipStream_t st) {
   bwd_args a;
   fill(a, z, p, ws);
+  constexpr int KT = sizeof(IO) == 2 ? 2 : 1, WN = sizeof(IO) == 2 ? 4 : 2;
   const unsigned blocks = plan_tiles(z, z.Hq / z.Hk, 128, a.od);
-  constexpr int KT = sizeof(IO) == 2 ? 2 : 1;
-  hipLaunchKernelGGL((gdn2_attn_dq_kernel<IO, D, KT>), dim3(blocks), dim3(256), 0, st, a);
+  if (few_tiles(a.od)) {
+    const unsigned few = plan_tiles(z, z.Hq / z.Hk, 32, a.od);
+    hipLaunchKernelGGL((gdn2_attn_dq_kernel<IO, D, 1, WN, 1>), dim3(few), dim3(64 * WN), 0, st, a);
+  } else {
+    hipLaunchKernelGGL((gdn2_attn_dq_kernel<IO, D, 4, 1, KT>), dim3(blocks), dim3(256), 0, st, a);
+  }
   return hipGetLastError();
 }
 template <typename IO, int D>

@@ -110,6 +110,9 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
   // Tiles under way from memory: a wave of its own stages little of e4m3
   // (8 KB a tile), so it keeps two.
   constexpr int DEPTH = !SHARED && F8 ? 2 : 1;
+  // Whole sequences' tiles come straight from memory: position p of a tile is
+  // chunk (p % CPR) ^ f of row p / CPR.
+  constexpr bool DMA = SHARED && !PAGED;
   static_assert(SN * CPR % NT == 0 && NT % CPR == 0, "staging split");
   constexpr int ROWS_PER_I = NT / CPR;
   // K and V tiles; with split keys also the room in which the waves join
@@ -207,7 +210,8 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
   const int row_b = TL::row_base(r, h) + wave_b, col_b = TL::col_base(lane) + wave_b;
   char *const kt = lds, *const vt = lds + TILEB;
   float *const kscale = scales + wn * 2 * SN, *const vscale = kscale + SN;
-  typename CS::raw rk[DEPTH][CH], rv[DEPTH][CH];
+  const int wv = __builtin_amdgcn_readfirstlane(wave);
+  typename CS::raw rk[DEPTH][DMA ? 1 : CH], rv[DEPTH][DMA ? 1 : CH];
   int ent[CH];
   uint8_t bk[DEPTH], bv[DEPTH];
   int ent_b = 0;
@@ -247,9 +251,16 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
         if (!ok)
           rk[set][i] = rv[set][i] = CS::zero();
       } else {
-        const unsigned off = static_cast<unsigned>(j - kb) * kstep + sc * TL::VPC;
-        rk[set][i] = CS::load(kp + off);
-        rv[set][i] = CS::load(vp + off);
+        if constexpr (DMA) {
+          const unsigned off = static_cast<unsigned>(j - kb) * kstep + (sc ^ TL::f(sr0 + ROWS_PER_I * i)) * TL::VPC;
+          char *const to = lds + (set * 2 * TILEB + 1024 * wv + 16 * NT * i);
+          dma16(kp + off, to);
+          dma16(vp + off, to + TILEB);
+        } else {
+          const unsigned off = static_cast<unsigned>(j - kb) * kstep + sc * TL::VPC;
+          rk[set][i] = CS::load(kp + off);
+          rv[set][i] = CS::load(vp + off);
+        }
       }
     }
     if constexpr (F8) {
@@ -262,8 +273,10 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
     }
   };
   auto store_tile = [&](int buf, int set) {
+    if constexpr (DMA)
+      return;
 #pragma unroll
-    for (int i = 0; i < CH; ++i)
+    for (int i = 0; i < (DMA ? 1 : CH); ++i)
 #pragma unroll
       for (int x = 0; x < RPC; ++x) {
         const int at = wave_b + buf * 2 * TILEB + TL::at(st / CPR + ROWS_PER_I * i, RPC * sc + x);
@@ -286,7 +299,10 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
 
   auto tile_step = [&](int it, auto set) {
     const int kb = k0 + it * BN, buf = SHARED ? it & 1 : 0;
-    if constexpr (SHARED) {
+    if constexpr (DMA) {
+      dma_wait();
+      __syncthreads();
+    } else if constexpr (SHARED) {
       store_tile(buf, set);
       __syncthreads();
     } else {
@@ -297,7 +313,7 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
       wave_order();
     }
     if (it + DEPTH < ntiles) {
-      load_tile(kb + DEPTH * BN, set);
+      load_tile(kb + DEPTH * BN, DMA ? buf ^ 1 : static_cast<int>(set));
       load_entries(kb + (DEPTH + 1) * BN);
     }
     const int rb = row_b + buf * 2 * TILEB, cb = col_b + buf * 2 * TILEB;
@@ -654,8 +670,9 @@ static void fill(fwd_args &a, const attn_sizes &z, const attn_ptrs &p) {
 template <typename IO, int D> hipError_t launch_attn_fwd(const attn_sizes &z, const attn_ptrs &p, hipStream_t st) {
   fwd_args a;
   fill(a, z, p);
-  constexpr int KT = sizeof(IO) == 2 ? 2 : 1;
-  return go<IO, IO, D, 4, 1, KT, false>(a, z, st);
+  constexpr int KT = sizeof(IO) == 2 ? 2 : 1, WN = sizeof(IO) == 2 ? 4 : 2;
+  plan_tiles(z, a.G, 128, a.od);
+  return few_tiles(a.od) ? go<IO, IO, D, 1, WN, 1, false>(a, z, st) : go<IO, IO, D, 4, 1, KT, false>(a, z, st);
 }
 
 template <typename IO, typename CT, int D>
