@@ -25,33 +25,43 @@ import math
 
 import torch
 
-from . import GDN2_BF16, GDN2_F32, _check, _dtype_code, _ptr, _require, lib
+from . import GDN2_BF16, GDN2_F32, _check, _dtype_code, _ptr, lib
 
 GDN2_F8E4M3 = 2
 ROPE_INTERLEAVED = 1 << 0
 ROPE_NO_NORM = 1 << 1
 
 
-def _device(first: torch.Tensor, *others) -> torch.device:
-    """The one device of a call's tensors, all of them contiguous on it."""
-    dev = first.device
-    for t in (first, *others):
-        if t is None:
-            continue
-        if not t.is_cuda or not t.is_contiguous():
-            raise ValueError("libgdn2 takes contiguous device tensors")
-        if t.device != dev:
-            raise ValueError(f"tensors on different devices ({dev} and {t.device})")
+def _device(*tensors) -> int:
+    """The index of the one GPU that holds a call's tensors, all contiguous."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and (t.get_device() != dev or dev < 0 or not t.is_contiguous()):
+            if not t.is_cuda or not t.is_contiguous():
+                raise ValueError("libgdn2 takes contiguous device tensors")
+            raise ValueError(f"tensors on different devices ({tensors[0].device} and {t.device})")
     return dev
 
 
-def _call(dev: torch.device, fn, *args) -> None:
+def _like(t, name: str, shape, dtype) -> None:
+    """A tensor of a call (``_device`` has seen it) of this shape and dtype."""
+    if t is None:
+        return
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}, not {list(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+
+
+def _call(dev: int, fn, *args) -> None:
     """fn(*args, stream) on the device's current stream, whatever device is current."""
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+    if dev == torch.cuda.current_device():
+        status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if status:
+        _check(status)
 
 
 def _heads(q, k, *like_k) -> tuple:
@@ -59,9 +69,9 @@ def _heads(q, k, *like_k) -> tuple:
         raise ValueError("q and k must be [B, T, H, d]")
     B, T, Hq, d = q.shape
     Hk = k.shape[2]
-    _require(k, "k", (B, T, Hk, d), q.dtype)
+    _like(k, "k", (B, T, Hk, d), q.dtype)
     for t, name in like_k:
-        _require(t, name, (B, T, Hk, d), q.dtype)
+        _like(t, name, (B, T, Hk, d), q.dtype)
     return B, T, Hq, Hk, d
 
 
@@ -76,13 +86,13 @@ def _packed(cu_seqlens, B) -> int:
     return cu_seqlens.numel() - 1
 
 
-def _workspace(ws, need: int, dev: torch.device):
+def _workspace(ws, need: int, dev: int):
     """(tensor or None, bytes) of a given workspace, or of a new one."""
     if ws is None:
         if need == 0:
             return None, 0
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif not ws.is_cuda or not ws.is_contiguous() or ws.device != dev:
+    elif ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the call's device")
     return ws, ws.numel() * ws.element_size()
 
@@ -125,9 +135,9 @@ def rope_frequencies(rotary_dim: int, theta: float = 10000.0, scaling: str | Non
 
 def _rope_args(q, k, freqs, wq, wk, positions, interleaved, norm):
     B, T, Hq, Hk, d = _heads(q, k)
-    _require(wq, "wq", (d,), torch.float32)
-    _require(wk, "wk", (d,), torch.float32)
-    _require(positions, "positions", (B, T), torch.int32)
+    _like(wq, "wq", (d,), torch.float32)
+    _like(wk, "wk", (d,), torch.float32)
+    _like(positions, "positions", (B, T), torch.int32)
     rot = 0
     if freqs is not None:
         if freqs.dtype != torch.float64 or freqs.dim() != 1:
@@ -151,8 +161,8 @@ def qk_norm_rope(q, k, freqs, wq=None, wk=None, positions=None, interleaved: boo
         out = torch.empty_like(q), torch.empty_like(k)
     else:
         _device(q, *out)
-        _require(out[0], "out[0]", tuple(q.shape), q.dtype)
-        _require(out[1], "out[1]", tuple(k.shape), q.dtype)
+        _like(out[0], "out[0]", q.shape, q.dtype)
+        _like(out[1], "out[1]", k.shape, q.dtype)
     _call(dev, lib().gdn2_qk_norm_rope_fwd, _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(freqs), _ptr(positions), B, T,
           Hq, Hk, d, rot, eps, _dtype_code(q), flags, _ptr(out[0]), _ptr(out[1]))
     return out[0], out[1]
@@ -166,19 +176,19 @@ def qk_norm_rope_bwd(q, k, freqs, dq_out, dk_out, wq=None, wk=None, positions=No
     hold preallocated tensors under those names."""
     dev = _device(q, k, freqs, dq_out, dk_out, wq, wk, positions)
     B, T, Hq, Hk, d, rot, flags = _rope_args(q, k, freqs, wq, wk, positions, interleaved, norm)
-    _require(dq_out, "dq_out", tuple(q.shape), q.dtype)
-    _require(dk_out, "dk_out", tuple(k.shape), q.dtype)
+    _like(dq_out, "dq_out", q.shape, q.dtype)
+    _like(dk_out, "dk_out", k.shape, q.dtype)
     out = dict(out or {})
     for name, like in (("dq", q), ("dk", k)):
         if name not in out:
             out[name] = torch.empty_like(like)
-        _require(out[name], name, tuple(like.shape), q.dtype)
+        _like(out[name], name, like.shape, q.dtype)
     need = 0
     if norm:
         for name in ("dwq", "dwk"):
             if name not in out:
                 out[name] = torch.empty(d, dtype=torch.float32, device=dev)
-            _require(out[name], name, (d,), torch.float32)
+            _like(out[name], name, (d,), torch.float32)
         need = int(lib().gdn2_qk_norm_rope_bwd_workspace_bytes(B, T, Hq, Hk, d))
     _device(q, *out.values())
     ws, ws_bytes = _workspace(workspace, need, dev)
@@ -203,8 +213,8 @@ def attn_fwd(q, k, v, cu_seqlens=None, window: int = 0, scale: float | None = No
     if lse is None and want_lse:
         lse = torch.empty((B, T, Hq), dtype=torch.float32, device=dev)
     _device(q, out, lse)
-    _require(out, "out", tuple(q.shape), q.dtype)
-    _require(lse, "lse", (B, T, Hq), torch.float32)
+    _like(out, "out", q.shape, q.dtype)
+    _like(lse, "lse", (B, T, Hq), torch.float32)
     _call(dev, lib().gdn2_attn_fwd, _ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), B, T, Hq, Hk, d, ns, window,
           d ** -0.5 if scale is None else scale, _dtype_code(q), _ptr(out), _ptr(lse))
     return out, lse
@@ -222,14 +232,14 @@ def attn_bwd(q, k, v, o, lse, dout, cu_seqlens=None, window: int = 0, scale: flo
     dev = _device(q, k, v, o, lse, dout, cu_seqlens)
     B, T, Hq, Hk, d = _heads(q, k, (v, "v"))
     ns = _packed(cu_seqlens, B)
-    _require(o, "o", tuple(q.shape), q.dtype)
-    _require(dout, "dout", tuple(q.shape), q.dtype)
-    _require(lse, "lse", (B, T, Hq), torch.float32)
+    _like(o, "o", q.shape, q.dtype)
+    _like(dout, "dout", q.shape, q.dtype)
+    _like(lse, "lse", (B, T, Hq), torch.float32)
     out = dict(out or {})
     for name, like in (("dq", q), ("dk", k), ("dv", v)):
         if name not in out:
             out[name] = torch.empty_like(like)
-        _require(out[name], name, tuple(like.shape), q.dtype)
+        _like(out[name], name, like.shape, q.dtype)
     _device(q, *out.values())
     ws, ws_bytes = _workspace(workspace, attn_bwd_workspace_bytes(B, T, Hq, Hk, d), dev)
     _call(dev, lib().gdn2_attn_bwd, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(cu_seqlens), B, T,
@@ -245,13 +255,13 @@ def _cache(k_cache, v_cache, k_scale, v_scale, dtype) -> tuple:
         raise ValueError("caches must be [pages, Hk, page size, d]")
     if k_cache.dtype not in (dtype, torch.float8_e4m3fn):
         raise TypeError(f"a cache of {k_cache.dtype} does not go with {dtype} (its own dtype or torch.float8_e4m3fn)")
-    _require(v_cache, "v_cache", tuple(k_cache.shape), k_cache.dtype)
+    _like(v_cache, "v_cache", k_cache.shape, k_cache.dtype)
     P, Hk, page, d = k_cache.shape
     f8 = k_cache.dtype == torch.float8_e4m3fn
     for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
         if f8 != (t is not None):
             raise ValueError(f"{name} goes with a torch.float8_e4m3fn cache")
-        _require(t, name, (P, Hk, page), torch.uint8)
+        _like(t, name, (P, Hk, page), torch.uint8)
     code = GDN2_F8E4M3 if f8 else (GDN2_BF16 if dtype == torch.bfloat16 else GDN2_F32)
     return P, Hk, page, d, code
 
@@ -269,7 +279,7 @@ def kv_cache_write(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None) ->
         raise TypeError("slots must be int64")
     if k.dim() < 2 or tuple(k.shape[-2:]) != (Hk, d) or k.numel() != n * Hk * d:
         raise ValueError(f"k must hold {n} tokens of [{Hk}, {d}]")
-    _require(v, "v", tuple(k.shape), k.dtype)
+    _like(v, "v", k.shape, k.dtype)
     _call(dev, lib().gdn2_kv_cache_write, _ptr(k), _ptr(v), _ptr(slots), n, Hk, d, P, page, dt, code, _ptr(k_cache),
           _ptr(v_cache), _ptr(k_scale), _ptr(v_scale))
 
@@ -289,8 +299,8 @@ def kv_cache_read(slots, k_cache, v_cache, k_scale=None, v_scale=None, dtype=Non
     if out is None:
         out = tuple(torch.empty((n, Hk, d), dtype=dtype, device=dev) for _ in range(2))
     _device(slots, *out)
-    _require(out[0], "out[0]", (n, Hk, d), dtype)
-    _require(out[1], "out[1]", (n, Hk, d), dtype)
+    _like(out[0], "out[0]", (n, Hk, d), dtype)
+    _like(out[1], "out[1]", (n, Hk, d), dtype)
     _call(dev, lib().gdn2_kv_cache_read, _ptr(slots), n, Hk, d, P, page, _dtype_code(out[0]), code, _ptr(k_cache),
           _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(out[0]), _ptr(out[1]))
     return out[0], out[1]
@@ -325,15 +335,15 @@ def attn_paged(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens=None, k_sc
     N = ns if ns else B
     if block_table.dim() != 2:
         raise ValueError("block_table must be [N, max pages]")
-    _require(block_table, "block_table", (N, block_table.shape[1]), torch.int32)
-    _require(seq_lens, "seq_lens", (N,), torch.int32)
+    _like(block_table, "block_table", (N, block_table.shape[1]), torch.int32)
+    _like(seq_lens, "seq_lens", (N,), torch.int32)
     if out is None:
         out = torch.empty_like(q)
     if lse is None and want_lse:
         lse = torch.empty((B, T, Hq), dtype=torch.float32, device=dev)
     _device(q, out, lse)
-    _require(out, "out", tuple(q.shape), q.dtype)
-    _require(lse, "lse", (B, T, Hq), torch.float32)
+    _like(out, "out", q.shape, q.dtype)
+    _like(lse, "lse", (B, T, Hq), torch.float32)
     mp = block_table.shape[1]
     need = 0
     if workspace is None:

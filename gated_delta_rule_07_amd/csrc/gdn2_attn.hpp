@@ -213,40 +213,56 @@ __device__ __forceinline__ void dma16(const void *src, char *lds) {
 }
 __device__ __forceinline__ void dma_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
-// What a thread stages at once of a cache's rows (element type CT) into a
-// tile of IO: N chunks of 16 bytes of the tile.  e4m3 codes become the values
-// they stand for (the row's scale is applied to the scores and weights, in
-// float32), which both formats hold exactly.
-template <typename IO, typename CT> struct chunk_src {
-  typedef u32x4 raw;
-  static constexpr int N = 1;
-  __device__ static __forceinline__ raw load(const CT *p) { return *reinterpret_cast<const u32x4 *>(p); }
-  __device__ static __forceinline__ raw zero() { return u32x4{0u, 0u, 0u, 0u}; }
-  __device__ static __forceinline__ u32x4 widen(raw x, int) { return x; }
-};
-template <> struct chunk_src<bf16_t, f8_t> {
-  typedef u32x4 raw;
-  static constexpr int N = 2;
-  __device__ static __forceinline__ raw load(const f8_t *p) { return *reinterpret_cast<const u32x4 *>(p); }
-  __device__ static __forceinline__ raw zero() { return u32x4{0u, 0u, 0u, 0u}; }
-  __device__ static __forceinline__ u32x4 widen(raw x, int i) {
-    u32x4 y;
-    y[0] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * i], 1.0f, false));
-    y[1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * i], 1.0f, true));
-    y[2] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * i + 1], 1.0f, false));
-    y[3] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[2 * i + 1], 1.0f, true));
-    return y;
+// 8 e4m3 codes as an operand: the values they stand for (the row's scale is
+// applied to the scores and weights, in float32), which both formats hold
+// exactly.
+template <typename T> __device__ __forceinline__ frag8<T> widen8(u32x2 x);
+template <> __device__ __forceinline__ frag8<bf16_t> widen8<bf16_t>(u32x2 x) {
+  u32x4 y;
+  y[0] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[0], 1.0f, false));
+  y[1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[0], 1.0f, true));
+  y[2] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[1], 1.0f, false));
+  y[3] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[1], 1.0f, true));
+  frag8<bf16_t> f;
+  f.v = __builtin_bit_cast(bf16x8, y);
+  return f;
+}
+template <> __device__ __forceinline__ frag8<float> widen8<float>(u32x2 x) {
+  const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(x[0], false), b = __builtin_amdgcn_cvt_pk_f32_fp8(x[0], true);
+  const f32x2 c = __builtin_amdgcn_cvt_pk_f32_fp8(x[1], false), d = __builtin_amdgcn_cvt_pk_f32_fp8(x[1], true);
+  frag8<float> f;
+  f.lo = f32x4{a[0], a[1], b[0], b[1]};
+  f.hi = f32x4{c[0], c[1], d[0], d[1]};
+  return f;
+}
+
+// A tile of rows of D e4m3 codes, read as operands of T; laid out and read
+// like the tile above (chunks of 16 codes).
+template <typename T, int D> struct tile8 {
+  static constexpr int ROWB = D, CPR = D / 16, VPC = 16;
+  __device__ static __forceinline__ int f(int r) { return D == 128 ? (r >> 1) & 7 : (r >> 2) & 3; }
+  __device__ static __forceinline__ int at(int r, int c) { return r * ROWB + ((c ^ f(r)) << 4); }
+  __device__ static __forceinline__ int row_base(int r, int h) { return r * ROWB + (f(r) << 4) + 8 * h; }
+  __device__ static __forceinline__ frag8<T> row(const char *t, int base, int kk) {
+    return widen8<T>(*reinterpret_cast<const u32x2 *>(t + (base ^ (kk << 4))));
   }
-};
-template <> struct chunk_src<float, f8_t> {
-  typedef unsigned raw;
-  static constexpr int N = 1;
-  __device__ static __forceinline__ raw load(const f8_t *p) { return *reinterpret_cast<const unsigned *>(p); }
-  __device__ static __forceinline__ raw zero() { return 0u; }
-  __device__ static __forceinline__ u32x4 widen(raw x, int) {
-    const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(x, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(x, true);
-    const f32x4 y = {a[0], a[1], b[0], b[1]};
-    return __builtin_bit_cast(u32x4, y);
+  // a transposing read hands lane i of 16 the codes of column i of an 8 x 16
+  // block whose row j / 2, codes 8 (j % 2) .. + 7 lane j points at; the
+  // block's rows are the tile's in acc order
+  __device__ static __forceinline__ int col_base(int lane) {
+    const int h = lane >> 5, j = lane & 15, ch = (lane >> 4) & 1, e = j >> 1, ra = 8 * (e >> 2) + 4 * h + (e & 3);
+    return ra * ROWB + ((ch ^ f(ra)) << 4) + ((j & 1) << 3);
+  }
+  __device__ static __forceinline__ frag8<T> col(const char *t, int base, int r0, int n) {
+    // (f has period 16 in the row: r0 is a multiple of 16)
+    typedef __attribute__((ext_vector_type(2))) int i32x2;
+    typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
+    return widen8<T>(__builtin_bit_cast(
+        u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2 *)(t + r0 * ROWB + (base ^ (n << 5))))));
+  }
+  __device__ static __forceinline__ float one(const char *t, int r, int ch) {
+    const unsigned code = *reinterpret_cast<const uint8_t *>(t + at(r, ch >> 4) + (ch & 15));
+    return __builtin_amdgcn_cvt_f32_fp8(code, 0);
   }
 };
 

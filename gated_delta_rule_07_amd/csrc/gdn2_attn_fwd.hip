@@ -97,26 +97,23 @@ template <typename IO, typename CT, int D, int WM, int WN, int KT, bool PAGED>
 __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
     gdn2_attn_fwd_kernel(fwd_args a) {
   typedef tile<IO, D> TL;
-  typedef chunk_src<IO, CT> CS;
+  typedef typename std::conditional<sizeof(CT) == 1, tile8<IO, D>, TL>::type KV;  // a tile of the cache's own type
   // SHARED: the workgroup's waves share a tile, double-buffered, with one
   // barrier a tile.  Else every wave stages the keys it alone reads (single
   // buffer, no barrier: a wave's LDS accesses stay in order).
   constexpr bool SHARED = WN == 1;
   constexpr int NT = SHARED ? 64 * WM : 64, BM = 32 * WM, BN = 32 * KT * WN, SN = 32 * KT, NB = SHARED ? 2 : 1;
-  constexpr int RPC = CS::N, CPR = TL::CPR / RPC;  // loads per row
-  constexpr int CH = SN * CPR / NT;                 // loads a thread stages of K (and of V)
-  constexpr int TILEB = SN * TL::ROWB;
+  constexpr int CPR = KV::CPR, CH = SN * CPR / NT;  // 16-byte chunks a thread stages of K (and of V)
+  constexpr int TILEB = SN * KV::ROWB;
   constexpr bool F8 = sizeof(CT) == 1;
-  // Tiles under way from memory: a wave of its own stages little of e4m3
-  // (8 KB a tile), so it keeps two.
-  constexpr int DEPTH = !SHARED && F8 ? 2 : 1;
   // Whole sequences' tiles come straight from memory: position p of a tile is
   // chunk (p % CPR) ^ f of row p / CPR.
   constexpr bool DMA = SHARED && !PAGED;
   static_assert(SN * CPR % NT == 0 && NT % CPR == 0, "staging split");
   constexpr int ROWS_PER_I = NT / CPR;
   // K and V tiles; with split keys also the room in which the waves join
-  constexpr int JOIN = SHARED ? 0 : WN * 32 * ((D + 4) * 4 + 8);
+  // (a part of JC channels at a time)
+  constexpr int JC = 64, JOIN = SHARED ? 0 : WN * 32 * ((JC + 4) * 4 + 8);
   constexpr int LDSB = 2 * NB * WN * TILEB > JOIN ? 2 * NB * WN * TILEB : JOIN;
   __shared__ __align__(16) char lds[LDSB];
   // waves of their own keep the queries, the same for all of them, here
@@ -207,13 +204,13 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
   const int st = SHARED ? tid : lane;
   const int sc = st % CPR, sr0 = st / CPR + (SHARED ? 0 : SN * wn);
   const int wave_b = wn * 2 * TILEB;  // the wave's tiles
-  const int row_b = TL::row_base(r, h) + wave_b, col_b = TL::col_base(lane) + wave_b;
+  const int row_b = KV::row_base(r, h) + wave_b, col_b = KV::col_base(lane) + wave_b;
   char *const kt = lds, *const vt = lds + TILEB;
   float *const kscale = scales + wn * 2 * SN, *const vscale = kscale + SN;
   const int wv = __builtin_amdgcn_readfirstlane(wave);
-  typename CS::raw rk[DEPTH][DMA ? 1 : CH], rv[DEPTH][DMA ? 1 : CH];
+  u32x4 rk[DMA ? 1 : CH], rv[DMA ? 1 : CH];
   int ent[CH];
-  uint8_t bk[DEPTH], bv[DEPTH];
+  uint8_t bk = 127, bv = 127;
   int ent_b = 0;
   const int32_t *table = PAGED ? a.table + static_cast<size_t>(sq.n) * a.max_pages : nullptr;
   const int pmask = (1 << a.page_shift) - 1;
@@ -234,7 +231,7 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
     }
   };
   const unsigned kstep = static_cast<unsigned>(a.Hk) * D;  // values of a token
-  auto load_tile = [&](int kb, int set) {
+  auto load_tile = [&](int kb, int buf) {
     const size_t base = PAGED ? 0 : (static_cast<size_t>(sq.start + kb) * a.Hk + hk) * D;
     const CT *const kp = static_cast<const CT *>(a.k) + base, *const vp = static_cast<const CT *>(a.v) + base;
 #pragma unroll
@@ -245,21 +242,21 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
         // an entry outside the cache stands for zeros
         const bool ok = static_cast<unsigned>(ent[i]) < static_cast<unsigned>(a.num_pages);
         const size_t off = (((static_cast<size_t>(ok ? ent[i] : 0) * a.Hk + hk) << a.page_shift) + (j & pmask)) * D +
-                           sc * (RPC * TL::VPC);
-        rk[set][i] = CS::load(kp + off);
-        rv[set][i] = CS::load(vp + off);
+                           sc * KV::VPC;
+        rk[i] = *reinterpret_cast<const u32x4 *>(kp + off);
+        rv[i] = *reinterpret_cast<const u32x4 *>(vp + off);
         if (!ok)
-          rk[set][i] = rv[set][i] = CS::zero();
+          rk[i] = rv[i] = u32x4{0u, 0u, 0u, 0u};
       } else {
         if constexpr (DMA) {
-          const unsigned off = static_cast<unsigned>(j - kb) * kstep + (sc ^ TL::f(sr0 + ROWS_PER_I * i)) * TL::VPC;
-          char *const to = lds + (set * 2 * TILEB + 1024 * wv + 16 * NT * i);
+          const unsigned off = static_cast<unsigned>(j - kb) * kstep + (sc ^ KV::f(sr0 + ROWS_PER_I * i)) * KV::VPC;
+          char *const to = lds + (buf * 2 * TILEB + 1024 * wv + 16 * NT * i);
           dma16(kp + off, to);
           dma16(vp + off, to + TILEB);
         } else {
-          const unsigned off = static_cast<unsigned>(j - kb) * kstep + sc * TL::VPC;
-          rk[set][i] = CS::load(kp + off);
-          rv[set][i] = CS::load(vp + off);
+          const unsigned off = static_cast<unsigned>(j - kb) * kstep + sc * KV::VPC;
+          rk[i] = *reinterpret_cast<const u32x4 *>(kp + off);
+          rv[i] = *reinterpret_cast<const u32x4 *>(vp + off);
         }
       }
     }
@@ -268,25 +265,23 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
       j = j < k1 ? j : k1 - 1;
       const bool ok = static_cast<unsigned>(ent_b) < static_cast<unsigned>(a.num_pages);
       const size_t off = ((static_cast<size_t>(ok ? ent_b : 0) * a.Hk + hk) << a.page_shift) + (j & pmask);
-      bk[set] = a.ks[off];
-      bv[set] = a.vs[off];
+      bk = a.ks[off];
+      bv = a.vs[off];
     }
   };
-  auto store_tile = [&](int buf, int set) {
+  auto store_tile = [&](int buf) {
     if constexpr (DMA)
       return;
 #pragma unroll
-    for (int i = 0; i < (DMA ? 1 : CH); ++i)
-#pragma unroll
-      for (int x = 0; x < RPC; ++x) {
-        const int at = wave_b + buf * 2 * TILEB + TL::at(st / CPR + ROWS_PER_I * i, RPC * sc + x);
-        *reinterpret_cast<u32x4 *>(kt + at) = CS::widen(rk[set][i], x);
-        *reinterpret_cast<u32x4 *>(vt + at) = CS::widen(rv[set][i], x);
-      }
+    for (int i = 0; i < (DMA ? 1 : CH); ++i) {
+      const int at = wave_b + buf * 2 * TILEB + KV::at(st / CPR + ROWS_PER_I * i, sc);
+      *reinterpret_cast<u32x4 *>(kt + at) = rk[i];
+      *reinterpret_cast<u32x4 *>(vt + at) = rv[i];
+    }
     if constexpr (F8) {
       if (st < SN) {
-        kscale[buf * 2 * SN + st] = scale_of(bk[set]);
-        vscale[buf * 2 * SN + st] = scale_of(bv[set]);
+        kscale[buf * 2 * SN + st] = scale_of(bk);
+        vscale[buf * 2 * SN + st] = scale_of(bv);
       }
     }
   };
@@ -297,31 +292,36 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
     o[n] = zero16();
   float m = neg_inf(), l = 0.f;  // l: this half's part of the sum
 
-  auto tile_step = [&](int it, auto set) {
+  if (ntiles > 0) {
+    load_entries(k0);
+    load_tile(k0, 0);
+    load_entries(k0 + BN);
+  }
+  for (int it = 0; it < ntiles; ++it) {
     const int kb = k0 + it * BN, buf = SHARED ? it & 1 : 0;
     if constexpr (DMA) {
       dma_wait();
       __syncthreads();
     } else if constexpr (SHARED) {
-      store_tile(buf, set);
+      store_tile(buf);
       __syncthreads();
     } else {
       // the lanes' reads of the tile before come first, their writes before
       // the reads below
       wave_order();
-      store_tile(buf, set);
+      store_tile(buf);
       wave_order();
     }
-    if (it + DEPTH < ntiles) {
-      load_tile(kb + DEPTH * BN, DMA ? buf ^ 1 : static_cast<int>(set));
-      load_entries(kb + (DEPTH + 1) * BN);
+    if (it + 1 < ntiles) {
+      load_tile(kb + BN, buf ^ 1);
+      load_entries(kb + 2 * BN);
     }
     const int rb = row_b + buf * 2 * TILEB, cb = col_b + buf * 2 * TILEB;
     const float *const ksc = kscale + buf * 2 * SN, *const vsc = vscale + buf * 2 * SN;
     const int wk = kb + SN * wn;  // the wave's first key
     // no rows, or nothing of the tile is visible to the wave
     if (row0 + 32 * wm >= rows || wk > pos_hi || wk >= k1 || (a.window > 0 && wk + 32 * KT - 1 <= pos_lo - a.window))
-      return;
+      continue;
     const bool masked = wk + 32 * KT - 1 > pos_lo || wk + 32 * KT > k1 ||
                         (a.window > 0 && wk <= pos_hi - a.window);
 
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
           const int y = g * GR + x;
           if constexpr (!SHARED)
             qf[g & 1][x] = TL::row(lq, qb, y % (D / 16));
-          kf[g & 1][x] = TL::row(kt + 32 * (y / (D / 16)) * TL::ROWB, rb, y % (D / 16));
+          kf[g & 1][x] = KV::row(kt + 32 * (y / (D / 16)) * KV::ROWB, rb, y % (D / 16));
         }
       };
       fetch(0);
@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
       auto fetch = [&](int g) {
 #pragma unroll
         for (int x = 0; x < GV; ++x)
-          vf[g & 1][x] = TL::col(vt, cb, 16 * (g / PER), g % PER * GV + x);
+          vf[g & 1][x] = KV::col(vt, cb, 16 * (g / PER), g % PER * GV + x);
       };
       fetch(0);
 #pragma unroll
@@ -474,27 +474,11 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
         for (int n = 0; n < D / 32; ++n)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float x = TL::one(vt + wave_b + buf * 2 * TILEB, j, 32 * n + 8 * (i >> 2) + 4 * h + (i & 3));
+            const float x = KV::one(vt + wave_b + buf * 2 * TILEB, j, 32 * n + 8 * (i >> 2) + 4 * h + (i & 3));
             if (vis && !(fabsf(x) <= 3.4028234663852886e38f))
               o[n][i] += p * x;
           }
       }
-    }
-  };
-  if (ntiles > 0) {
-    load_entries(k0);
-#pragma unroll
-    for (int x = 0; x < DEPTH; ++x)
-      if (x == 0 || x < ntiles) {
-        load_tile(k0 + x * BN, x);
-        load_entries(k0 + (x + 1) * BN);
-      }
-  }
-  for (int it = 0; it < ntiles; it += DEPTH) {
-    tile_step(it, std::integral_constant<int, 0>());
-    if constexpr (DEPTH == 2) {
-      if (it + 1 < ntiles)
-        tile_step(it + 1, std::integral_constant<int, 1>());
     }
   }
 
@@ -503,8 +487,8 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
   if constexpr (WN > 1) {
     // join the waves' parts: weights 2^(m_w - M)
     static_assert(WM == 1, "one row block");
-    constexpr int OLD = D + 4;
-    float *jo = reinterpret_cast<float *>(lds);                 // [WN][32][OLD]
+    constexpr int OLD = JC + 4;
+    float *jo = reinterpret_cast<float *>(lds);  // [WN][32][OLD]
     float *jm = jo + WN * 32 * OLD, *jl = jm + WN * 32;
     __syncthreads();
     if (h == 0) {
@@ -523,30 +507,31 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
       L += jl[w * 32 + r] * fast_exp2(jm[w * 32 + r] - base);
     const float f = fast_exp2(m - base);
 #pragma unroll
-    for (int n = 0; n < D / 32; ++n)
+    for (int n0 = 0; n0 < D / 32; n0 += JC / 32) {
+      if (n0 > 0)
+        __syncthreads();
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        f32x4 x;
+      for (int n = 0; n < JC / 32; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          x[i] = o[n][4 * g + i] * f;
-        *reinterpret_cast<f32x4 *>(&jo[(wn * 32 + r) * OLD + 32 * n + 8 * g + 4 * h]) = x;
-      }
-    __syncthreads();
-    // wave w sums the waves' parts of channel block w of every row
-    m = M;
-    l = L;
-    for (int n = wn; n < D / 32; n += WN)
+        for (int g = 0; g < 4; ++g) {
+          f32x4 x;
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
+          for (int i = 0; i < 4; ++i)
+            x[i] = o[n0 + n][4 * g + i] * f;
+          *reinterpret_cast<f32x4 *>(&jo[(wn * 32 + r) * OLD + 32 * n + 8 * g + 4 * h]) = x;
+        }
+      __syncthreads();
+      // the waves take the part's groups of 8 channels of every row in turn
+      for (int y = wn; y < JC / 8; y += WN) {
         f32x4 x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < WN; ++w)
-          x += *reinterpret_cast<const f32x4 *>(&jo[(w * 32 + r) * OLD + 32 * n + 8 * g + 4 * h]);
-        store_row<IO, D>(a, x, l, qrow, split, row_ok, 32 * n + 8 * g + 4 * h);
+          x += *reinterpret_cast<const f32x4 *>(&jo[(w * 32 + r) * OLD + 8 * y + 4 * h]);
+        store_row<IO, D>(a, x, L, qrow, split, row_ok, 32 * n0 + 8 * y + 4 * h);
       }
+    }
     if (wn == 0 && h == 0 && row_ok)
-      store_lse(a, m, l, qrow, split);
+      store_lse(a, M, L, qrow, split);
   } else {
 #pragma unroll
     for (int n = 0; n < D / 32; ++n)
@@ -680,7 +665,7 @@ hipError_t launch_attn_paged(const attn_sizes &z, const attn_ptrs &p, int splits
   fwd_args a;
   fill(a, z, p);
   a.splits = splits;
-  constexpr int KT = sizeof(IO) == 2 ? 2 : 1;
+  constexpr int KT = sizeof(CT) <= 2 ? 2 : 1;
   if (splits > 1) {
     const size_t rows = static_cast<size_t>(z.Ttot) * z.Hq;
     a.part_o = static_cast<float *>(ws);

@@ -243,25 +243,32 @@ template <typename IO, int D> __global__ void __launch_bounds__(256) gdn2_rope_b
   }
 }
 
-// dw[i] = sum over the workgroups' parts: 16 channels a workgroup, 16
-// threads a channel, joined in a fixed order.
+// dw[i] = sum over the workgroups' parts: 16 channels a workgroup, 64 threads
+// a channel with up to 16 loads under way each, joined in a fixed order.
 template <int D>
-__global__ void __launch_bounds__(256) gdn2_rope_dw_kernel(const float *part, int parts, float *dwq, float *dwk) {
-  __shared__ float red[16][16];
+__global__ void __launch_bounds__(1024) gdn2_rope_dw_kernel(const float *part, int parts, float *dwq, float *dwk) {
+  __shared__ float red[64][17];
   const int col = threadIdx.x & 15, g = threadIdx.x >> 4, i = blockIdx.x * 16 + col;
-  float x = 0.f;
-  for (int p = g; p < parts; p += 16)
-    x += part[static_cast<size_t>(p) * 2 * D + i];
-  red[g][col] = x;
-  __syncthreads();
-  if (g == 0) {
-    float y = 0.f;
+  float x[16];
 #pragma unroll
-    for (int w = 0; w < 16; ++w)
-      y += red[w][col];
+  for (int p = 0; p < 16; ++p)
+    x[p] = g + 64 * p < parts ? part[static_cast<size_t>(g + 64 * p) * 2 * D + i] : 0.f;
+#pragma unroll
+  for (int s = 8; s > 0; s >>= 1)
+#pragma unroll
+    for (int p = 0; p < s; ++p)
+      x[p] += x[p + s];
+  red[g][col] = x[0];
+  __syncthreads();
+  for (int s = 32; s > 0; s >>= 1) {
+    if (g < s)
+      red[g][col] += red[g + s][col];
+    __syncthreads();
+  }
+  if (g == 0) {
     float *dst = i < D ? dwq : dwk;
     if (dst)
-      dst[i % D] = y;
+      dst[i % D] = red[0][col];
   }
 }
 
@@ -276,7 +283,7 @@ static int parts_of(long tokens, int heads, int D) {
 int rope_bwd_groups(long tokens, int Hq, int Hk, int D) {
   const long waves = tokens * parts_of(tokens, Hq + Hk, D);
   const long g = (waves + 3) / 4;
-  return static_cast<int>(g > 1024 ? 1024 : g);
+  return static_cast<int>(g > 1024 ? 1024 : g);  // (the join takes up to 1024 parts)
 }
 
 static rope_args pack(const rope_call &z) {
@@ -318,7 +325,7 @@ template <typename IO, int D> hipError_t launch_rope_bwd(const rope_call &z, flo
   return hipGetLastError();
 }
 template <int D> hipError_t launch_rope_dw(const float *part, int groups, float *dwq, float *dwk, hipStream_t st) {
-  hipLaunchKernelGGL((gdn2_rope_dw_kernel<D>), dim3(2 * D / 16), dim3(256), 0, st, part, groups, dwq, dwk);
+  hipLaunchKernelGGL((gdn2_rope_dw_kernel<D>), dim3(2 * D / 16), dim3(1024), 0, st, part, groups, dwq, dwk);
   return hipGetLastError();
 }
 
