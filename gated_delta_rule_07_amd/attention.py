@@ -53,13 +53,22 @@ def _like(t, name: str, shape, dtype) -> None:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
 
 
+def _stream_of(dev: int) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+# torch's own accessor of the same handle where it has one: a microsecond less
+# a call than the Stream object
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_of)
+
+
 def _call(dev: int, fn, *args) -> None:
     """fn(*args, stream) on the device's current stream, whatever device is current."""
     if dev == torch.cuda.current_device():
-        status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        status = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            status = fn(*args, _raw_stream(dev))
     if status:
         _check(status)
 

@@ -251,8 +251,10 @@ __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1))
   typedef tile<IO, D> TL;
   constexpr int NT = 64 * WK * WR, BK = 32 * WK, BQ = 32 * WR, CPR = TL::CPR, CH = BQ * CPR / NT, RPI = NT / CPR;
   constexpr int TILEB = BQ * TL::ROWB, KTB = BK * TL::ROWB, KCH = BK * CPR / NT;
-  // a second buffer for the tile where it does not cost a workgroup a CU
-  constexpr int NB = 2 * KTB + 4 * TILEB <= 80000 || (2 * KTB + 2 * TILEB > 80000 && 2 * KTB + 4 * TILEB <= 150000) ? 2 : 1;
+  // A second buffer for the tile where it fits and does not cost a workgroup a
+  // CU (8 waves of over 128 registers are alone on one anyway).
+  constexpr int ONE = 2 * KTB + 2 * TILEB, TWO = ONE + 2 * TILEB;
+  constexpr int NB = TWO <= 80000 || (TWO <= 150000 && (ONE > 80000 || NT == 512)) ? 2 : 1;
   static_assert(BQ * CPR % NT == 0 && BK * CPR % NT == 0, "staging split");
   // K, V, Q and dO; in the end the room in which the sums are joined
   constexpr int TILES = 2 * KTB + NB * 2 * TILEB, JOIN = WK * WR * 32 * D * 4;

@@ -16,82 +16,11 @@
 //
 // WM waves share key tiles of 32 KT keys along 32-row blocks; WN waves split
 // the tile's keys (each keeps its own m, l, O, joined at the end).
-#include "gdn2_attn.hpp"
+#include "gdn2_attn_fwd.hpp"
 #include <type_traits>
 
 namespace gdn2 {
 namespace attn {
-
-struct fwd_args {
-  const void *q, *k, *v;
-  void *o;
-  float *lse;
-  const int32_t *cu;         // packed queries, or nullptr: N sequences of T tokens
-  const int32_t *table;      // paged: [N, max_pages]
-  const int32_t *seq_lens;   // paged: keys of each sequence
-  const uint8_t *ks, *vs;    // paged e4m3: [pages, Hk, page] exponent bytes
-  float *part_o, *part_lse;  // splits > 1: [splits, T total, Hq(, D)]
-  int N, T, Hq, Hk, G;
-  int Ttot;                  // tokens of q in all
-  int max_pages, num_pages, page_shift;
-  int window, splits;
-  float c;                   // scale log2 e
-  order od;
-};
-
-// Infinities and NaN of an operand set to zero; whether there were any.
-__device__ __forceinline__ bool drop_nonfinite(frag8<bf16_t> &x) {
-  u32x4 w = __builtin_bit_cast(u32x4, x.v);
-  bool any = false;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const bool lo = (w[i] & 0x7f80u) == 0x7f80u, hi = (w[i] & 0x7f800000u) == 0x7f800000u;
-    any |= lo | hi;
-    w[i] &= (lo ? 0xffff0000u : 0xffffffffu) & (hi ? 0x0000ffffu : 0xffffffffu);
-  }
-  x.v = __builtin_bit_cast(bf16x8, w);
-  return any;
-}
-__device__ __forceinline__ bool drop_nonfinite(frag8<float> &x) {
-  bool any = false;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const bool lo = !(fabsf(x.lo[i]) <= 3.4028234663852886e38f), hi = !(fabsf(x.hi[i]) <= 3.4028234663852886e38f);
-    any |= lo | hi;
-    x.lo[i] = lo ? 0.f : x.lo[i];
-    x.hi[i] = hi ? 0.f : x.hi[i];
-  }
-  return any;
-}
-
-// The wave's LDS accesses before and after, by any of its lanes, keep their
-// order (the hardware keeps it; this keeps the compiler to it).
-__device__ __forceinline__ void wave_order() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
-// Four channels of a row: its output, or with split keys its float32 part.
-template <typename IO, int D>
-__device__ __forceinline__ void store_row(const fwd_args &a, f32x4 x, float l, size_t qrow, int split, bool ok, int ch) {
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  x *= inv;
-  if (!ok)
-    return;
-  if (a.splits > 1)
-    io<float>::store4(a.part_o + (static_cast<size_t>(split) * a.Ttot * a.Hq + qrow) * D + ch, x);
-  else
-    io<IO>::store4(static_cast<IO *>(a.o) + qrow * D + ch, x);
-}
-// ln of the row's sum (with split keys: of the part's, in base 2)
-__device__ __forceinline__ void store_lse(const fwd_args &a, float m, float l, size_t qrow, int split) {
-  const float x = m + log2f(l);
-  if (a.splits > 1)
-    a.part_lse[static_cast<size_t>(split) * a.Ttot * a.Hq + qrow] = x;
-  else if (a.lse)
-    a.lse[qrow] = x * LN2;
-}
 
 template <typename IO, typename CT, int D, int WM, int WN, int KT, bool PAGED>
 __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
@@ -209,7 +138,7 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
   float *const kscale = scales + wn * 2 * SN, *const vscale = kscale + SN;
   const int wv = __builtin_amdgcn_readfirstlane(wave);
   u32x4 rk[DMA ? 1 : CH], rv[DMA ? 1 : CH];
-  int ent[CH];
+  int ent[CH], bad = 0;
   uint8_t bk = 127, bv = 127;
   int ent_b = 0;
   const int32_t *table = PAGED ? a.table + static_cast<size_t>(sq.n) * a.max_pages : nullptr;
@@ -234,19 +163,20 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
   auto load_tile = [&](int kb, int buf) {
     const size_t base = PAGED ? 0 : (static_cast<size_t>(sq.start + kb) * a.Hk + hk) * D;
     const CT *const kp = static_cast<const CT *>(a.k) + base, *const vp = static_cast<const CT *>(a.v) + base;
+    if constexpr (PAGED)
+      bad = 0;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       int j = kb + sr0 + ROWS_PER_I * i;
       j = j < k1 ? j : k1 - 1;
       if constexpr (PAGED) {
-        // an entry outside the cache stands for zeros
+        // (an entry outside the cache stands for zeros, see store_tile)
         const bool ok = static_cast<unsigned>(ent[i]) < static_cast<unsigned>(a.num_pages);
+        bad |= ok ? 0 : 1 << i;
         const size_t off = (((static_cast<size_t>(ok ? ent[i] : 0) * a.Hk + hk) << a.page_shift) + (j & pmask)) * D +
                            sc * KV::VPC;
         rk[i] = *reinterpret_cast<const u32x4 *>(kp + off);
         rv[i] = *reinterpret_cast<const u32x4 *>(vp + off);
-        if (!ok)
-          rk[i] = rv[i] = u32x4{0u, 0u, 0u, 0u};
       } else {
         if constexpr (DMA) {
           const unsigned off = static_cast<unsigned>(j - kb) * kstep + (sc ^ KV::f(sr0 + ROWS_PER_I * i)) * KV::VPC;
@@ -272,6 +202,14 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
   auto store_tile = [&](int buf) {
     if constexpr (DMA)
       return;
+    if constexpr (PAGED) {
+      if (__any(bad)) {
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+          if (bad >> i & 1)
+            rk[i] = rv[i] = u32x4{0u, 0u, 0u, 0u};
+      }
+    }
 #pragma unroll
     for (int i = 0; i < (DMA ? 1 : CH); ++i) {
       const int at = wave_b + buf * 2 * TILEB + KV::at(st / CPR + ROWS_PER_I * i, sc);
@@ -548,13 +486,16 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
   }
 }
 
-// Joins the parts of split keys: a workgroup per (token, query head), wave w
-// takes the parts w, w + 4, ..; weights 2^(lse_s - max lse); the order of the
-// sums is fixed.
-template <typename IO, int D> __global__ void __launch_bounds__(256) gdn2_attn_join_kernel(fwd_args a) {
-  __shared__ float red[4][D + 1];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const size_t rows = static_cast<size_t>(a.Ttot) * a.Hq, row = blockIdx.x;
+// Joins the parts of split keys: W waves per (token, query head), wave w of a
+// row takes the parts w, w + W, ..; weights 2^(lse_s - max lse); the order of
+// the sums is fixed.
+template <typename IO, int D, int W> __global__ void __launch_bounds__(256) gdn2_attn_join_kernel(fwd_args a) {
+  __shared__ float red[W][D + 1];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, w0 = W == 1 ? 0 : wave;
+  const size_t rows = static_cast<size_t>(a.Ttot) * a.Hq;
+  const size_t row = W == 1 ? static_cast<size_t>(blockIdx.x) * 4 + wave : blockIdx.x;
+  if (row >= rows)
+    return;
   if (a.cu && row >= static_cast<size_t>(a.cu[a.N] < 0 ? 0 : a.cu[a.N]) * a.Hq)
     return;  // behind the last sequence
   float M = neg_inf();
@@ -570,7 +511,7 @@ template <typename IO, int D> __global__ void __launch_bounds__(256) gdn2_attn_j
   for (int i = 0; i < V; ++i)
     acc[i] = 0.f;
 #pragma unroll 4
-  for (int s = wave; s < a.splits; s += 4) {
+  for (int s = w0; s < a.splits; s += W) {
     // (a part without keys: weight 0 and zeros; NaN stays NaN)
     const float w = fast_exp2(a.part_lse[s * rows + row] - base);
     const float *p = a.part_o + (s * rows + row) * D + V * lane;
@@ -579,19 +520,33 @@ template <typename IO, int D> __global__ void __launch_bounds__(256) gdn2_attn_j
     for (int i = 0; i < V; ++i)
       acc[i] += w * p[i];
   }
+  if constexpr (W > 1) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      red[wave][V * lane + i] = acc[i];
+    if (lane == 0)
+      red[wave][D] = L;
+    __syncthreads();
+    if (wave > 0)
+      return;
+    L = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+      L += red[w][D];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      acc[i] = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+        acc[i] += red[w][V * lane + i];
+    }
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  IO *o = static_cast<IO *>(a.o) + row * D + V * lane;
 #pragma unroll
   for (int i = 0; i < V; ++i)
-    red[wave][V * lane + i] = acc[i];
-  if (lane == 0)
-    red[wave][D] = L;
-  __syncthreads();
-  L = (red[0][D] + red[1][D]) + (red[2][D] + red[3][D]);
-  const int c = threadIdx.x;
-  if (c < D) {
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    static_cast<IO *>(a.o)[row * D + c] = io<IO>::from_f(((red[0][c] + red[1][c]) + (red[2][c] + red[3][c])) * inv);
-  }
-  if (a.lse && c == 0)
+    o[i] = io<IO>::from_f(acc[i] * inv);
+  if (a.lse && lane == 0)
     a.lse[row] = (base + log2f(L)) * LN2;
 }
 
@@ -602,9 +557,18 @@ template <typename IO, int D> __global__ void __launch_bounds__(256) gdn2_attn_j
 static bool few_rows(const attn_sizes &z) {
   return static_cast<long long>(z.Ttot) * (z.Hq / z.Hk) <= 32LL * z.N;
 }
-// Parts along the keys of a paged call: enough workgroups for several rounds
-// of the chip's 512 (sequences differ in length), no part of the longest
-// possible sequence under 128 keys, at most 128 parts.
+// At most 16 rows for every sequence and kv head: the decode kernel
+// (bfloat16), with 16-row products.
+static bool decode_rows(const attn_sizes &z) {
+  return !z.packed && static_cast<long long>(z.T) * (z.Hq / z.Hk) <= 16;
+}
+
+// Parts along the keys of a paged call: enough workgroups that sequences of
+// different lengths even out over the CUs, no part of the longest possible
+// sequence under 128 keys, at most 128 parts.  (Decode of 64 sequences x 4 kv
+// heads: 136 us at 2048 workgroups, 151 at 1024 and 512; one 1024-token chunk
+// among 23 tokens: 113 us at 768, 125 at 1024, 137 at 2048, where its parts'
+// outputs weigh more.)
 int attn_paged_splits(const attn_sizes &z) {
   order od;
   const bool few = few_rows(z);
@@ -613,7 +577,7 @@ int attn_paged_splits(const attn_sizes &z) {
   long long keys = z.max_keys;
   if (z.window > 0 && keys > z.window + 128LL)
     keys = z.window + 128LL;
-  long long s = ((few ? 2048 : 1024) + blocks - 1) / blocks;
+  long long s = ((few ? 2048 : 768) + blocks - 1) / blocks;
   if (s > keys / 128)
     s = keys / 128;
   return s < 1 ? 1 : (s > 128 ? 128 : static_cast<int>(s));
@@ -671,6 +635,12 @@ hipError_t launch_attn_paged(const attn_sizes &z, const attn_ptrs &p, int splits
     a.part_o = static_cast<float *>(ws);
     a.part_lse = a.part_o + rows * D * splits;
   }
+  if constexpr (sizeof(IO) == 2) {
+    if (decode_rows(z)) {
+      plan_tiles(z, a.G, 16, a.od);
+      return launch_attn_decode<CT, D>(a, st);
+    }
+  }
   constexpr int WN = sizeof(IO) == 2 ? 4 : 2;
   return few_rows(z) ? go<IO, CT, D, 1, WN, 1, true>(a, z, st) : go<IO, CT, D, 4, 1, KT, true>(a, z, st);
 }
@@ -683,7 +653,11 @@ hipError_t launch_attn_join(const attn_sizes &z, const attn_ptrs &p, int splits,
   const size_t rows = static_cast<size_t>(z.Ttot) * z.Hq;
   a.part_o = static_cast<float *>(ws);
   a.part_lse = a.part_o + rows * D * splits;
-  hipLaunchKernelGGL((gdn2_attn_join_kernel<IO, D>), dim3(static_cast<unsigned>(rows)), dim3(256), 0, st, a);
+  // one wave a row where there are rows enough, or few parts
+  if (rows >= 8192 || splits <= 4)
+    hipLaunchKernelGGL((gdn2_attn_join_kernel<IO, D, 1>), dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL((gdn2_attn_join_kernel<IO, D, 4>), dim3(static_cast<unsigned>(rows)), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 
