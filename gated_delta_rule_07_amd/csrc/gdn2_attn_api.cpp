@@ -362,7 +362,7 @@ size_t gdn2_attn_bwd_workspace_bytes(int B, int T, int Hq, int Hk, int d) {
     (void)ok();
     return 0;
   }
-  return gdn2::attn::attn_bwd_bytes(static_cast<size_t>(z.Ttot) * Hq);
+  return T == 0 ? 0 : gdn2::attn::attn_bwd_bytes(z, d);
 }
 
 gdn2_status_t gdn2_attn_bwd(const void *q, const void *k, const void *v, const void *o, const float *lse,
@@ -379,7 +379,7 @@ gdn2_status_t gdn2_attn_bwd(const void *q, const void *k, const void *v, const v
   st = check_ptrs(fn, {q, k, v, o, lse, dout, dq, dk, dv}, {cu_seqlens, workspace});
   if (st != GDN2_OK)
     return st;
-  const size_t need = gdn2::attn::attn_bwd_bytes(static_cast<size_t>(z.Ttot) * Hq);
+  const size_t need = gdn2::attn::attn_bwd_bytes(z, d);
   if (!workspace || workspace_bytes < need)
     return fail(GDN2_ERR_WORKSPACE_TOO_SMALL, "%s: workspace holds %zu bytes, %zu are needed", fn, workspace_bytes,
                 need);

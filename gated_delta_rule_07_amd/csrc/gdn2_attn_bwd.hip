@@ -25,7 +25,9 @@ struct bwd_args {
   const int32_t *cu;
   int N, T, Ttot, Hq, Hk, G, window;
   float c, scale;
-  int gs;   // heads of a row tile of the dk, dv kernel
+  int gs;            // heads of a row tile of the dk, dv kernel
+  int parts;         // workgroups that share a key tile's rows (dk, dv kernel)
+  float *part_sums;  // parts > 1: [parts, 2, Ttot, Hk, D], sums of dk / scale and dv
   order od;
 };
 
@@ -265,7 +267,9 @@ __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1))
   const int wkey = wave % WK, wrow = wave / WK;
   int unit, slot, hk, key0;
   span sq;
-  if (!place(a.od, blockIdx.x, unit, slot) || !locate(a, unit, a.od.tiles - 1 - slot, 1, BK, lane, sq, hk, key0))
+  const int part = blockIdx.x % a.parts;
+  if (!place(a.od, blockIdx.x / a.parts, unit, slot) ||
+      !locate(a, unit, a.od.tiles - 1 - slot, 1, BK, lane, sq, hk, key0))
     return;
   const int key_end = key0 + BK < sq.len ? key0 + BK : sq.len;
   // Tokens whose rows see a key of the workgroup.  A tile is TB whole tokens
@@ -355,11 +359,14 @@ __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1))
 #pragma unroll
   for (int n = 0; n < D / 32; ++n)
     dk[n] = dv[n] = zero16();
-  load_tile(0);
-  for (int it = 0; it < ntiles; ++it) {
+  // this workgroup's share of the tiles
+  const int per = (ntiles + a.parts - 1) / a.parts, it0 = part * per, it1 = it0 + per < ntiles ? it0 + per : ntiles;
+  if (it0 < it1)
+    load_tile(it0);
+  for (int it = it0; it < it1; ++it) {
     const int buf = NB == 2 ? it & 1 : 0;
     const int bo = buf * 2 * TILEB;
-    if (NB == 1 && it > 0)
+    if (NB == 1 && it > it0)
       __syncthreads();  // the tile before is read
     if constexpr (NB == 2) {
       dma_wait();
@@ -377,7 +384,7 @@ __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1))
       s_pos[buf][tid] = rp;
     }
     __syncthreads();
-    if (it + 1 < ntiles)
+    if (it + 1 < it1)
       load_tile(it + 1);
     const int u0 = 32 * wrow;
     if (u0 >= nrows)
@@ -474,7 +481,17 @@ __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1))
   auto store = [&](const f32x16(&x)[D / 32], float scale, IO *out) {
     if (key >= sq.len)
       return;
-    IO *row = out + (static_cast<size_t>(sq.start + key) * a.Hk + hk) * D + 4 * h;
+    const size_t at = (static_cast<size_t>(sq.start + key) * a.Hk + hk) * D + 4 * h;
+    if (a.parts > 1) {
+      float *const sums = a.part_sums + (2 * part + (wrow == 0 ? 0 : 1)) * (static_cast<size_t>(a.Ttot) * a.Hk * D) + at;
+#pragma unroll
+      for (int n = 0; n < D / 32; ++n)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          io<float>::store4(sums + 32 * n + 8 * g,
+                            f32x4{x[n][4 * g], x[n][4 * g + 1], x[n][4 * g + 2], x[n][4 * g + 3]});
+      return;
+    }
 #pragma unroll
     for (int n = 0; n < D / 32; ++n)
 #pragma unroll
@@ -483,7 +500,7 @@ __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1))
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           z[i] = x[n][4 * g + i] * scale;
-        io<IO>::store4(row + 32 * n + 8 * g, z);
+        io<IO>::store4(out + at + 32 * n + 8 * g, z);
       }
   };
 #pragma unroll
@@ -514,7 +531,41 @@ __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1))
   }
 }
 
+// The parts' sums, in order, to dk and dv: four channels a thread, dk's then
+// dv's.
+template <typename IO, int D> __global__ void __launch_bounds__(256) gdn2_attn_dkv_join_kernel(bwd_args a) {
+  const size_t rows = static_cast<size_t>(a.Ttot) * a.Hk * D;
+  const size_t at = (static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (at >= 2 * rows)
+    return;
+  const bool is_v = at >= rows;
+  const size_t e = is_v ? at - rows : at;
+  if (a.cu && static_cast<long>(e / (static_cast<size_t>(a.Hk) * D)) >= a.cu[a.N])
+    return;  // behind the last sequence
+  f32x4 x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int p = 0; p < a.parts; ++p)
+    x += io<float>::load4(a.part_sums + 2 * p * rows + at);
+  io<IO>::store4(static_cast<IO *>(is_v ? a.dv : a.dk) + e, x * (is_v ? 1.f : a.scale));
+}
+
 // ------------------------------------------------------------- launchers --
+// Workgroups that share a 64-key tile's rows: where a call has few key tiles
+// (few tokens, or one kv head for many query heads), enough for 1024 of them,
+// at most 16 and at least 1024 rows each.  (4096 tokens, 16 query heads on one
+// kv head, d = 128: dk and dv 1867 us with one, 320 with 16; 11 packed
+// sequences, 9973 tokens, 12 heads on 4, d = 64: 166 with one, 130 with two;
+// 1543 float32 tokens, 4 heads on 4: 22 with one, 34 with three.)  The rule sees
+// the sizes the workspace is asked for: tokens and heads, no sequence lengths.
+int attn_bwd_parts(const attn_sizes &z) {
+  const long long seqs = z.packed ? 1 : z.N;
+  const long long tiles = seqs * ((z.T + 63) / 64) * z.Hk, rows = static_cast<long long>(z.T) * (z.Hq / z.Hk);
+  long long p = (1024 + tiles - 1) / (tiles > 0 ? tiles : 1);
+  if (p > rows / 1024)
+    p = rows / 1024;
+  return p < 1 ? 1 : (p > 16 ? 16 : static_cast<int>(p));
+}
+
 static void fill(bwd_args &a, const attn_sizes &z, const attn_ptrs &p, void *ws) {
   a.q = p.q;
   a.k = p.k;
@@ -536,6 +587,8 @@ static void fill(bwd_args &a, const attn_sizes &z, const attn_ptrs &p, void *ws)
   a.window = z.window;
   a.c = z.scale * LOG2E;
   a.scale = z.scale;
+  a.parts = attn_bwd_parts(z);
+  a.part_sums = a.parts > 1 ? reinterpret_cast<float *>(static_cast<char *>(ws) + attn_bwd_stat_bytes(z)) : nullptr;
   a.gs = a.G < 32 ? a.G : 32;
   while (a.G % a.gs)
     --a.gs;
@@ -570,17 +623,24 @@ hipError_t launch_attn_bwd_dkv(const attn_sizes &z, const attn_ptrs &p, void *ws
   bwd_args a;
   fill(a, z, p, ws);
   // Where the tiles do not give every CU two, the longest sequence's first
-  // keys, which every row sees, take as long as the call: half as many keys
-  // and twice the row parts a workgroup.  (bfloat16, 11 packed sequences of up
-  // to 3167 tokens x 4 kv heads, d = 64: 356 tiles, 157 against 200 us; 8 x
-  // 4096 x 4, d = 128, window 2048: 1024 tiles, 1321 against 985 us.)
-  constexpr int WK = sizeof(IO) == 2 ? 4 : 2, WR4 = D * sizeof(IO) <= 256 ? 4 : 2;
+  // keys, which every row sees, take as long as the call: d = 64 then takes
+  // half as many keys and twice the row parts a workgroup.  (bfloat16, 11 packed
+  // sequences of up to 3167 tokens x 4 kv heads: 356 tiles, 157 against 200 us;
+  // d = 128 has no registers for it, 8 waves of 64 keys would go through
+  // scratch.)
+  constexpr int WK = sizeof(IO) == 2 ? 4 : 2;
+  constexpr bool HALF = D * sizeof(IO) <= 128 || sizeof(IO) == 4;
+  constexpr int WKH = HALF ? WK / 2 : WK, WRH = D == 64 ? 4 : 2;
   unsigned blocks = plan_tiles(z, 1, 32 * WK, a.od);
-  if (static_cast<long long>(a.od.units) * a.od.tiles >= 512) {
-    hipLaunchKernelGGL((gdn2_attn_dkv_kernel<IO, D, WK, 2>), dim3(blocks), dim3(128 * WK), 0, st, a);
+  if (!HALF || (a.parts == 1 && static_cast<long long>(a.od.units) * a.od.tiles >= 512)) {
+    hipLaunchKernelGGL((gdn2_attn_dkv_kernel<IO, D, WK, 2>), dim3(blocks * a.parts), dim3(128 * WK), 0, st, a);
   } else {
-    blocks = plan_tiles(z, 1, 16 * WK, a.od);
-    hipLaunchKernelGGL((gdn2_attn_dkv_kernel<IO, D, WK / 2, WR4>), dim3(blocks), dim3(32 * WK * WR4), 0, st, a);
+    blocks = plan_tiles(z, 1, 32 * WKH, a.od);
+    hipLaunchKernelGGL((gdn2_attn_dkv_kernel<IO, D, WKH, WRH>), dim3(blocks * a.parts), dim3(64 * WKH * WRH), 0, st, a);
+  }
+  if (a.parts > 1) {
+    const size_t n = static_cast<size_t>(z.Ttot) * z.Hk * D / 2;  // threads
+    hipLaunchKernelGGL((gdn2_attn_dkv_join_kernel<IO, D>), dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, st, a);
   }
   return hipGetLastError();
 }

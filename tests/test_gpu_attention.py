@@ -102,6 +102,16 @@ def test_attn_many_sequences(g):
     run_attn(g, lens, 4, 2, 64, BF16, 9, True, True, seed=4)
 
 
+@pytest.mark.parametrize("dtype,d", [(BF16, 64), (BF16, 128), (F32, 64), (F32, 128)])
+def test_attn_one_kv_head(g, dtype, d):
+    """Many query heads on one kv head: few key tiles with many rows, shared
+    by several workgroups."""
+    print(f"attn one kv head d={d} {dtype}", flush=True)
+    run_attn(g, [700, 0, 411, 33], 16, 1, d, dtype, 0, True, True, seed=8, tail=5)
+    run_attn(g, [700, 0, 411, 33], 35, 1, d, dtype, 90, True, True, seed=9, tail=5)
+    run_attn(g, [130], 67, 1, d, dtype, 0, False, True, seed=10)
+
+
 def test_attn_long(g):
     """A long sequence (rows of 64 key tiles) with a window and without."""
     print("attn long 4096", flush=True)
