@@ -103,8 +103,10 @@ gdn2_status_t check_attn(const char *fn, int B, int T, int Hq, int Hk, int d, in
   if (!(scale > 0.f) || !std::isfinite(scale))
     return fail(GDN2_ERR_INVALID_ARGUMENT, "%s: scale must be positive and finite", fn);
   const long long tot = static_cast<long long>(B) * T, N = packed ? num_seqs : B;
-  if (tot > MAX_ROWS || tot * Hq > MAX_ROWS || N * Hk > MAX_UNITS)
-    return fail(GDN2_ERR_UNSUPPORTED, "%s: too large (at most 2^26 - 1 query rows, 2^20 - 1 sequence-heads)", fn);
+  // (a row tile's offsets within 128 tokens are 32-bit: 2^15 heads of 128)
+  if (Hq > (1 << 15) || tot > MAX_ROWS || tot * Hq > MAX_ROWS || N * Hk > MAX_UNITS)
+    return fail(GDN2_ERR_UNSUPPORTED,
+                "%s: too large (at most 2^15 query heads, 2^26 - 1 query rows, 2^20 - 1 sequence-heads)", fn);
   z.N = static_cast<int>(N);
   z.T = T;
   z.Ttot = static_cast<int>(tot);

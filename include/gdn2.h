@@ -412,9 +412,11 @@ gdn2_status_t gdn2_decode_step(const void *q, const void *k, const void *v, cons
  * the backward's score gradients) are rounded to bfloat16 as operands of
  * their matrix products.  Every sum has a fixed order: the same call gives
  * the same bits.  Outputs may not alias inputs, except where said.
- * Limits: at most 2^26 - 1 (token, query head) rows a call, and 2^20 - 1
- * (sequence, kv head) pairs.  Rows of the tensors behind cu_seqlens[N] are
- * neither read nor written. */
+ * Limits: at most 2^15 query heads, 2^26 - 1 (token, query head) rows a call,
+ * and 2^20 - 1 (sequence, kv head) pairs.  Rows of the tensors behind
+ * cu_seqlens[N] are neither read nor written.  A workspace's contents on entry
+ * are irrelevant; calls that may run at the same time need workspaces of
+ * their own. */
 
 /* flags of gdn2_qk_norm_rope_fwd / _bwd */
 #define GDN2_ROPE_INTERLEAVED (1u << 0) /* pairs are channels (2j, 2j + 1); without

@@ -82,6 +82,7 @@ def test_attn_refusals(L, f):
         assert f(L, scale=s) == 1
     assert f(L, q=None) == 1 and f(L, q=FAKE + 8) == 1 and f(L, o=None) == 1 and f(L, lse=FAKE + 4) == 1
     assert f(L, cu=FAKE + 4, B=1, N=2) == 1
+    assert f(L, T=1, B=1, Hq=1 << 16, Hk=1) == 2
     assert f(L, B=BIG, T=BIG) == 2 and f(L, T=1 << 24) == 2 and f(L, B=1, cu=FAKE, N=BIG) == 2
     assert f(L, T=0) == 0
     assert L.gdn2_last_error() == b""

@@ -463,6 +463,56 @@ def test_paged_nonfinite_values_reach_only_their_rows(g):
         assert (torch.isnan(seen).all() if cdt == F8 else (seen[..., 3] == math.inf).all())
 
 
+def test_paged_offsets_past_32_bits(g):
+    """Caches of 5 GiB each (bfloat16) and 2.5 GiB (e4m3): the sequence's keys
+    lie in the last pages.  Only those are ever touched."""
+    Hk, page, d, n, T = 8, 64, 128, 150, 40
+    pages = 5 * (1 << 30) // (Hk * page * d * 2)
+    for cdt in (BF16, F8):
+        gn = gen(51)
+        kc, vc = (torch.empty((pages, Hk, page, d), dtype=cdt, device="cuda") for _ in range(2))
+        ks, vs = (torch.empty((pages, Hk, page), dtype=torch.uint8, device="cuda") for _ in range(2)) \
+            if cdt == F8 else (None, None)
+        k, v = randn(gn, (n, Hk, d), BF16), randn(gn, (n, Hk, d), BF16)
+        table = torch.tensor([[pages - 1, pages - 3, pages - 2]], dtype=torch.int32, device="cuda")
+        t = torch.arange(n, device="cuda")
+        slots = table[0, t // page].long() * page + t % page
+        print(f"paged large cache {cdt} pages={pages}", flush=True)
+        g.kv_cache_write(k, v, slots, kc, vc, ks, vs)
+        rk, rv = g.kv_cache_read(slots, kc, vc, ks, vs)
+        if cdt == F8:
+            k, v = (ref.quantise(x.double())[0] for x in (k, v))
+        assert torch.equal(rk.double(), k.double()) and torch.equal(rv.double(), v.double())
+        lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+        for t_new in (1, T):
+            q = randn(gn, (1, t_new, 16, d), BF16)
+            o, lse = g.attn_paged(q, kc, vc, table, lens, k_scale=ks, v_scale=vs, want_lse=True)
+            r = ref.attn(q[0].double(), k.double(), v.double(), 0, d ** -0.5)
+            ref.check_attn({"o": o[0], "lse": lse[0]}, r, BF16, n, d, f"new {t_new}")
+        del kc, vc, ks, vs
+        torch.cuda.empty_cache()
+
+
+def test_paged_entries_outside_the_cache_stand_for_zeros(g):
+    gn = gen(52)
+    Hk, page, d, n = 2, 16, 64, 100
+    for dtype, cdt in CACHES:
+        for T, Hq in ((1, 4), (9, 4), (60, 4)):
+            kc, vc, ks, vs, kd, vd = make_cache(g, gn, 8, Hk, page, d, dtype, cdt)
+            table = torch.arange(8, dtype=torch.int32, device="cuda")[None].clone()
+            kd, vd = kd.clone(), vd.clone()
+            for at, e in ((1, 8), (3, -1), (4, 1 << 30)):
+                table[0, at] = e
+                kd[at * page:(at + 1) * page] = 0
+                vd[at * page:(at + 1) * page] = 0
+            print(f"paged bad entries T={T} {dtype} {cdt}", flush=True)
+            q = randn(gn, (1, T, Hq, d), dtype)
+            o, lse = g.attn_paged(q, kc, vc, table, torch.tensor([n], dtype=torch.int32, device="cuda"), k_scale=ks,
+                                  v_scale=vs, want_lse=True)
+            r = ref.attn(q[0].double(), kd[:n], vd[:n], 0, d ** -0.5)
+            ref.check_attn({"o": o[0], "lse": lse[0]}, r, dtype, n, d, f"new {T}")
+
+
 # ------------------------------------------------------- as they are used
 def layer_weights(gn, d, Hq, Hk):
     return torch.rand(d, generator=gn, device="cuda") + 0.5, torch.rand(d, generator=gn, device="cuda") + 0.5
