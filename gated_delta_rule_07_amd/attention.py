@@ -134,6 +134,8 @@ def rope_frequencies(rotary_dim: int, theta: float = 10000.0, scaling: str | Non
     elif scaling == "yarn":
         if original_length is None:
             raise ValueError("yarn scaling needs original_length")
+        if not beta_fast > beta_slow:
+            raise ValueError("yarn scaling needs beta_fast > beta_slow")
         turns = original_length * f / (2 * math.pi)
         keep = ((turns - beta_slow) / (beta_fast - beta_slow)).clamp(0.0, 1.0)
         f = f * keep + f / factor * (1.0 - keep)
@@ -230,6 +232,8 @@ def attn_fwd(q, k, v, cu_seqlens=None, window: int = 0, scale: float | None = No
 
 
 def attn_bwd_workspace_bytes(B: int, T: int, Hq: int, Hk: int, d: int, dtype: torch.dtype = torch.bfloat16) -> int:
+    """Bytes of workspace ``attn_bwd`` needs (B = 1 and the total T when
+    packed; the same for either dtype)."""
     return int(lib().gdn2_attn_bwd_workspace_bytes(B, T, Hq, Hk, d))
 
 

@@ -442,7 +442,9 @@ gdn2_status_t gdn2_attn_paged(const void *q, const void *k_cache, const void *v_
     return st;
   if (T == 0)
     return ok();
-  st = check_ptrs(fn, {q, k_cache, v_cache, block_table, seq_lens, o}, {cu_seqlens, lse, workspace});
+  // (a table of no pages has no entries: nothing reads it)
+  st = check_ptrs(fn, {q, k_cache, v_cache, max_pages ? block_table : seq_lens, seq_lens, o},
+                  {cu_seqlens, lse, workspace, block_table});
   if (st != GDN2_OK)
     return st;
   const size_t need = paged_bytes(z, d);

@@ -521,10 +521,11 @@ size_t gdn2_attn_paged_workspace_bytes(int B, int T, int Hq, int Hk, int d, int 
  * its L new queries stand at the positions seq_lens[n] - L .. seq_lens[n] - 1
  * and see keys as in gdn2_attn_fwd.  q and o are [B, T, Hq, d] (T new tokens
  * for each of B sequences; decode is T = 1) or packed by cu_seqlens
- * [1, T, Hq, d].  A query at a negative position sees nothing: o = 0,
- * lse = -inf.  A table entry outside the cache stands for a page of zeros;
- * entries that no query sees (behind seq_lens, before the window) are not
- * read.  lse [B, T, Hq] float32 or NULL.  max_pages * page_size <= 2^28.
+ * [1, T, Hq, d].  A query at a negative position (more new tokens than keys,
+ * seq_lens[n] = 0 for padding) sees nothing: o = 0, lse = -inf.  A table entry
+ * outside the cache stands for a page of zeros; entries that no query sees
+ * (behind seq_lens, before the window) are not read, and a table of no pages
+ * may be NULL.  lse [B, T, Hq] float32 or NULL.  max_pages * page_size <= 2^28.
  * Where the call has too few rows to fill the GPU, its keys are split into
  * parts (their number depends on the sizes alone) that a second kernel joins
  * from the workspace. */
@@ -545,8 +546,8 @@ const char *gdn2_last_error(void);
 int gdn2_abi_version(void);
 
 /* Kernel timing for benchmarks.  While enabled, every kernel launch made by
- * gdn2_chunk_fwd / gdn2_decode_step is bracketed by two HIP events recorded
- * on the launch stream.  gdn2_profile_read synchronises those events and
+ * the entry points above is bracketed by two HIP events recorded on the
+ * launch stream.  gdn2_profile_read synchronises those events and
  * returns, per kernel name, the summed time in milliseconds and the launch
  * count; reset != 0 clears the record.  Enabling creates events (not device
  * memory); it is not for use under graph capture. */

@@ -175,6 +175,7 @@ def test_rope_frequencies():
     mid = (turns > 1) & (turns < 32)
     assert mid.any() and (yarn[mid] < f[mid]).all() and (yarn[mid] > f[mid] / 8).all()
     for kw in (dict(rotary_dim=12), dict(rotary_dim=0), dict(rotary_dim=64, scaling="x"),
-               dict(rotary_dim=64, scaling="yarn", factor=2.0), dict(rotary_dim=64, scaling="linear", factor=0.0)):
+               dict(rotary_dim=64, scaling="yarn", factor=2.0),
+               dict(rotary_dim=64, scaling="yarn", factor=2.0, original_length=4096, beta_fast=1.0), dict(rotary_dim=64, scaling="linear", factor=0.0)):
         with pytest.raises(ValueError):
             g.rope_frequencies(device="cpu", **kw)

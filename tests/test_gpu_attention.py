@@ -119,6 +119,50 @@ def test_attn_long(g):
     run_attn(g, [4096], 4, 2, 128, BF16, 2048, False, True, seed=6)
 
 
+def test_offsets_past_32_bits(g):
+    """Tensors of 4 GiB each and more: packed sequences of zeros, then one of
+    70 tokens behind 2^24 rows."""
+    Hq = Hk = 128
+    d, n, lead, N = 128, 70, 1 << 17, 1 << 8
+    T = lead + n
+    gn = gen(55)
+
+    def tensor():
+        x = torch.zeros((1, T, Hq, d), dtype=BF16, device="cuda")
+        x[0, lead:] = randn(gn, (n, Hq, d), BF16)
+        return x
+
+    cu = torch.arange(0, lead + 1, lead // N, dtype=torch.int32, device="cuda")
+    cu = torch.cat([cu, torch.tensor([T], dtype=torch.int32, device="cuda")])
+    q, k, v, do = (tensor() for _ in range(4))
+    print("large tensors: forward", flush=True)
+    o, lse = g.attn_fwd(q, k, v, cu)
+    last = [x[0, lead:].double() for x in (q, k, v)]
+    r = ref.attn(*last, 0, d ** -0.5)
+    ref.check_attn({"o": o[0, lead:], "lse": lse[0, lead:]}, r, BF16, n, d, "last sequence")
+    assert (o[0, :lead] == 0).all()
+    print("large tensors: backward", flush=True)
+    gr = g.attn_bwd(q, k, v, o, lse, do, cu)
+    small = [x[:, lead:].contiguous() for x in (q, k, v, o, lse, do)]
+    want = g.attn_bwd(*small)
+    for name, x in gr.items():
+        # (other workgroup shapes: the sums' order differs, 70 terms at most)
+        y = want[name].double()
+        assert (x[0, lead:].double() - y[0]).abs().max() <= 2 ** -7 * y.abs().max(), name
+        assert (x[0, :lead] == 0).all(), name
+    print("large tensors: norm and rotation", flush=True)
+    f = g.rope_frequencies(d)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")[None]
+    q2, k2 = g.qk_norm_rope(q, k, f, positions=pos)
+    s2 = g.qk_norm_rope(small[0], small[1], f, positions=pos[:, lead:].contiguous())
+    assert torch.equal(q2[:, lead:], s2[0]) and torch.equal(k2[:, lead:], s2[1])
+    gr = g.qk_norm_rope_bwd(q, k, f, do, do, positions=pos)
+    w = g.qk_norm_rope_bwd(small[0], small[1], f, small[5], small[5], positions=pos[:, lead:].contiguous())
+    assert torch.equal(gr["dq"][:, lead:], w["dq"]) and torch.equal(gr["dk"][:, lead:], w["dk"])
+    del gr, w, q, k, v, do, o, q2, k2
+    torch.cuda.empty_cache()
+
+
 def test_attn_gradients_against_differences(g):
     """dL along random directions, L = sum(o * do): the kernels' gradients
     against central differences of the float64 definition.  The definition's
@@ -491,6 +535,19 @@ def test_paged_offsets_past_32_bits(g):
             ref.check_attn({"o": o[0], "lse": lse[0]}, r, BF16, n, d, f"new {t_new}")
         del kc, vc, ks, vs
         torch.cuda.empty_cache()
+
+
+def test_paged_table_of_no_pages(g):
+    """A batch that holds no keys yet: every query sees nothing."""
+    gn = gen(53)
+    for dtype, cdt in CACHES:
+        for shape in ((3, 1, 4, 64), (2, 40, 4, 64)):
+            kc, vc, ks, vs, _, _ = make_cache(g, gn, 2, 2, 16, 64, dtype, cdt)
+            q = randn(gn, shape, dtype)
+            table = torch.empty((shape[0], 0), dtype=torch.int32, device="cuda")
+            lens = torch.full((shape[0],), 7, dtype=torch.int32, device="cuda")
+            o, lse = g.attn_paged(q, kc, vc, table, lens, k_scale=ks, v_scale=vs, want_lse=True)
+            assert (o == 0).all() and (lse == -math.inf).all()
 
 
 def test_paged_entries_outside_the_cache_stand_for_zeros(g):
