@@ -343,7 +343,10 @@ inline unsigned plan_tiles(const attn_sizes &z, int GR, int BM, order &od) {
   return 8u * static_cast<unsigned>(od.units / od.g) * static_cast<unsigned>(od.tpr);
 }
 // Fewer 128-row tiles than CUs: such calls take 32-row tiles whose keys the
-// waves split.
+// waves split.  (float32, 5 sequences, 1543 tokens, 4 heads: 54 tiles, forward
+// and backward 118 us with 128 rows, 69 with 32; bfloat16, 11 sequences, 9973
+// tokens, 12 heads on 4: 980 tiles, forward 66 us with 128 rows, 78 with 32,
+// dq 70 and 88.)
 inline bool few_tiles(const order &od) { return static_cast<long long>(od.units) * od.tiles < 256; }
 
 }  // namespace attn
