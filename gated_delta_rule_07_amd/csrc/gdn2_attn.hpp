@@ -61,7 +61,8 @@ __device__ __forceinline__ f32x16 zero16() {
 
 // Registers 8j .. 8j+7 of an accumulator as an operand (acc order), rounded
 // to T: the products' operands are bfloat16 for bfloat16 tensors (half a
-// step, 2^-9, per weight; their sums and the accumulator stay float32).
+// step, at most 2^-8 relative, per weight; the row's sum is taken before the
+// rounding, and it and the accumulator stay float32).
 template <typename T> __device__ __forceinline__ frag8<T> pack8(const f32x16 &x, int j);
 template <> __device__ __forceinline__ frag8<bf16_t> pack8<bf16_t>(const f32x16 &x, int j) {
   typedef __attribute__((ext_vector_type(8))) float f32x8;

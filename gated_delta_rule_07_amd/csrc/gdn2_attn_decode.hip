@@ -14,6 +14,10 @@
 //   - K comes in operand layout straight from memory (k of a product is
 //     summed over in any order: an e4m3 lane takes 16 neighbouring channels
 //     as two operands); only V, needed transposed, goes through shared memory.
+// Measured, 64 sequences of 4K to 16K keys, 16 query heads on 4, d = 128, pages
+// of 64: e4m3 131 us (647 MB, 4.9 TB/s; a large copy 4.7), bfloat16 5.7 TB/s;
+// the general kernel's 32-row tiles took 175.  One sequence, window 2048: 7 us
+// and 4 for the join, two launches' latency.
 #include <type_traits>
 
 #include "gdn2_attn_fwd.hpp"

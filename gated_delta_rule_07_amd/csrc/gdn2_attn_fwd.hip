@@ -16,6 +16,17 @@
 //
 // WM waves share key tiles of 32 KT keys along 32-row blocks; WN waves split
 // the tile's keys (each keeps its own m, l, O, joined at the end).
+//
+// The bound is issue: a wave's 32 x 64 tile at d = 128 is 32 matrix products
+// (1024 cycles) beside about 290 vector operations, 32 of them exponentials.  So
+// the operands are read a group of products ahead, the tiles come straight from
+// memory into shared memory (no registers, no address arithmetic a chunk), and
+// the reference of the exponents moves only where it has to.  Measured: one
+// sequence of 32768 tokens, 16 heads on 4, d = 128, bfloat16: 4.3 to 4.4 ms,
+// 1000 to 1020 TFLOP/s (an 8192^3 product: 1212; without tiles straight from
+// memory 4650 us, without read-ahead and with a rescale every tile 4880); 8 x
+// 4096 tokens, window 2048: 480 to 500 us.  Paged, 1024 tokens at 12000 keys among
+// 23 single tokens: 105 us with the join's 10 (341 MB: 73 us at a copy's rate).
 #include "gdn2_attn_fwd.hpp"
 #include <type_traits>
 

@@ -16,6 +16,11 @@
 // fraction of a turn in 64 bits (position 10^6 times a frequency of 1 keeps
 // 2^-33 of a turn, where float32 would keep 2^-7), its sine and cosine are
 // float32.
+//
+// Measured, 32768 tokens x (16 + 4) heads, d = 128, bfloat16: forward 60 us
+// (336 MB, 5.6 TB/s), backward 109 us (503 MB, 4.6 TB/s) and 5 us for the sum of
+// the weight gradients' parts; a large copy runs at 4.7 TB/s.  32 tokens (a
+// decode step): 4 us, a launch's own latency.
 #include "gdn2_device.hpp"
 #include "gdn2_kernels.hpp"
 
