@@ -256,9 +256,13 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
 // 32 wr .. + 31; the row parts' sums are joined at the end.  K, V and the
 // tile of Q and dO are read from shared memory: K and V in registers would
 // leave one wave a SIMD (their 64 registers beside the 128 of the sums): 1584 us
-// at the sizes above, and 940 as it is.  Shared memory is then what is busiest
-// (every product's operands come from it, about three quarters of the time); at
-// d = 64 K and V in registers gain 3 %, not enough for a second form.
+// at the sizes above, and 940 as it is.  Now the products are busy 36 % of the
+// cycles, shared memory a third, and a wave waits 40 % of its life, for operands
+// and at the barrier, in step with the other wave of its SIMD.  Two groups of
+// waves half a tile apart (1190), operands four or five products ahead (1005 to
+// 1025) and the statistics and first operands of the second half read early
+// (990), all beside 1005 on that card, do not change that; at d = 64 K and V in
+// registers gain 3 %, not enough for a second form.
 template <typename IO, int D, int WK, int WR>
 __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1)) gdn2_attn_dkv_kernel(bwd_args a) {
   typedef tile<IO, D> TL;
