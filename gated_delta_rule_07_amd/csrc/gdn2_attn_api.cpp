@@ -399,16 +399,12 @@ gdn2_status_t gdn2_attn_bwd(const void *q, const void *k, const void *v, const v
   const hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e;
   {
-    prof_scope ps("attn_bwd_stat", s);
-    GDN2_ATTN_DISPATCH(e, dt, d, launch_attn_bwd_stat, z, p, workspace, s);
+    prof_scope ps("attn_bwd_dq", s);
+    GDN2_ATTN_DISPATCH(e, dt, d, launch_attn_bwd_dq, z, p, workspace, s);
   }
   if (e == hipSuccess) {
     prof_scope ps("attn_bwd_dkv", s);
     GDN2_ATTN_DISPATCH(e, dt, d, launch_attn_bwd_dkv, z, p, workspace, s);
-  }
-  if (e == hipSuccess) {
-    prof_scope ps("attn_bwd_dq", s);
-    GDN2_ATTN_DISPATCH(e, dt, d, launch_attn_bwd_dq, z, p, workspace, s);
   }
   return launched(fn, e);
 }

@@ -5,8 +5,11 @@
 //   dv_j = sum_i p_ij do_i;  dk_j = scale sum_i ds_ij q_i;
 //   dq_i = scale sum_j ds_ij k_j.
 //
-// Two kernels recompute p from the forward's lse: one owns key rows (dk, dv)
-// and walks the queries, one owns query rows (dq) and walks the keys.  That
+// Two kernels recompute p from the forward's lse: one owns query rows (dq) and
+// walks the keys, one owns key rows (dk, dv) and walks the queries; the first
+// also forms delta, from the rows of dO it holds, and leaves the rows'
+// statistics for the second (a pass of its own: 2170 us against 2146 for a step
+// at the sizes below, 54.5 against 52.3 for 1543 float32 tokens).  That
 // is seven products where one kernel with atomic additions into dq would do
 // five, and in exchange every sum has a fixed order (the same bits every run)
 // and no float32 copy of dq passes through memory.  The query rows are the
@@ -14,9 +17,8 @@
 // that share a key row is part of the same product.
 //
 // Measured, 8 x 4096 tokens, 16 heads on 4, d = 128, window 2048, bfloat16 (206
-// GFLOP a product; an 8192^3 product runs at 1212 TFLOP/s): statistics 50 us
-// (memory: 277 MB), dk and dv 940 to 1000 us (825 to 877 TFLOP/s), dq 575 to 595 us
-// (1040 to 1075 TFLOP/s).
+// GFLOP a product; an 8192^3 product runs at 1212 TFLOP/s): dq 590 to 610 us
+// (1010 to 1050 TFLOP/s), dk and dv 940 to 990 us (830 to 877 TFLOP/s).
 #include "gdn2_attn.hpp"
 
 namespace gdn2 {
@@ -36,32 +38,20 @@ struct bwd_args {
   order od;
 };
 
-// delta and the base-2 lse of every row, in row-tile order: D / 8 lanes a
-// row, 8 channels each.
-template <typename IO, int D> __global__ void __launch_bounds__(256) gdn2_attn_stat_kernel(bwd_args a) {
-  constexpr int LPR = D / 8, RPB = 256 / LPR;
-  const int j = threadIdx.x % LPR;
-  const size_t rows = static_cast<size_t>(a.Ttot) * a.Hq;
-  const size_t row = static_cast<size_t>(blockIdx.x) * RPB + threadIdx.x / LPR;
-  if (row >= rows)
-    return;
-  const size_t tok = row / static_cast<unsigned>(a.Hq);
-  if (a.cu && static_cast<long>(tok) >= a.cu[a.N])
-    return;  // behind the last sequence
-  const IO *o = static_cast<const IO *>(a.o) + row * D + 8 * j;
-  const IO *d = static_cast<const IO *>(a.dout) + row * D + 8 * j;
-  const f32x4 o0 = io<IO>::load4(o), o1 = io<IO>::load4(o + 4), d0 = io<IO>::load4(d), d1 = io<IO>::load4(d + 4);
-  float x = 0.f;
+// the sum of products of 8 values, in float32
+__device__ __forceinline__ float dot8(const frag8<bf16_t> &x, const frag8<bf16_t> &y) {
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    s += static_cast<float>(x.v[i]) * static_cast<float>(y.v[i]);
+  return s;
+}
+__device__ __forceinline__ float dot8(const frag8<float> &x, const frag8<float> &y) {
+  float s = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    x += o0[i] * d0[i] + o1[i] * d1[i];
-#pragma unroll
-  for (int s = 1; s < LPR; s <<= 1)
-    x += __shfl_xor(x, s, 64);
-  if (j == 0) {
-    const int head = static_cast<int>(row - tok * a.Hq), hk = head / a.G, g = head % a.G;
-    a.stat[(static_cast<size_t>(hk) * a.Ttot + tok) * a.G + g] = f32x2{a.lse[row] * LOG2E, x};
-  }
+    s += x.lo[i] * y.lo[i] + x.hi[i] * y.hi[i];
+  return s;
 }
 
 // The sequence of a workgroup's tile and the tile's first row in it (rows:
@@ -120,14 +110,20 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
   const int wr0 = row0 + 32 * wm < rows ? row0 + 32 * wm : rows - 1;
   const int wr1 = row0 + 32 * wm + 31 < rows ? row0 + 32 * wm + 31 : rows - 1;
   const int pos_lo = wr0 / a.G, pos_hi = wr1 / a.G;
-  const f32x2 st = a.stat[(static_cast<size_t>(hk) * a.Ttot + sq.start) * a.G + cl_row];
-
   frag8<IO> q[D / 16], d[D / 16];
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk) {
     q[kk] = load8<IO>(static_cast<const IO *>(a.q) + qrow * D + 16 * kk + 8 * h);
     d[kk] = load8<IO>(static_cast<const IO *>(a.dout) + qrow * D + 16 * kk + 8 * h);
   }
+  // the row's statistics, left for the dk, dv kernel too
+  f32x2 st = {a.lse[qrow] * LOG2E, 0.f};
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk)
+    st[1] += dot8(load8<IO>(static_cast<const IO *>(a.o) + qrow * D + 16 * kk + 8 * h), d[kk]);
+  st[1] += __shfl_xor(st[1], 32, 64);
+  if (h == 0 && wn == 0 && row_ok)
+    a.stat[(static_cast<size_t>(hk) * a.Ttot + sq.start) * a.G + cl_row] = st;
   // Tiles come straight from memory: position p of one is chunk (p % CPR) ^ f
   // of row p / CPR.
   const int sc = tid % CPR, sr0 = tid / CPR, wv = __builtin_amdgcn_readfirstlane(wave);
@@ -610,16 +606,6 @@ static void fill(bwd_args &a, const attn_sizes &z, const attn_ptrs &p, void *ws)
 }
 
 template <typename IO, int D>
-hipError_t launch_attn_bwd_stat(const attn_sizes &z, const attn_ptrs &p, void *ws, hipStream_t st) {
-  bwd_args a;
-  fill(a, z, p, ws);
-  const size_t rows = static_cast<size_t>(z.Ttot) * z.Hq;
-  constexpr int RPB = 256 / (D / 8);
-  hipLaunchKernelGGL((gdn2_attn_stat_kernel<IO, D>), dim3(static_cast<unsigned>((rows + RPB - 1) / RPB)), dim3(256), 0,
-                     st, a);
-  return hipGetLastError();
-}
-template <typename IO, int D>
 hipError_t launch_attn_bwd_dq(const attn_sizes &z, const attn_ptrs &p, void *ws, hipStream_t st) {
   bwd_args a;
   fill(a, z, p, ws);
@@ -662,9 +648,8 @@ hipError_t launch_attn_bwd_dkv(const attn_sizes &z, const attn_ptrs &p, void *ws
   return hipGetLastError();
 }
 
-#define GDN2_INST_ATTN_BWD(IO, D)                                                                           \
-  template hipError_t launch_attn_bwd_stat<IO, D>(const attn_sizes &, const attn_ptrs &, void *, hipStream_t); \
-  template hipError_t launch_attn_bwd_dq<IO, D>(const attn_sizes &, const attn_ptrs &, void *, hipStream_t);   \
+#define GDN2_INST_ATTN_BWD(IO, D)                                                                         \
+  template hipError_t launch_attn_bwd_dq<IO, D>(const attn_sizes &, const attn_ptrs &, void *, hipStream_t); \
   template hipError_t launch_attn_bwd_dkv<IO, D>(const attn_sizes &, const attn_ptrs &, void *, hipStream_t);
 GDN2_INST_ATTN_BWD(float, 64)
 GDN2_INST_ATTN_BWD(float, 128)

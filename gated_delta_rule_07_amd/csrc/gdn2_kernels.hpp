@@ -148,8 +148,8 @@ template <typename IO, typename CT, int D>
 hipError_t launch_attn_paged(const attn_sizes &z, const attn_ptrs &p, int splits, void *ws, hipStream_t st);
 template <typename IO, int D>
 hipError_t launch_attn_join(const attn_sizes &z, const attn_ptrs &p, int splits, void *ws, hipStream_t st);
-// Backward: per-row statistics into ws, then dq, then dk and dv.  ws holds the
-// statistics and, where attn_bwd_parts workgroups share a key tile's rows,
+// Backward: dq, which leaves the rows' statistics in ws, then dk and dv, which
+// read them.  ws holds the statistics and, where attn_bwd_parts workgroups share a key tile's rows,
 // their sums.
 int attn_bwd_parts(const attn_sizes &z);
 inline size_t attn_bwd_stat_bytes(const attn_sizes &z) {
@@ -159,8 +159,6 @@ inline size_t attn_bwd_bytes(const attn_sizes &z, int d) {
   const size_t parts = static_cast<size_t>(attn_bwd_parts(z));
   return attn_bwd_stat_bytes(z) + (parts > 1 ? parts * 2 * z.Ttot * z.Hk * d * 4 : 0);
 }
-template <typename IO, int D>
-hipError_t launch_attn_bwd_stat(const attn_sizes &z, const attn_ptrs &p, void *ws, hipStream_t st);
 template <typename IO, int D>
 hipError_t launch_attn_bwd_dq(const attn_sizes &z, const attn_ptrs &p, void *ws, hipStream_t st);
 template <typename IO, int D>
