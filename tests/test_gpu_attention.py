@@ -668,6 +668,52 @@ def test_training_step_in_a_graph(g):
     replay(step, [o, lse, ga["dv"], *gb.values()], lambda: g.attn_fwd(q0, k0, v))
 
 
+def test_two_calls_at_once(g):
+    """Calls on two streams, each with a workspace of its own, and two graphs
+    that take turns on one workspace, give the serial results."""
+    gn = gen(63)
+    B, T, Hq, Hk, d = 1, 1500, 8, 1, 128
+    x = [[randn(gn, (B, T, h, d), BF16) for h in (Hq, Hk, Hk, Hq)] for _ in range(2)]
+    kc, vc, _, _, _, _ = make_cache(g, gn, 200, Hk, 16, d, BF16, BF16)
+    table = torch.arange(200, dtype=torch.int32, device="cuda").view(2, 100).contiguous()
+    lens = torch.tensor([1600, 999], dtype=torch.int32, device="cuda")
+    qd = [randn(gn, (2, 1, Hq, d), BF16) for _ in range(2)]
+    need = max(g.attn_bwd_workspace_bytes(B, T, Hq, Hk, d), g.attn_paged_workspace_bytes(qd[0], kc, table))
+    ws = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in range(2)]
+
+    def step(i, w):
+        q, k, v, do = x[i]
+        o, lse = g.attn_fwd(q, k, v, window=700)
+        gr = g.attn_bwd(q, k, v, o, lse, do, window=700, workspace=w)
+        od, _ = g.attn_paged(qd[i], kc, vc, table, lens, workspace=w)
+        return [o, lse, gr["dq"], gr["dk"], gr["dv"], od]
+
+    want = [step(i, ws[0]) for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        got = [None, None]
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i] = step(i, ws[i])
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert all(torch.equal(a, b) for a, b in zip(got[i], want[i]))
+    graphs, outs = [], []
+    for i in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(step(i, ws[0]))
+        graphs.append(graph)
+    for _ in range(3):
+        for i in range(2):
+            for t in outs[i]:
+                t.fill_(7.0)
+            graphs[i].replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(outs[i], want[i]))
+
+
 def test_decode_step_in_a_graph(g):
     gn = gen(42)
     N, Hq, Hk, d, page, n = 4, 8, 2, 128, 32, 900
