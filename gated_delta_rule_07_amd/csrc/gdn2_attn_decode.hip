@@ -196,6 +196,9 @@ __global__ void __launch_bounds__(256, 3) gdn2_attn_decode_kernel(fwd_args a) {
           for (int x = 0; x < LK; ++x)
             rk[t][x] = rv[t][x] = u32x4{0u, 0u, 0u, 0u};
         }
+      // (0 times the scale of whatever row was read instead need not be 0)
+      if (F8 && (bad >> (lane >> 4) % TK & 1))
+        bk = bv = 127;
     }
     wave_order();
 #pragma unroll

@@ -209,6 +209,7 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
       int j = kb + SN * wn + st % SN;
       j = j < k1 ? j : k1 - 1;
       const bool ok = static_cast<unsigned>(ent_b) < static_cast<unsigned>(a.num_pages);
+      bad |= ok ? 0 : 1 << CH;
       const size_t off = ((static_cast<size_t>(ok ? ent_b : 0) * a.Hk + hk) << a.page_shift) + (j & pmask);
       bk = a.ks[off];
       bv = a.vs[off];
@@ -223,6 +224,9 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
         for (int i = 0; i < CH; ++i)
           if (bad >> i & 1)
             rk[i] = rv[i] = u32x4{0u, 0u, 0u, 0u};
+        // (0 times the scale of whatever row was read instead need not be 0)
+        if (F8 && (bad >> CH & 1))
+          bk = bv = 127;
       }
     }
 #pragma unroll
