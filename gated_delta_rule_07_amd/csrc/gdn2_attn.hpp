@@ -16,8 +16,8 @@
 // column r.
 #pragma once
 
+#include "gdn2_attn_kernels.hpp"
 #include "gdn2_device.hpp"
-#include "gdn2_kernels.hpp"
 
 namespace gdn2 {
 namespace attn {

@@ -9,8 +9,8 @@
 #include <cmath>
 #include <initializer_list>
 
+#include "gdn2_attn_kernels.hpp"
 #include "gdn2_host.hpp"
-#include "gdn2_kernels.hpp"
 
 using namespace gdn2::host;
 using gdn2::attn::attn_ptrs;

@@ -21,8 +21,8 @@
 // (336 MB, 5.6 TB/s), backward 109 us (503 MB, 4.6 TB/s) and 5 us for the sum of
 // the weight gradients' parts; a large copy runs at 4.7 TB/s.  32 tokens (a
 // decode step): 4 us, a launch's own latency.
+#include "gdn2_attn_kernels.hpp"
 #include "gdn2_device.hpp"
-#include "gdn2_kernels.hpp"
 
 namespace gdn2 {
 namespace attn {
