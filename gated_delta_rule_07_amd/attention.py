@@ -22,6 +22,7 @@ or ``torch.float8_e4m3fn`` with uint8 exponent bytes [pages, Hk, page size].
 from __future__ import annotations
 
 import math
+import operator
 
 import torch
 
@@ -93,6 +94,15 @@ def _packed(cu_seqlens, B) -> int:
     if B != 1:
         raise ValueError("packed sequences need B == 1")
     return cu_seqlens.numel() - 1
+
+
+def _window(window) -> int:
+    """A window as the C ABI's int, which a larger one would wrap around in:
+    one of 2^31 - 1 tokens hides nothing."""
+    window = operator.index(window)
+    if window < 0:
+        raise ValueError(f"negative window {window}")
+    return min(window, 2 ** 31 - 1)
 
 
 def _workspace(ws, need: int, dev: int):
@@ -216,6 +226,7 @@ def attn_fwd(q, k, v, cu_seqlens=None, window: int = 0, scale: float | None = No
     token's last ``window`` keys (itself included).  ``scale`` defaults to
     d^-0.5.  Returns (o, lse): lse float32 [B, T, Hq] is what the backward
     needs (None when ``want_lse`` is False and none is given)."""
+    window = _window(window)
     dev = _device(q, k, v, cu_seqlens)
     B, T, Hq, Hk, d = _heads(q, k, (v, "v"))
     ns = _packed(cu_seqlens, B)
@@ -242,6 +253,7 @@ def attn_bwd(q, k, v, o, lse, dout, cu_seqlens=None, window: int = 0, scale: flo
     """Backward of ``attn_fwd``: from its o and lse on the same inputs and
     dL/do, a dict with dq, dk, dv.  ``out`` may hold preallocated tensors
     under those names."""
+    window = _window(window)
     dev = _device(q, k, v, o, lse, dout, cu_seqlens)
     B, T, Hq, Hk, d = _heads(q, k, (v, "v"))
     ns = _packed(cu_seqlens, B)
@@ -324,7 +336,7 @@ def attn_paged_workspace_bytes(q, k_cache, block_table, cu_seqlens=None, window:
     B, T, Hq, d = q.shape
     ns = 0 if cu_seqlens is None else cu_seqlens.numel() - 1
     return int(lib().gdn2_attn_paged_workspace_bytes(B, T, Hq, k_cache.shape[1], d, ns, k_cache.shape[2],
-                                                     block_table.shape[1], window))
+                                                     block_table.shape[1], _window(window)))
 
 
 def attn_paged(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens=None, k_scale=None, v_scale=None,
@@ -336,6 +348,7 @@ def attn_paged(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens=None, k_sc
     ``cu_seqlens`` (a chunk of a prompt among single tokens, say);
     ``block_table`` int32 [N, max pages], ``seq_lens`` int32 [N] keys of each
     sequence, the new ones included.  Returns (o, lse or None)."""
+    window = _window(window)
     dev = _device(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, k_scale, v_scale)
     if q.dim() != 4:
         raise ValueError("q must be [N, T, Hq, d]")

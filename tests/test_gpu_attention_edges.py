@@ -1,13 +1,12 @@
 """Attention operators on an MI355X at the edges of what their documentation
-allows: table entries outside the cache beside a page of NaN, windows past the
-test_gpu_attention.py."""
+allows.  Bounds as in test_gpu_attention.py."""
 import math
 
 import pytest
 import torch
 
 import attention_ref as ref
-from test_gpu_attention import CACHES, g, gen, make_cache, randn  # noqa: F401
+from test_gpu_attention import BF16, CACHES, g, gen, make_cache, randn  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -38,3 +37,25 @@ def test_paged_bad_entries_beside_a_page_of_nan(g, T, dtype, cdt):
                           want_lse=True)
     r = ref.attn(q[0].double(), kd[:n], vd[:n], 0, d ** -0.5)
     ref.check_attn({"o": o[0], "lse": lse[0]}, r, dtype, n, d, f"new {T}")
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31, 2 ** 32 + 5, 2 ** 63])
+def test_window_past_the_range_of_an_int(g, window):
+    """A window longer than every sequence hides nothing, however long it is."""
+    gn = gen(73)
+    q, k, v, do = (randn(gn, (1, 300, h, 64), BF16) for h in (4, 2, 2, 4))
+    o, lse = g.attn_fwd(q, k, v)
+    gr = g.attn_bwd(q, k, v, o, lse, do)
+    ow, lw = g.attn_fwd(q, k, v, window=window)
+    gw = g.attn_bwd(q, k, v, o, lse, do, window=window)
+    assert torch.equal(o, ow) and torch.equal(lse, lw)
+    assert all(torch.equal(gr[n], gw[n]) for n in gr)
+    kc, vc, _, _, _, _ = make_cache(g, gn, 20, 2, 16, 64, BF16, BF16)
+    table = torch.arange(20, dtype=torch.int32, device="cuda")[None]
+    lens = torch.tensor([300], dtype=torch.int32, device="cuda")
+    for t in (1, 40):
+        x = q[:, :t].contiguous()
+        assert g.attn_paged_workspace_bytes(x, kc, table, window=window) == g.attn_paged_workspace_bytes(x, kc, table)
+        want, _ = g.attn_paged(x, kc, vc, table, lens)
+        got, _ = g.attn_paged(x, kc, vc, table, lens, window=window)
+        assert torch.equal(got, want)
