@@ -100,8 +100,9 @@ gdn2_status_t check_attn(const char *fn, int B, int T, int Hq, int Hk, int d, in
     return fail(GDN2_ERR_INVALID_ARGUMENT, "%s: num_seqs without cu_seqlens", fn);
   if (window < 0)
     return fail(GDN2_ERR_INVALID_ARGUMENT, "%s: negative window %d", fn, window);
-  if (!(scale > 0.f) || !std::isfinite(scale))
-    return fail(GDN2_ERR_INVALID_ARGUMENT, "%s: scale must be positive and finite", fn);
+  // (the kernels' exponents are in base 2, scale log2 e: finite too)
+  if (!(scale > 0.f) || !std::isfinite(scale * 1.4426950408889634f))
+    return fail(GDN2_ERR_INVALID_ARGUMENT, "%s: scale must be positive and at most 2.3e38", fn);
   const long long tot = static_cast<long long>(B) * T, N = packed ? num_seqs : B;
   // (a row tile's offsets within 128 tokens are 32-bit: 2^15 heads of 128)
   if (Hq > (1 << 15) || tot > MAX_ROWS || tot * Hq > MAX_ROWS || N * Hk > MAX_UNITS)

@@ -463,7 +463,7 @@ gdn2_status_t gdn2_qk_norm_rope_bwd(const void *q, const void *k, const float *w
  *   sequence, with window > 0 only those with j > i - window.
  *   cu_seqlens, B, T, num_seqs : as for gdn2_chunk_fwd.
  *   window    : 0 for none.
- *   scale     : positive and finite.
+ *   scale     : positive, at most 2.3e38.
  *   lse       : [B, T, Hq] float32, ln sum_j exp(scale q_i . k_j), or NULL.
  * An infinity or NaN in a token's key or value reaches the rows that see it
  * and no others. */
