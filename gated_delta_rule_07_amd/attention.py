@@ -311,7 +311,8 @@ def kv_cache_write(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None) ->
 
 def kv_cache_read(slots, k_cache, v_cache, k_scale=None, v_scale=None, dtype=None, out=None):
     """The keys and values of ``slots`` (int64 [n]), each [n, Hk, d] of
-    ``dtype`` (a quantised cache: bfloat16 by default, both exact; else the
+    ``dtype`` (a quantised cache: bfloat16 by default, both exact, but for
+    float32 rows under 2^-116, whose smallest values bfloat16 rounds; else the
     cache's own).  A slot outside the cache reads as zeros.  ``out``:
     preallocated (k, v).  Returns (k, v)."""
     dev = _device(slots, k_cache, v_cache, k_scale, v_scale)

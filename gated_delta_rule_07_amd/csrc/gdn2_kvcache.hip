@@ -8,8 +8,9 @@
 //   e = the smallest integer with max |x| <= 448 * 2^e  (at least -126),
 // so that scaling is exact in both directions: the only rounding is the
 // code's own (to nearest even, 2^-4 relative at most half a step), and what
-// is read back, code * 2^e, is exact in bfloat16 and float32.  A row holding
-// an infinity or NaN gets the byte 255 and reads back as NaN.
+// is read back, code * 2^e, is exact in float32, and in bfloat16 for e >= -124
+// (codes are multiples of 2^-9, bfloat16's smallest subnormal is 2^-133).  A row
+// holding an infinity or NaN gets the byte 255 and reads back as NaN.
 //
 // The bound is memory: one read and one write per value.  D / 8 lanes hold a
 // row, 8 values (16 bytes of bfloat16) each, so a row's maximum takes 3 or 4

@@ -491,8 +491,10 @@ gdn2_status_t gdn2_attn_bwd(const void *q, const void *k, const void *v, const v
  * page_size] bytes, hold for every row (token, kv head) the byte e + 127 of
  * its scale 2^e, e the smallest integer >= -126 with max |x| <= 448 * 2^e
  * (127 for a row of zeros), and the codes are x * 2^-e rounded to nearest
- * even: code * 2^e is exact in float32 and bfloat16.  A row holding an
- * infinity or NaN gets the byte 255 and stands for NaN throughout.
+ * even: code * 2^e is exact in float32, and in bfloat16 for e >= -124 or rows
+ * that were bfloat16 (else, largest magnitude up to 448 * 2^-125, the smallest
+ * codes may lie under its smallest subnormal and are rounded once).  A row
+ * holding an infinity or NaN gets the byte 255 and stands for NaN throughout.
  *
  * gdn2_kv_cache_write stores n tokens' keys and values, [n, Hk, d], into
  * slots[0 .. n-1] (int64); a slot outside the cache is skipped (a padded

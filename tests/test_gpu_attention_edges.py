@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import attention_ref as ref
-from test_gpu_attention import BF16, CACHES, g, gen, make_cache, randn  # noqa: F401
+from test_gpu_attention import BF16, CACHES, F8, F32, g, gen, make_cache, randn  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -59,3 +59,36 @@ def test_window_past_the_range_of_an_int(g, window):
         want, _ = g.attn_paged(x, kc, vc, table, lens)
         got, _ = g.attn_paged(x, kc, vc, table, lens, window=window)
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_cache_rows_of_the_smallest_exponents(g, dtype):
+    """Rows down to the format's smallest scale, 2^-126, whose codes are
+    multiples of 2^-135: exact in float32 always, in bfloat16 (smallest
+    subnormal 2^-133) from e = -124 up and rounded once below."""
+    gn = gen(74)
+    d, page, Hk = 64, 16, 2
+    es = torch.arange(-131, -115, device="cuda")
+    n = es.numel()
+    top = torch.exp2(es.double() + 8.5)[:, None, None]     # a row's largest value: between 448 2^(e-1) and 448 2^e
+    x = torch.rand((n, Hk, d), generator=gn, device="cuda", dtype=torch.float64) * 2 - 1
+    x[..., 0] = 1
+    k = (x * top).to(dtype)
+    kc, vc = (torch.zeros((1, Hk, page, d), device="cuda").to(F8) for _ in range(2))
+    ks, vs = (torch.zeros((1, Hk, page), dtype=torch.uint8, device="cuda") for _ in range(2))
+    slots = torch.arange(n, device="cuda")
+    g.kv_cache_write(k, k, slots, kc, vc, ks, vs)
+    val, byte = ref.quantise(k.double())
+    assert torch.equal(ks[0].t(), byte) and torch.equal(vs[0].t(), byte)
+    e = byte.int() - 127
+    assert e.min() == -126 and e.max() > -120
+    for y in g.kv_cache_read(slots, kc, vc, ks, vs, dtype=F32):
+        assert torch.equal(y.double(), val)
+    for y in g.kv_cache_read(slots, kc, vc, ks, vs, dtype=BF16):
+        off = (y.double() - val).abs()
+        assert (off[e >= -124] == 0).all()
+        assert (off <= 2.0 ** -134).all()
+        # (rows that were bfloat16: a multiple of 2^-133 is 4 m steps of 2^-135,
+        # and rounding that to a code's grid, steps of 1, 2, 4, .., leaves a
+        # multiple of 4: always exact)
+        assert (off > 0).any() == (dtype == F32)
