@@ -1,0 +1,98 @@
+"""The attention kernels' variants on an MI355X, each at shapes that select it:
+the rules that pick a variant are read from the sources, so that a changed
+threshold fails here rather than leaving a variant untested.  Bounds as in
+test_gpu_attention.py."""
+import math
+import os
+import re
+
+import pytest
+import torch
+
+import attention_ref as ref
+from test_gpu_attention import BF16, F32, g, gen, randn, run_attn  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def source(name):
+    import gated_delta_rule_07_amd as mod
+    with open(os.path.join(os.path.dirname(mod.LIB_PATH), "csrc", name)) as f:
+        return f.read()
+
+
+def rows_128(units, tiles):
+    """Whether a whole-sequence call (forward, dq) of this many 128-row tiles
+    takes the 128-row kernels (few_tiles)."""
+    n = re.search(r"bool few_tiles\(const order &od\) \{ return static_cast<long long>\(od\.units\) \* od\.tiles < (\d+); \}",
+                  source("gdn2_attn.hpp"))
+    return units * tiles >= int(n.group(1))
+
+
+def fixed_128(B, T, Hq, Hk):
+    return rows_128(B * Hk, -(-T * (Hq // Hk) // 128))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("window", [0, 2048])
+def test_128_row_tiles_long(g, window, d, dtype):
+    """Forward and backward over many unmasked key tiles."""
+    B, T, Hq, Hk = 1, 4096, 16, 4
+    assert fixed_128(B, T, Hq, Hk)
+    print(f"128-row tiles, T={T} window={window} d={d} {dtype}", flush=True)
+    run_attn(g, [T] * B, Hq, Hk, d, dtype, window, False, True, seed=81)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [64, 128])
+def test_128_row_tiles_packed(g, d, dtype):
+    lens, Hq, Hk = [1300, 0, 1, 777, 2000, 129], 8, 2
+    assert rows_128(Hk, sum(lens) * (Hq // Hk) // 128 + len(lens))
+    for window in (0, 500):
+        print(f"128-row tiles, packed window={window} d={d} {dtype}", flush=True)
+        run_attn(g, lens, Hq, Hk, d, dtype, window, True, True, seed=82, tail=21)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_128_row_tiles_large_scores(g, dtype):
+    """Scores of hundreds: one key takes all the weight."""
+    gn = gen(83)
+    B, T, Hq, Hk, d = 16, 210, 16, 4, 64
+    assert fixed_128(B, T, Hq, Hk)
+    print(f"128-row tiles, large scores {dtype}", flush=True)
+    q, k, v = (randn(gn, (B, T, h, d), dtype) * 30 for h in (Hq, Hk, Hk))
+    o, lse = g.attn_fwd(q, k, v)
+    for b in range(B):
+        r = ref.attn(q[b].double(), k[b].double(), v[b].double(), 0, d ** -0.5)
+        ref.check_attn({"o": o[b], "lse": lse[b]}, r, dtype, T, d, f"large {b}")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("window", [0, 40])
+def test_128_row_tiles_nonfinite_values_reach_only_their_rows(g, window, bad, dtype):
+    gn = gen(84)
+    B, T, Hq, Hk, d, b, at = 16, 210, 16, 4, 128, 5, 101
+    G = Hq // Hk
+    assert fixed_128(B, T, Hq, Hk)
+    q, k, v = (randn(gn, (B, T, h, d), dtype) for h in (Hq, Hk, Hk))
+    clean, _ = g.attn_fwd(q, k, v, window=window)
+    for which in ("k", "v"):
+        print(f"128-row tiles, {bad} in {which} window={window} {dtype}", flush=True)
+        k2, v2 = k.clone(), v.clone()
+        (k2 if which == "k" else v2)[b, at, 0, 5] = bad
+        o, _ = g.attn_fwd(q, k2, v2, window=window)
+        see = torch.zeros((B, T, Hq), dtype=torch.bool, device="cuda")
+        see[b, at:(at + window if window else T), :G] = True
+        # rows that do not see the key: the same bits
+        assert torch.equal(o[~see], clean[~see]), which
+        if which == "v":
+            x = o[see][:, 5].float()
+            want = torch.full_like(x, bad)
+            assert torch.equal(torch.isnan(x), torch.isnan(want))
+            assert (torch.isnan(want) | (x == want)).all()
+            rest = [c for c in range(d) if c != 5]
+            # the same weights: the sums may differ by the order of a term
+            a, c = o[see][:, rest].double(), clean[see][:, rest].double()
+            assert ((a - c).abs() <= 2.0 ** -7 * c.abs() + 2.0 ** -9).all()
