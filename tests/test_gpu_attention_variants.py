@@ -96,3 +96,51 @@ def test_128_row_tiles_nonfinite_values_reach_only_their_rows(g, window, bad, dt
             # the same weights: the sums may differ by the order of a term
             a, c = o[see][:, rest].double(), clean[see][:, rest].double()
             assert ((a - c).abs() <= 2.0 ** -7 * c.abs() + 2.0 ** -9).all()
+
+
+def whole_key_tiles(T, B, Hq, Hk, keys):
+    """Whether dk and dv of a fixed-length call take the form of `keys` keys a
+    workgroup, without parts: a rule on the number of its key tiles."""
+    s = source("gdn2_attn_bwd.hip")
+    n = re.search(r"a\.parts == 1 && static_cast<long long>\(a\.od\.units\) \* a\.od\.tiles >= (\d+)", s)
+    p = re.search(r"long long p = \((\d+) \+ tiles - 1\) / \(tiles > 0 \? tiles : 1\);\s+if \(p > rows / (\d+)\)\s+p = rows / (\d+);", s)
+    assert p.group(2) == p.group(3)
+    tiles = B * -(-T // 64) * Hk
+    parts = max(1, min((int(p.group(1)) + tiles - 1) // tiles, T * (Hq // Hk) // int(p.group(2)), 16))
+    return parts == 1 and B * Hk * -(-T // keys) >= int(n.group(1))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [64, 128])
+def test_dkv_whole_key_tiles(g, d, dtype):
+    """dk and dv where there are key tiles enough for the larger form: 128
+    keys a workgroup in bfloat16, 64 in float32."""
+    B, T, Hq, Hk = 64, 130, 16, 8
+    assert fixed_128(B, T, Hq, Hk) and whole_key_tiles(T, B, Hq, Hk, 128 if dtype == BF16 else 64)
+    for window in (0, 100):
+        print(f"dk, dv of whole key tiles, window={window} d={d} {dtype}", flush=True)
+        run_attn(g, [T] * B, Hq, Hk, d, dtype, window, False, True, seed=85)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [64, 128])
+def test_dkv_whole_key_tiles_packed(g, d, dtype):
+    """The same, packed: sequences of up to several key tiles, empty ones, and
+    groups of heads that a row tile does not divide (5 of 64 rows)."""
+    lens = [(97 * i * i + 13) % 401 if i % 7 else 0 for i in range(90)]
+    Hq, Hk = 40, 8
+    assert whole_key_tiles(sum(lens), 1, Hq, Hk, 128 if dtype == BF16 else 64)
+    for window in (0, 130):
+        print(f"dk, dv of whole key tiles, packed window={window} d={d} {dtype}", flush=True)
+        run_attn(g, lens, Hq, Hk, d, dtype, window, True, True, seed=86, tail=3)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("window", [1, 64, 1000])
+def test_dkv_parts_under_a_window(g, window, dtype):
+    """Few key tiles whose rows several workgroups share while the window
+    leaves them few rows each, or none."""
+    T, Hq, Hk, d = 2300, 8, 1, 128
+    assert g.attn_bwd_workspace_bytes(1, T, Hq, Hk, d) > -(-T * Hq * 8 // 256) * 256  # parts
+    print(f"dk, dv in parts, window={window} {dtype}", flush=True)
+    run_attn(g, [T], Hq, Hk, d, dtype, window, False, True, seed=window)
