@@ -10,7 +10,7 @@ import pytest
 import torch
 
 import attention_ref as ref
-from test_gpu_attention import BF16, F32, g, gen, randn, run_attn  # noqa: F401
+from test_gpu_attention import BF16, CACHES, F32, g, gen, randn, run_attn, run_paged  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -144,3 +144,38 @@ def test_dkv_parts_under_a_window(g, window, dtype):
     assert g.attn_bwd_workspace_bytes(1, T, Hq, Hk, d) > -(-T * Hq * 8 // 256) * 256  # parts
     print(f"dk, dv in parts, window={window} {dtype}", flush=True)
     run_attn(g, [T], Hq, Hk, d, dtype, window, False, True, seed=window)
+
+
+def paged_rows(Ttot, N, Hq, Hk, T=None):
+    """Rows of a paged call's tiles: 16 (the decode kernel, bfloat16, T tokens
+    for every sequence), 32 or 128."""
+    s = source("gdn2_attn_fwd.hip")
+    few = int(re.search(r"z\.Ttot\) \* \(z\.Hq / z\.Hk\) <= (\d+)LL \* z\.N", s).group(1))
+    dec = int(re.search(r"!z\.packed && static_cast<long long>\(z\.T\) \* \(z\.Hq / z\.Hk\) <= (\d+)", s).group(1))
+    if T is not None and T * (Hq // Hk) <= dec:
+        return 16
+    return 32 if Ttot * (Hq // Hk) <= few * N else 128
+
+
+@pytest.mark.parametrize("dtype,cdt", CACHES)
+@pytest.mark.parametrize("d", [64, 128])
+def test_paged_32_row_tiles(g, d, dtype, cdt):
+    """17 to 32 rows for every sequence (speculative steps)."""
+    for T, Hq, Hk, page, window in ((5, 8, 2, 16, 0), (8, 8, 2, 64, 50), (1, 20, 1, 32, 0), (6, 15, 3, 16, 333)):
+        lk = [T, 50, 700, 1, 2049]
+        assert paged_rows(T * len(lk), len(lk), Hq, Hk, T) == 32
+        print(f"paged 32-row tiles T={T} Hq={Hq} Hk={Hk} page={page} W={window} d={d} {dtype} {cdt}", flush=True)
+        run_paged(g, [T] * len(lk), lk, Hq, Hk, d, page, dtype, cdt, window, False, seed=T, poison=True)
+
+
+@pytest.mark.parametrize("dtype,cdt", CACHES)
+@pytest.mark.parametrize("d", [64, 128])
+def test_paged_32_row_tiles_packed(g, d, dtype, cdt):
+    """Packed batches of single tokens, and of a few tokens each."""
+    for lq, lk, Hq, Hk, page, window, tail in (([1] * 9, [1, 15, 16, 17, 300, 64, 2000, 33, 128], 8, 2, 16, 0, 0),
+                                               ([1] * 70, [(37 * i * i + 1) % 200 + 1 for i in range(70)], 8, 2, 32, 60, 7),
+                                               ([1, 2, 0, 3, 1], [700, 420, 33, 2, 0], 8, 2, 64, 0, 13),
+                                               ([1, 2, 0, 3, 1], [700, 420, 33, 2, 5], 16, 1, 256, 77, 3)):
+        assert paged_rows(sum(lq) + tail, len(lq), Hq, Hk) == 32
+        print(f"paged 32-row tiles packed n={len(lq)} Hq={Hq} Hk={Hk} page={page} W={window} d={d} {dtype} {cdt}", flush=True)
+        run_paged(g, lq, lk, Hq, Hk, d, page, dtype, cdt, window, True, seed=page, tail=tail, poison=True)
