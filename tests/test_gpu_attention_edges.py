@@ -92,3 +92,43 @@ def test_cache_rows_of_the_smallest_exponents(g, dtype):
         # and rounding that to a code's grid, steps of 1, 2, 4, .., leaves a
         # multiple of 4: always exact)
         assert (off > 0).any() == (dtype == F32)
+
+
+@pytest.mark.parametrize("Hq,Hk,T", [(1 << 15, 1 << 15, 130), (1 << 15, 1, 3), (1 << 15, 1 << 12, 40)])
+def test_most_query_heads(g, Hq, Hk, T):
+    """2^15 query heads, each its own kv head or sharing: some heads of every
+    part against float64."""
+    gn = gen(75)
+    d, G = 64, Hq // Hk
+    print(f"most heads Hq={Hq} Hk={Hk} T={T}", flush=True)
+    q, k, v, do = (randn(gn, (1, T, h, d), BF16) for h in (Hq, Hk, Hk, Hq))
+    o, lse = g.attn_fwd(q, k, v)
+    gr = g.attn_bwd(q, k, v, o, lse, do)
+    for h in sorted({0, Hk // 2, Hk - 1}):
+        hq = slice(h * G, (h + 1) * G)
+        r = ref.attn(q[0, :, hq].double(), k[0, :, h:h + 1].double(), v[0, :, h:h + 1].double(), 0, d ** -0.5,
+                     do[0, :, hq].double())
+        ref.check_attn({"o": o[0, :, hq], "lse": lse[0, :, hq], "dq": gr["dq"][0, :, hq]}, r, BF16, T, d, f"head {h}")
+        # a kv head's gradients sum T G terms, not T
+        ref.check_attn({"o": o[0, :, hq], "dk": gr["dk"][0, :, h:h + 1], "dv": gr["dv"][0, :, h:h + 1]}, r, BF16, T * G, d,
+                       f"kv head {h}")
+
+
+def test_cache_slots_read_twice_and_far_away(g):
+    """A slot may be read more than once; slots far outside read as zeros and
+    are not written."""
+    gn = gen(76)
+    Hk, page, d, n = 3, 16, 128, 40
+    for dtype, cdt in CACHES:
+        kc, vc, ks, vs, kd, vd = make_cache(g, gn, 4, Hk, page, d, dtype, cdt)
+        far = [-(1 << 63), -(1 << 32), -1, 4 * page, 1 << 31, 1 << 32, (1 << 32) + 5, (1 << 63) - 1]
+        slots = torch.cat([torch.tensor(far, device="cuda"), torch.arange(n, device="cuda"), torch.full((n,), 7, device="cuda")])
+        keep = [x.clone() for x in (kc.view(torch.uint8), vc.view(torch.uint8))]
+        x = randn(gn, (len(far), Hk, d), dtype)
+        g.kv_cache_write(x, x, slots[:len(far)].contiguous(), kc, vc, ks, vs)
+        assert torch.equal(kc.view(torch.uint8), keep[0]) and torch.equal(vc.view(torch.uint8), keep[1])
+        for y, c in zip(g.kv_cache_read(slots, kc, vc, ks, vs, dtype=dtype), (kd, vd)):
+            m = len(far)
+            assert (y[:m] == 0).all()
+            assert torch.equal(y[m:m + n].double(), c[:n])
+            assert torch.equal(y[m + n:].double(), c[7].expand(n, Hk, d))
