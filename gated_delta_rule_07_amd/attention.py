@@ -131,7 +131,10 @@ def rope_frequencies(rotary_dim: int, theta: float = 10000.0, scaling: str | Non
                 original_length are interpolated, those with more than
                 beta_fast keep f_j, in between the two are mixed linearly in
                 the number of turns (YaRN, arXiv:2309.00071, section 3.2; its
-                attention temperature goes into ``scale``)."""
+                attention temperature goes into ``scale``).  Checkpoints
+                trained with a mix that is linear in the pair's index between
+                two correction indices have other frequencies in between:
+                give ``freqs`` their own table."""
     if rotary_dim <= 0 or rotary_dim % 8:
         raise ValueError("rotary_dim must be a positive multiple of 8")
     if not factor > 0:
@@ -346,7 +349,8 @@ def attn_paged(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens=None, k_sc
     """Attention of new tokens over a paged cache that already holds their own
     keys and values (``kv_cache_write``).  q [N, T, Hq, d] (T new tokens for
     each of N sequences; decode is T = 1) or packed [1, T, Hq, d] with
-    ``cu_seqlens`` (a chunk of a prompt among single tokens, say);
+    ``cu_seqlens`` (a chunk of a prompt among single tokens, say; a batch of
+    single tokens alone runs faster unpacked);
     ``block_table`` int32 [N, max pages], ``seq_lens`` int32 [N] keys of each
     sequence, the new ones included.  Returns (o, lse or None)."""
     window = _window(window)

@@ -436,7 +436,10 @@ gdn2_status_t gdn2_decode_step(const void *q, const void *k, const void *v, cons
  *               reduced in 64 bits, so far positions keep their precision.
  *   positions : [B, T] int32, any values, or NULL for 0 .. T-1 in every row.
  *   rotary_dim: a multiple of 8, 0 .. d.
- *   eps       : >= 0 (a row of zeros with eps = 0 gives NaN).
+ *   eps       : >= 0 (a row of zeros with eps = 0 gives NaN).  The squares are
+ *               summed in float32: a row whose sum of squares passes 3.4e38
+ *               comes out as zeros, and with eps = 0 rows below 1e-19 lose
+ *               accuracy.
  *   q_out, k_out : outputs; may be q and k themselves. */
 gdn2_status_t gdn2_qk_norm_rope_fwd(const void *q, const void *k, const float *wq, const float *wk,
                                     const double *freqs, const int32_t *positions, int B, int T, int Hq, int Hk, int d,
@@ -466,7 +469,8 @@ gdn2_status_t gdn2_qk_norm_rope_bwd(const void *q, const void *k, const float *w
  *   scale     : positive, at most 2.3e38.
  *   lse       : [B, T, Hq] float32, ln sum_j exp(scale q_i . k_j), or NULL.
  * An infinity or NaN in a token's key or value reaches the rows that see it
- * and no others. */
+ * and no others.  A row whose visible scores are all -inf counts as one that
+ * sees nothing: o = 0, lse = -inf. */
 gdn2_status_t gdn2_attn_fwd(const void *q, const void *k, const void *v, const int32_t *cu_seqlens, int B, int T,
                             int Hq, int Hk, int d, int num_seqs, int window, float scale, gdn2_dtype_t dt, void *o,
                             float *lse, void *stream);
@@ -524,7 +528,8 @@ size_t gdn2_attn_paged_workspace_bytes(int B, int T, int Hq, int Hk, int d, int 
  * and see keys as in gdn2_attn_fwd.  q and o are [B, T, Hq, d] (T new tokens
  * for each of B sequences; decode is T = 1) or packed by cu_seqlens
  * [1, T, Hq, d].  A query at a negative position (more new tokens than keys,
- * seq_lens[n] = 0 for padding) sees nothing: o = 0, lse = -inf.  A table entry
+ * seq_lens[n] = 0 for padding) sees nothing: o = 0, lse = -inf.  Batches of
+ * single tokens run faster as [B, 1, Hq, d] than packed.  A table entry
  * outside the cache stands for a page of zeros; entries that no query sees
  * (behind seq_lens, before the window) are not read, and a table of no pages
  * may be NULL.  lse [B, T, Hq] float32 or NULL.  max_pages * page_size <= 2^28.

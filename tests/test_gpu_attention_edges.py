@@ -132,3 +132,28 @@ def test_cache_slots_read_twice_and_far_away(g):
             assert (y[:m] == 0).all()
             assert torch.equal(y[m:m + n].double(), c[:n])
             assert torch.equal(y[m + n:].double(), c[7].expand(n, Hk, d))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("B", [1, 32])
+def test_rows_whose_scores_are_all_minus_infinity(g, B, dtype):
+    """Such a row counts as one that sees nothing: o = 0, lse = -inf, in the
+    32-row and the 128-row kernels and over the cache."""
+    gn = gen(77)
+    T, Hq, Hk, d, n = 210, 16, 4, 64, 3
+    q, k, v = (randn(gn, (B, T, h, d), dtype) for h in (Hq, Hk, Hk))
+    q[:, :, :, 5] = 1
+    k[:, :n, :, 5] = -math.inf
+    o, lse = g.attn_fwd(q, k, v)
+    assert (o[:, :n] == 0).all() and (lse[:, :n] == -math.inf).all()
+    r = ref.attn(q[0, n:].double(), k[0, n:].double(), v[0, n:].double(), 0, d ** -0.5)
+    ref.check_attn({"o": o[0, n:], "lse": lse[0, n:]}, r, dtype, T, d, "rows that see other keys")
+    kc, vc = (torch.zeros((B, Hk, 16, d), device="cuda").to(dtype) for _ in range(2))
+    slots = (torch.arange(B, device="cuda")[:, None] * 16 + torch.arange(n, device="cuda")).reshape(-1)
+    kn, vn = (x[:, :n].contiguous() for x in (k, v))
+    g.kv_cache_write(kn, vn, slots, kc, vc)
+    table = torch.arange(B, dtype=torch.int32, device="cuda")[:, None].contiguous()
+    for t in (1, n, 60):   # (60: rows without any key too)
+        lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+        o, lse = g.attn_paged(q[:, :t].contiguous(), kc, vc, table, lens, want_lse=True)
+        assert (o == 0).all() and (lse == -math.inf).all()
