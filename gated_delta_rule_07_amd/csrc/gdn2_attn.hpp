@@ -321,7 +321,10 @@ __device__ __forceinline__ span packed_span(const int32_t *cu, int n, int T) {
 // with its own L2: the tiles of one unit (a sequence's kv head, which reads
 // the same keys and values) are kept on one die, or, with fewer than 8 (or
 // an odd number of) units, dealt out over 8 / gcd dies.  Later tiles see more
-// keys, so each die starts with its last ones.
+// keys, so each die starts with its last ones.  A unit of fewer tiles than 8 / gcd
+// leaves dies without work: units that are no multiple of 8 and have few tiles
+// run on a part of the chip (decode of 2048 keys each, e4m3: 1024 sequences on one kv
+// head 106 us, 1025 452; 172 sequences on three kv heads 71, 171 240).
 struct order {
   int units, tiles, g, tpr;  // g = gcd(units, 8), tpr = ceil(tiles / (8 / g))
 };

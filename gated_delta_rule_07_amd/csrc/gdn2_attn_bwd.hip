@@ -563,11 +563,17 @@ template <typename IO, int D> __global__ void __launch_bounds__(256) gdn2_attn_d
 // ------------------------------------------------------------- launchers --
 // Workgroups that share a 64-key tile's rows: where a call has few key tiles
 // (few tokens, or one kv head for many query heads), enough for 1024 of them,
-// at most 16 and at least 1024 rows each.  (4096 tokens, 16 query heads on one
+// at most 16 and at most one for every 1024 rows of the call, whether or not a
+// window or a sequence's end hides rows from a tile.  (4096 tokens, 16 query heads on one
 // kv head, d = 128: dk and dv 1867 us with one, 320 with 16; 11 packed
 // sequences, 9973 tokens, 12 heads on 4, d = 64: 166 with one, 130 with two;
 // 1543 float32 tokens, 4 heads on 4: 22 with one, 34 with three.)  The rule sees
-// the sizes the workspace is asked for: tokens and heads, no sequence lengths.
+// the sizes the workspace is asked for: tokens and heads, no sequence lengths
+// and no window.  Counting only the rows a window leaves a tile gains where
+// the parts' sums outweigh the call and loses where few tiles need the parts:
+// 4096 tokens, d = 128, 4 heads on 4, window 100: 42 us as it is, 20 counted so;
+// 16 heads on one, window 64: 49 and 72, window 512: 79 and 98; 16 on 2, d = 64,
+// window 256: 49 and 30.
 int attn_bwd_parts(const attn_sizes &z) {
   const long long seqs = z.packed ? 1 : z.N;
   const long long tiles = seqs * ((z.T + 63) / 64) * z.Hk, rows = static_cast<long long>(z.T) * (z.Hq / z.Hk);

@@ -26,8 +26,8 @@
 // 3.75 ms) and the two waves a SIMD that registers allow (the products are busy
 // 46 % of the cycles, 56 % with the softmax taken out, shared memory 23 %; a
 // deeper read-ahead changes nothing).  Measured: one
-// sequence of 32768 tokens, 16 heads on 4, d = 128, bfloat16: 4.3 to 4.4 ms,
-// 1000 to 1020 TFLOP/s (an 8192^3 product: 1212; without tiles straight from
+// sequence of 32768 tokens, 16 heads on 4, d = 128, bfloat16: 4.3 to 4.5 ms,
+// 975 to 1020 TFLOP/s (an 8192^3 product: 1212; without tiles straight from
 // memory 4650 us, without read-ahead and with a rescale every tile 4880); 8 x
 // 4096 tokens, window 2048: 480 to 500 us.  Paged, 1024 tokens at 12000 keys among
 // 23 single tokens: 105 us with the join's 10 (341 MB: 73 us at a copy's rate).
@@ -348,7 +348,8 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
     mx = half_max(mx) * a.c;
     // The reference of a row's exponents stays while its maximum is not more
     // than 8 above it (weights up to 2^8: no loss, they are floating point),
-    // so that most tiles rescale nothing.
+    // so that most tiles rescale nothing.  (A published refinement of the running
+    // maximum: the rescale is conditional on how far it rose.)
     const bool up = mx > m + 8.f;
     if (__any(up)) {
       const float m_new = up ? mx : m;
@@ -577,7 +578,9 @@ static bool few_rows(const attn_sizes &z) {
   return static_cast<long long>(z.Ttot) * (z.Hq / z.Hk) <= 32LL * z.N;
 }
 // At most 16 rows for every sequence and kv head: the decode kernel
-// (bfloat16), with 16-row products.
+// (bfloat16), with 16-row products.  Packed calls have their sequences' lengths on
+// the device only and take the 32-row kernel even if all are single tokens (64
+// sequences of 4K to 16K keys, e4m3: 133 us with T = 1, 150 packed).
 static bool decode_rows(const attn_sizes &z) {
   return !z.packed && static_cast<long long>(z.T) * (z.Hq / z.Hk) <= 16;
 }
