@@ -98,6 +98,16 @@ def configure(L: ctypes.CDLL) -> ctypes.CDLL:
     L.gdn2_attn_paged_workspace_bytes.argtypes = [i] * 9
     L.gdn2_attn_paged.restype = i
     L.gdn2_attn_paged.argtypes = [vp] * 8 + [i] * 10 + [f, i, i, vp, vp, vp, sz, vp]
+    L.gdn2_attn_sink_fwd.restype = i
+    L.gdn2_attn_sink_fwd.argtypes = [vp] * 4 + [i] * 8 + [f, i, vp, vp, vp]
+    L.gdn2_attn_sink_bwd_workspace_bytes.restype = sz
+    L.gdn2_attn_sink_bwd_workspace_bytes.argtypes = [i] * 7
+    L.gdn2_attn_sink_bwd.restype = i
+    L.gdn2_attn_sink_bwd.argtypes = [vp] * 7 + [i] * 8 + [f, i, vp, vp, vp, vp, sz, vp]
+    L.gdn2_attn_sink_paged_workspace_bytes.restype = sz
+    L.gdn2_attn_sink_paged_workspace_bytes.argtypes = [i] * 10
+    L.gdn2_attn_sink_paged.restype = i
+    L.gdn2_attn_sink_paged.argtypes = [vp] * 8 + [i] * 11 + [f, i, i, vp, vp, vp, sz, vp]
     L.gdn2_kv_cache_write.restype = i
     L.gdn2_kv_cache_write.argtypes = [vp] * 3 + [i] * 7 + [vp] * 5
     L.gdn2_kv_cache_read.restype = i

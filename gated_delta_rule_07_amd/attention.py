@@ -105,6 +105,14 @@ def _window(window) -> int:
     return min(window, 2 ** 31 - 1)
 
 
+def _sinks(sinks) -> int:
+    """A number of sinks as the C ABI's int (one of 2^31 - 1 tokens or more is every token)."""
+    sinks = operator.index(sinks)
+    if sinks < 0:
+        raise ValueError(f"negative number of sinks {sinks}")
+    return min(sinks, 2 ** 31 - 1)
+
+
 def _workspace(ws, need: int, dev: int):
     """(tensor or None, bytes) of a given workspace, or of a new one."""
     if ws is None:
@@ -224,12 +232,12 @@ def qk_norm_rope_bwd(q, k, freqs, dq_out, dk_out, wq=None, wk=None, positions=No
 
 # ------------------------------------------------------------ whole sequences
 def attn_fwd(q, k, v, cu_seqlens=None, window: int = 0, scale: float | None = None, out=None, lse=None,
-             want_lse: bool = True):
+             want_lse: bool = True, sinks: int = 0):
     """Causal attention over whole sequences, with ``window`` > 0 over each
-    token's last ``window`` keys (itself included).  ``scale`` defaults to
-    d^-0.5.  Returns (o, lse): lse float32 [B, T, Hq] is what the backward
+    token's last ``window`` keys (itself included) and its sequence's first
+    ``sinks`` keys (at most 1024).  ``scale`` defaults to d^-0.5.  Returns (o, lse): lse float32 [B, T, Hq] is what the backward
     needs (None when ``want_lse`` is False and none is given)."""
-    window = _window(window)
+    window, sinks = _window(window), _sinks(sinks)
     dev = _device(q, k, v, cu_seqlens)
     B, T, Hq, Hk, d = _heads(q, k, (v, "v"))
     ns = _packed(cu_seqlens, B)
@@ -240,23 +248,25 @@ def attn_fwd(q, k, v, cu_seqlens=None, window: int = 0, scale: float | None = No
     _device(q, out, lse)
     _like(out, "out", q.shape, q.dtype)
     _like(lse, "lse", (B, T, Hq), torch.float32)
-    _call(dev, lib().gdn2_attn_fwd, _ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), B, T, Hq, Hk, d, ns, window,
+    _call(dev, lib().gdn2_attn_sink_fwd, _ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), B, T, Hq, Hk, d, ns, window, sinks,
           d ** -0.5 if scale is None else scale, _dtype_code(q), _ptr(out), _ptr(lse))
     return out, lse
 
 
-def attn_bwd_workspace_bytes(B: int, T: int, Hq: int, Hk: int, d: int, dtype: torch.dtype = torch.bfloat16) -> int:
+def attn_bwd_workspace_bytes(B: int, T: int, Hq: int, Hk: int, d: int, dtype: torch.dtype = torch.bfloat16,
+                             sinks: int = 0, num_seqs: int = 0) -> int:
     """Bytes of workspace ``attn_bwd`` needs (B = 1 and the total T when
-    packed; the same for either dtype)."""
-    return int(lib().gdn2_attn_bwd_workspace_bytes(B, T, Hq, Hk, d))
+    packed, with sinks also ``num_seqs``; the same for either dtype and any
+    window)."""
+    return int(lib().gdn2_attn_sink_bwd_workspace_bytes(B, T, Hq, Hk, d, num_seqs, _sinks(sinks)))
 
 
 def attn_bwd(q, k, v, o, lse, dout, cu_seqlens=None, window: int = 0, scale: float | None = None, workspace=None,
-             out=None):
+             out=None, sinks: int = 0):
     """Backward of ``attn_fwd``: from its o and lse on the same inputs and
     dL/do, a dict with dq, dk, dv.  ``out`` may hold preallocated tensors
     under those names."""
-    window = _window(window)
+    window, sinks = _window(window), _sinks(sinks)
     dev = _device(q, k, v, o, lse, dout, cu_seqlens)
     B, T, Hq, Hk, d = _heads(q, k, (v, "v"))
     ns = _packed(cu_seqlens, B)
@@ -269,9 +279,10 @@ def attn_bwd(q, k, v, o, lse, dout, cu_seqlens=None, window: int = 0, scale: flo
             out[name] = torch.empty_like(like)
         _like(out[name], name, like.shape, q.dtype)
     _device(q, *out.values())
-    ws, ws_bytes = _workspace(workspace, attn_bwd_workspace_bytes(B, T, Hq, Hk, d), dev)
-    _call(dev, lib().gdn2_attn_bwd, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(cu_seqlens), B, T,
-          Hq, Hk, d, ns, window, d ** -0.5 if scale is None else scale, _dtype_code(q), _ptr(out["dq"]),
+    need = 0 if workspace is not None else attn_bwd_workspace_bytes(B, T, Hq, Hk, d, q.dtype, sinks, ns)
+    ws, ws_bytes = _workspace(workspace, need, dev)
+    _call(dev, lib().gdn2_attn_sink_bwd, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(cu_seqlens), B, T,
+          Hq, Hk, d, ns, window, sinks, d ** -0.5 if scale is None else scale, _dtype_code(q), _ptr(out["dq"]),
           _ptr(out["dk"]), _ptr(out["dv"]), _ptr(ws), ws_bytes)
     return out
 
@@ -335,25 +346,27 @@ def kv_cache_read(slots, k_cache, v_cache, k_scale=None, v_scale=None, dtype=Non
     return out[0], out[1]
 
 
-def attn_paged_workspace_bytes(q, k_cache, block_table, cu_seqlens=None, window: int = 0) -> int:
+def attn_paged_workspace_bytes(q, k_cache, block_table, cu_seqlens=None, window: int = 0, sinks: int = 0) -> int:
     """Bytes of workspace ``attn_paged`` needs for these tensors (0: none)."""
     B, T, Hq, d = q.shape
     ns = 0 if cu_seqlens is None else cu_seqlens.numel() - 1
-    return int(lib().gdn2_attn_paged_workspace_bytes(B, T, Hq, k_cache.shape[1], d, ns, k_cache.shape[2],
-                                                     block_table.shape[1], _window(window)))
+    return int(lib().gdn2_attn_sink_paged_workspace_bytes(B, T, Hq, k_cache.shape[1], d, ns, k_cache.shape[2],
+                                                          block_table.shape[1], _window(window), _sinks(sinks)))
 
 
 def attn_paged(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens=None, k_scale=None, v_scale=None,
                window: int = 0, scale: float | None = None, out=None, lse=None, want_lse: bool = False,
-               workspace=None):
+               workspace=None, sinks: int = 0):
     """Attention of new tokens over a paged cache that already holds their own
     keys and values (``kv_cache_write``).  q [N, T, Hq, d] (T new tokens for
     each of N sequences; decode is T = 1) or packed [1, T, Hq, d] with
     ``cu_seqlens`` (a chunk of a prompt among single tokens, say; a batch of
     single tokens alone runs faster unpacked);
     ``block_table`` int32 [N, max pages], ``seq_lens`` int32 [N] keys of each
-    sequence, the new ones included.  Returns (o, lse or None)."""
-    window = _window(window)
+    sequence, the new ones included.  ``sinks``: first keys that stay visible
+    behind the window; pages that hold neither a sink nor a key of the window
+    are not read.  Returns (o, lse or None)."""
+    window, sinks = _window(window), _sinks(sinks)
     dev = _device(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens, k_scale, v_scale)
     if q.dim() != 4:
         raise ValueError("q must be [N, T, Hq, d]")
@@ -378,9 +391,9 @@ def attn_paged(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens=None, k_sc
     mp = block_table.shape[1]
     need = 0
     if workspace is None:
-        need = int(lib().gdn2_attn_paged_workspace_bytes(B, T, Hq, Hk, d, ns, page, mp, window))
+        need = int(lib().gdn2_attn_sink_paged_workspace_bytes(B, T, Hq, Hk, d, ns, page, mp, window, sinks))
     ws, ws_bytes = _workspace(workspace, need, dev)
-    _call(dev, lib().gdn2_attn_paged, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+    _call(dev, lib().gdn2_attn_sink_paged, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
           _ptr(block_table), _ptr(seq_lens), _ptr(cu_seqlens), B, T, Hq, Hk, d, ns, P, page, mp, window,
-          d ** -0.5 if scale is None else scale, dt, code, _ptr(out), _ptr(lse), _ptr(ws), ws_bytes)
+          sinks, d ** -0.5 if scale is None else scale, dt, code, _ptr(out), _ptr(lse), _ptr(ws), ws_bytes)
     return out, lse

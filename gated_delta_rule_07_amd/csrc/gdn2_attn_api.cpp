@@ -22,6 +22,7 @@ namespace {
 
 constexpr long long MAX_ROWS = (1LL << 26) - 1;   // query rows (token, head): a wave each, work-items in 32 bits
 constexpr long long MAX_UNITS = (1LL << 20) - 1;  // sequence x kv head
+constexpr int MAX_SINKS = 1024;
 
 bool attn_dim(int d) { return d == 64 || d == 128; }
 bool known(gdn2_dtype_t dt) { return dt == GDN2_F32 || dt == GDN2_BF16; }
@@ -83,10 +84,24 @@ gdn2_status_t check_heads(const char *fn, int Hq, int Hk, int d, gdn2_dtype_t dt
   return GDN2_OK;
 }
 
+// The window and its sinks of a call whose sequences have at most `keys` keys:
+// none of either where they hide nothing.
+gdn2_status_t check_window(const char *fn, int window, int sinks, long long keys, attn_sizes &z) {
+  if (window < 0 || sinks < 0)
+    return fail(GDN2_ERR_INVALID_ARGUMENT, "%s: negative %s %d", fn, window < 0 ? "window" : "number of sinks",
+                window < 0 ? window : sinks);
+  const bool hides = window > 0 && static_cast<long long>(window) + sinks < keys;
+  if (hides && sinks > MAX_SINKS)
+    return fail(GDN2_ERR_UNSUPPORTED, "%s: %d sinks (at most %d)", fn, sinks, MAX_SINKS);
+  z.window = hides ? window : 0;
+  z.sinks = hides ? sinks : 0;
+  return GDN2_OK;
+}
+
 // Sizes of a call on B sequences of T tokens (num_seqs == 0) or num_seqs
 // packed sequences of T tokens in all.
 gdn2_status_t check_attn(const char *fn, int B, int T, int Hq, int Hk, int d, int num_seqs, bool packed, int window,
-                         float scale, gdn2_dtype_t dt, attn_sizes &z) {
+                         int sinks, float scale, gdn2_dtype_t dt, attn_sizes &z) {
   const gdn2_status_t st = check_heads(fn, Hq, Hk, d, dt);
   if (st != GDN2_OK)
     return st;
@@ -98,8 +113,9 @@ gdn2_status_t check_attn(const char *fn, int B, int T, int Hq, int Hk, int d, in
     return fail(GDN2_ERR_INVALID_ARGUMENT, "%s: packed sequences need B == 1 and num_seqs > 0", fn);
   if (!packed && num_seqs != 0)
     return fail(GDN2_ERR_INVALID_ARGUMENT, "%s: num_seqs without cu_seqlens", fn);
-  if (window < 0)
-    return fail(GDN2_ERR_INVALID_ARGUMENT, "%s: negative window %d", fn, window);
+  const gdn2_status_t sw = check_window(fn, window, sinks, T, z);
+  if (sw != GDN2_OK)
+    return sw;
   // (the kernels' exponents are in base 2, scale log2 e: finite too)
   if (!(scale > 0.f) || !std::isfinite(scale * 1.4426950408889634f))
     return fail(GDN2_ERR_INVALID_ARGUMENT, "%s: scale must be positive and at most 2.3e38", fn);
@@ -114,7 +130,6 @@ gdn2_status_t check_attn(const char *fn, int B, int T, int Hq, int Hk, int d, in
   z.Hq = Hq;
   z.Hk = Hk;
   z.packed = packed;
-  z.window = window >= T ? 0 : window;  // a window of a whole sequence hides nothing
   z.scale = scale;
   z.max_pages = z.num_pages = z.page_shift = 0;
   z.max_keys = T;
@@ -236,8 +251,9 @@ gdn2_status_t kv_cache_io(const char *fn, const void *k, const void *v, const in
 
 // Sizes of a paged call, without its pointers.
 gdn2_status_t check_paged(const char *fn, int B, int T, int Hq, int Hk, int d, int num_seqs, int page_size,
-                          int max_pages, int window, float scale, gdn2_dtype_t dt, attn_sizes &z) {
-  const gdn2_status_t st = check_attn(fn, B, T, Hq, Hk, d, num_seqs, num_seqs > 0, window, scale, dt, z);
+                          int max_pages, int window, int sinks, float scale, gdn2_dtype_t dt, attn_sizes &z) {
+  gdn2_status_t st = check_attn(fn, B, T, Hq, Hk, d, num_seqs, num_seqs > 0, window < 0 ? window : 0,
+                                sinks < 0 ? sinks : 0, scale, dt, z);
   if (st != GDN2_OK)
     return st;
   const int sh = page_shift(page_size);
@@ -249,13 +265,135 @@ gdn2_status_t check_paged(const char *fn, int B, int T, int Hq, int Hk, int d, i
   z.max_pages = max_pages;
   z.max_keys = static_cast<long long>(max_pages) * page_size;
   // a query sees at most max_keys + T positions
-  z.window = window >= z.max_keys + T ? 0 : window;
-  return GDN2_OK;
+  return check_window(fn, window, sinks, z.max_keys + T, z);
 }
 
 size_t paged_bytes(const attn_sizes &z, int d) {
   const int s = gdn2::attn::attn_paged_splits(z);
   return s <= 1 ? 0 : static_cast<size_t>(s) * z.Ttot * z.Hq * (d + 1) * sizeof(float);
+}
+
+gdn2_status_t attn_fwd(const char *fn, const void *q, const void *k, const void *v, const int32_t *cu_seqlens, int B,
+                       int T, int Hq, int Hk, int d, int num_seqs, int window, int sinks, float scale, gdn2_dtype_t dt,
+                       void *o, float *lse, void *stream) {
+  attn_sizes z;
+  gdn2_status_t st = check_attn(fn, B, T, Hq, Hk, d, num_seqs, cu_seqlens != nullptr, window, sinks, scale, dt, z);
+  if (st != GDN2_OK)
+    return st;
+  if (T == 0)
+    return ok();
+  st = check_ptrs(fn, {q, k, v, o}, {cu_seqlens, lse});
+  if (st != GDN2_OK)
+    return st;
+  attn_ptrs p = {};
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.cu = cu_seqlens;
+  p.o = o;
+  p.lse = lse;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e;
+  prof_scope ps("attn_fwd", s);
+  GDN2_ATTN_DISPATCH(e, dt, d, launch_attn_fwd, z, p, s);
+  return launched(fn, e);
+}
+
+gdn2_status_t attn_bwd(const char *fn, const void *q, const void *k, const void *v, const void *o, const float *lse,
+                       const void *dout, const int32_t *cu_seqlens, int B, int T, int Hq, int Hk, int d, int num_seqs,
+                       int window, int sinks, float scale, gdn2_dtype_t dt, void *dq, void *dk, void *dv,
+                       void *workspace, size_t workspace_bytes, void *stream) {
+  attn_sizes z;
+  gdn2_status_t st = check_attn(fn, B, T, Hq, Hk, d, num_seqs, cu_seqlens != nullptr, window, sinks, scale, dt, z);
+  if (st != GDN2_OK)
+    return st;
+  if (T == 0)
+    return ok();
+  st = check_ptrs(fn, {q, k, v, o, lse, dout, dq, dk, dv}, {cu_seqlens, workspace});
+  if (st != GDN2_OK)
+    return st;
+  const size_t need = gdn2::attn::attn_bwd_bytes(z, d) + gdn2::attn::attn_bwd_far_bytes(z, d);
+  if (!workspace || workspace_bytes < need)
+    return fail(GDN2_ERR_WORKSPACE_TOO_SMALL, "%s: workspace holds %zu bytes, %zu are needed", fn, workspace_bytes,
+                need);
+  attn_ptrs p = {};
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.cu = cu_seqlens;
+  p.o = const_cast<void *>(o);
+  p.lse = const_cast<float *>(lse);
+  p.dout = dout;
+  p.dq = dq;
+  p.dk = dk;
+  p.dv = dv;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e;
+  {
+    prof_scope ps("attn_bwd_dq", s);
+    GDN2_ATTN_DISPATCH(e, dt, d, launch_attn_bwd_dq, z, p, workspace, s);
+  }
+  if (e == hipSuccess && z.sinks) {
+    prof_scope ps("attn_bwd_far", s);
+    GDN2_ATTN_DISPATCH(e, dt, d, launch_attn_bwd_far, z, p, workspace, s);
+  }
+  if (e == hipSuccess) {
+    prof_scope ps("attn_bwd_dkv", s);
+    GDN2_ATTN_DISPATCH(e, dt, d, launch_attn_bwd_dkv, z, p, workspace, s);
+  }
+  return launched(fn, e);
+}
+
+gdn2_status_t attn_paged(const char *fn, const void *q, const void *k_cache, const void *v_cache,
+                         const uint8_t *k_scale, const uint8_t *v_scale, const int32_t *block_table,
+                         const int32_t *seq_lens, const int32_t *cu_seqlens, int B, int T, int Hq, int Hk, int d,
+                         int num_seqs, int num_pages, int page_size, int max_pages, int window, int sinks, float scale,
+                         gdn2_dtype_t dt, gdn2_dtype_t cache_dt, void *o, float *lse, void *workspace,
+                         size_t workspace_bytes, void *stream) {
+  attn_sizes z;
+  if ((cu_seqlens != nullptr) != (num_seqs > 0))
+    return fail(GDN2_ERR_INVALID_ARGUMENT, "%s: cu_seqlens goes with num_seqs > 0", fn);
+  gdn2_status_t st = check_paged(fn, B, T, Hq, Hk, d, num_seqs, page_size, max_pages, window, sinks, scale, dt, z);
+  if (st != GDN2_OK)
+    return st;
+  st = check_cache(fn, num_pages, page_size, dt, cache_dt, k_scale, v_scale);
+  if (st != GDN2_OK)
+    return st;
+  if (T == 0)
+    return ok();
+  // (a table of no pages has no entries: nothing reads it)
+  st = check_ptrs(fn, {q, k_cache, v_cache, max_pages ? block_table : seq_lens, seq_lens, o},
+                  {cu_seqlens, lse, workspace, block_table});
+  if (st != GDN2_OK)
+    return st;
+  const size_t need = paged_bytes(z, d);
+  if (need && (!workspace || workspace_bytes < need))
+    return fail(GDN2_ERR_WORKSPACE_TOO_SMALL, "%s: workspace holds %zu bytes, %zu are needed", fn, workspace_bytes,
+                need);
+  z.num_pages = num_pages;
+  attn_ptrs p = {};
+  p.q = q;
+  p.k = k_cache;
+  p.v = v_cache;
+  p.ks = k_scale;
+  p.vs = v_scale;
+  p.table = block_table;
+  p.seq_lens = seq_lens;
+  p.cu = cu_seqlens;
+  p.o = o;
+  p.lse = lse;
+  const int splits = gdn2::attn::attn_paged_splits(z);
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e;
+  {
+    prof_scope ps("attn_paged", s);
+    GDN2_CACHE_DISPATCH(e, dt, cache_dt == GDN2_F8E4M3, d, launch_attn_paged, z, p, splits, workspace, s);
+  }
+  if (e == hipSuccess && splits > 1) {
+    prof_scope ps("attn_paged_join", s);
+    GDN2_ATTN_DISPATCH(e, dt, d, launch_attn_join, z, p, splits, workspace, s);
+  }
+  return launched(fn, e);
 }
 
 }  // namespace
@@ -335,86 +473,62 @@ gdn2_status_t gdn2_qk_norm_rope_bwd(const void *q, const void *k, const float *w
 gdn2_status_t gdn2_attn_fwd(const void *q, const void *k, const void *v, const int32_t *cu_seqlens, int B, int T,
                             int Hq, int Hk, int d, int num_seqs, int window, float scale, gdn2_dtype_t dt, void *o,
                             float *lse, void *stream) {
-  const char *fn = "gdn2_attn_fwd";
-  attn_sizes z;
-  gdn2_status_t st = check_attn(fn, B, T, Hq, Hk, d, num_seqs, cu_seqlens != nullptr, window, scale, dt, z);
-  if (st != GDN2_OK)
-    return st;
-  if (T == 0)
-    return ok();
-  st = check_ptrs(fn, {q, k, v, o}, {cu_seqlens, lse});
-  if (st != GDN2_OK)
-    return st;
-  attn_ptrs p = {};
-  p.q = q;
-  p.k = k;
-  p.v = v;
-  p.cu = cu_seqlens;
-  p.o = o;
-  p.lse = lse;
-  const hipStream_t s = static_cast<hipStream_t>(stream);
-  hipError_t e;
-  prof_scope ps("attn_fwd", s);
-  GDN2_ATTN_DISPATCH(e, dt, d, launch_attn_fwd, z, p, s);
-  return launched(fn, e);
+  return attn_fwd("gdn2_attn_fwd", q, k, v, cu_seqlens, B, T, Hq, Hk, d, num_seqs, window, 0, scale, dt, o, lse, stream);
+}
+
+gdn2_status_t gdn2_attn_sink_fwd(const void *q, const void *k, const void *v, const int32_t *cu_seqlens, int B, int T,
+                                 int Hq, int Hk, int d, int num_seqs, int window, int sinks, float scale,
+                                 gdn2_dtype_t dt, void *o, float *lse, void *stream) {
+  return attn_fwd("gdn2_attn_sink_fwd", q, k, v, cu_seqlens, B, T, Hq, Hk, d, num_seqs, window, sinks, scale, dt, o, lse,
+                  stream);
 }
 
 size_t gdn2_attn_bwd_workspace_bytes(int B, int T, int Hq, int Hk, int d) {
   attn_sizes z;
-  if (check_attn("gdn2_attn_bwd_workspace_bytes", B, T, Hq, Hk, d, 0, false, 0, 1.f, GDN2_F32, z) != GDN2_OK) {
+  if (check_attn("gdn2_attn_bwd_workspace_bytes", B, T, Hq, Hk, d, 0, false, 0, 0, 1.f, GDN2_F32, z) != GDN2_OK) {
     (void)ok();
     return 0;
   }
   return T == 0 ? 0 : gdn2::attn::attn_bwd_bytes(z, d);
 }
 
+size_t gdn2_attn_sink_bwd_workspace_bytes(int B, int T, int Hq, int Hk, int d, int num_seqs, int sinks) {
+  attn_sizes z;
+  // (no window hides more than one token's; a call that takes more sinks has none that hides anything)
+  if (check_attn("gdn2_attn_sink_bwd_workspace_bytes", B, T, Hq, Hk, d, num_seqs, num_seqs > 0, 1,
+                 sinks > MAX_SINKS ? 0 : sinks, 1.f, GDN2_F32, z) != GDN2_OK) {
+    (void)ok();
+    return 0;
+  }
+  return T == 0 ? 0 : gdn2::attn::attn_bwd_bytes(z, d) + gdn2::attn::attn_bwd_far_bytes(z, d);
+}
+
 gdn2_status_t gdn2_attn_bwd(const void *q, const void *k, const void *v, const void *o, const float *lse,
                             const void *dout, const int32_t *cu_seqlens, int B, int T, int Hq, int Hk, int d,
                             int num_seqs, int window, float scale, gdn2_dtype_t dt, void *dq, void *dk, void *dv,
                             void *workspace, size_t workspace_bytes, void *stream) {
-  const char *fn = "gdn2_attn_bwd";
-  attn_sizes z;
-  gdn2_status_t st = check_attn(fn, B, T, Hq, Hk, d, num_seqs, cu_seqlens != nullptr, window, scale, dt, z);
-  if (st != GDN2_OK)
-    return st;
-  if (T == 0)
-    return ok();
-  st = check_ptrs(fn, {q, k, v, o, lse, dout, dq, dk, dv}, {cu_seqlens, workspace});
-  if (st != GDN2_OK)
-    return st;
-  const size_t need = gdn2::attn::attn_bwd_bytes(z, d);
-  if (!workspace || workspace_bytes < need)
-    return fail(GDN2_ERR_WORKSPACE_TOO_SMALL, "%s: workspace holds %zu bytes, %zu are needed", fn, workspace_bytes,
-                need);
-  attn_ptrs p = {};
-  p.q = q;
-  p.k = k;
-  p.v = v;
-  p.cu = cu_seqlens;
-  p.o = const_cast<void *>(o);
-  p.lse = const_cast<float *>(lse);
-  p.dout = dout;
-  p.dq = dq;
-  p.dk = dk;
-  p.dv = dv;
-  const hipStream_t s = static_cast<hipStream_t>(stream);
-  hipError_t e;
-  {
-    prof_scope ps("attn_bwd_dq", s);
-    GDN2_ATTN_DISPATCH(e, dt, d, launch_attn_bwd_dq, z, p, workspace, s);
-  }
-  if (e == hipSuccess) {
-    prof_scope ps("attn_bwd_dkv", s);
-    GDN2_ATTN_DISPATCH(e, dt, d, launch_attn_bwd_dkv, z, p, workspace, s);
-  }
-  return launched(fn, e);
+  return attn_bwd("gdn2_attn_bwd", q, k, v, o, lse, dout, cu_seqlens, B, T, Hq, Hk, d, num_seqs, window, 0, scale, dt,
+                  dq, dk, dv, workspace, workspace_bytes, stream);
+}
+
+gdn2_status_t gdn2_attn_sink_bwd(const void *q, const void *k, const void *v, const void *o, const float *lse,
+                                 const void *dout, const int32_t *cu_seqlens, int B, int T, int Hq, int Hk, int d,
+                                 int num_seqs, int window, int sinks, float scale, gdn2_dtype_t dt, void *dq, void *dk,
+                                 void *dv, void *workspace, size_t workspace_bytes, void *stream) {
+  return attn_bwd("gdn2_attn_sink_bwd", q, k, v, o, lse, dout, cu_seqlens, B, T, Hq, Hk, d, num_seqs, window, sinks,
+                  scale, dt, dq, dk, dv, workspace, workspace_bytes, stream);
 }
 
 size_t gdn2_attn_paged_workspace_bytes(int B, int T, int Hq, int Hk, int d, int num_seqs, int page_size, int max_pages,
                                        int window) {
+  return gdn2_attn_sink_paged_workspace_bytes(B, T, Hq, Hk, d, num_seqs, page_size, max_pages, window, 0);
+}
+
+size_t gdn2_attn_sink_paged_workspace_bytes(int B, int T, int Hq, int Hk, int d, int num_seqs, int page_size,
+                                            int max_pages, int window, int sinks) {
   attn_sizes z;
-  if (check_paged("gdn2_attn_paged_workspace_bytes", B, T, Hq, Hk, d, num_seqs, page_size, max_pages, window, 1.f,
-                  GDN2_F32, z) != GDN2_OK) {
+  if (check_paged("gdn2_attn_sink_paged_workspace_bytes", B, T, Hq, Hk, d, num_seqs, page_size, max_pages, window, sinks,
+                  1.f, GDN2_F32, z) != GDN2_OK) {
     (void)ok();
     return 0;
   }
@@ -427,51 +541,20 @@ gdn2_status_t gdn2_attn_paged(const void *q, const void *k_cache, const void *v_
                               int num_pages, int page_size, int max_pages, int window, float scale, gdn2_dtype_t dt,
                               gdn2_dtype_t cache_dt, void *o, float *lse, void *workspace, size_t workspace_bytes,
                               void *stream) {
-  const char *fn = "gdn2_attn_paged";
-  attn_sizes z;
-  if ((cu_seqlens != nullptr) != (num_seqs > 0))
-    return fail(GDN2_ERR_INVALID_ARGUMENT, "%s: cu_seqlens goes with num_seqs > 0", fn);
-  gdn2_status_t st = check_paged(fn, B, T, Hq, Hk, d, num_seqs, page_size, max_pages, window, scale, dt, z);
-  if (st != GDN2_OK)
-    return st;
-  st = check_cache(fn, num_pages, page_size, dt, cache_dt, k_scale, v_scale);
-  if (st != GDN2_OK)
-    return st;
-  if (T == 0)
-    return ok();
-  // (a table of no pages has no entries: nothing reads it)
-  st = check_ptrs(fn, {q, k_cache, v_cache, max_pages ? block_table : seq_lens, seq_lens, o},
-                  {cu_seqlens, lse, workspace, block_table});
-  if (st != GDN2_OK)
-    return st;
-  const size_t need = paged_bytes(z, d);
-  if (need && (!workspace || workspace_bytes < need))
-    return fail(GDN2_ERR_WORKSPACE_TOO_SMALL, "%s: workspace holds %zu bytes, %zu are needed", fn, workspace_bytes,
-                need);
-  z.num_pages = num_pages;
-  attn_ptrs p = {};
-  p.q = q;
-  p.k = k_cache;
-  p.v = v_cache;
-  p.ks = k_scale;
-  p.vs = v_scale;
-  p.table = block_table;
-  p.seq_lens = seq_lens;
-  p.cu = cu_seqlens;
-  p.o = o;
-  p.lse = lse;
-  const int splits = gdn2::attn::attn_paged_splits(z);
-  const hipStream_t s = static_cast<hipStream_t>(stream);
-  hipError_t e;
-  {
-    prof_scope ps("attn_paged", s);
-    GDN2_CACHE_DISPATCH(e, dt, cache_dt == GDN2_F8E4M3, d, launch_attn_paged, z, p, splits, workspace, s);
-  }
-  if (e == hipSuccess && splits > 1) {
-    prof_scope ps("attn_paged_join", s);
-    GDN2_ATTN_DISPATCH(e, dt, d, launch_attn_join, z, p, splits, workspace, s);
-  }
-  return launched(fn, e);
+  return attn_paged("gdn2_attn_paged", q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens, B, T,
+                    Hq, Hk, d, num_seqs, num_pages, page_size, max_pages, window, 0, scale, dt, cache_dt, o, lse,
+                    workspace, workspace_bytes, stream);
+}
+
+gdn2_status_t gdn2_attn_sink_paged(const void *q, const void *k_cache, const void *v_cache, const uint8_t *k_scale,
+                                   const uint8_t *v_scale, const int32_t *block_table, const int32_t *seq_lens,
+                                   const int32_t *cu_seqlens, int B, int T, int Hq, int Hk, int d, int num_seqs,
+                                   int num_pages, int page_size, int max_pages, int window, int sinks, float scale,
+                                   gdn2_dtype_t dt, gdn2_dtype_t cache_dt, void *o, float *lse, void *workspace,
+                                   size_t workspace_bytes, void *stream) {
+  return attn_paged("gdn2_attn_sink_paged", q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens, B,
+                    T, Hq, Hk, d, num_seqs, num_pages, page_size, max_pages, window, sinks, scale, dt, cache_dt, o, lse,
+                    workspace, workspace_bytes, stream);
 }
 
 gdn2_status_t gdn2_kv_cache_write(const void *k, const void *v, const int64_t *slots, int n, int Hk, int d,

@@ -31,6 +31,9 @@ struct bwd_args {
   f32x2 *stat;  // [Hk, Ttot, G]: lse log2 e, delta
   const int32_t *cu;
   int N, T, Ttot, Hq, Hk, G, window;
+  int sinks;         // first keys visible behind the window (0: none, or no window)
+  int far_parts;     // workgroups that share the rows which see a sink from behind the window
+  float *far_sums;   // sinks > 0: [far_parts, 2, N, sinks, Hk, D], their sums of dk / scale and dv
   float c, scale;
   int gs;            // heads of a row tile of the dk, dv kernel
   int parts;         // workgroups that share a key tile's rows (dk, dv kernel)
@@ -79,7 +82,9 @@ __device__ __forceinline__ bool locate(const bwd_args &a, int unit, int slot, in
 // q and dO stay in registers (64 at d = 128 beside dq's 64: two waves a SIMD),
 // K and V come straight from memory into shared memory, a tile ahead (621 us
 // through registers, 575 so).
-template <typename IO, int D, int WM, int WN, int KT>
+// SINK: keys and positions are numbered without the gap between the sinks and
+// the window, as in the forward.
+template <typename IO, int D, int WM, int WN, int KT, bool SINK>
 __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1)) gdn2_attn_dq_kernel(bwd_args a) {
   typedef tile<IO, D> TL;
   constexpr int NT = 64 * WM * WN, BM = 32 * WM, BN = 32 * KT * WN, CPR = TL::CPR, CH = BN * CPR / NT, RPI = NT / CPR;
@@ -95,21 +100,27 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
     return;
   const int rows = sq.len * a.G;
   const int last_row = row0 + BM - 1 < rows - 1 ? row0 + BM - 1 : rows - 1;
-  const int k1 = last_row / a.G + 1;
+  int k1 = last_row / a.G + 1;
   int k0 = 0;
   if (a.window > 0) {
     k0 = row0 / a.G - a.window + 1;
     k0 = k0 < 0 ? 0 : k0;
   }
+  int gap = 0;
+  if constexpr (SINK) {
+    gap = k0 > a.sinks ? k0 - a.sinks : 0;
+    k0 = 0;
+    k1 -= gap;
+  }
   const int ntiles = (k1 - k0 + BN - 1) / BN;
   const int my_row = row0 + 32 * wm + r;
   const bool row_ok = my_row < rows;
   const int cl_row = row_ok ? my_row : rows - 1;
-  const int pos = cl_row / a.G, g = cl_row % a.G;
-  const size_t qrow = static_cast<size_t>(sq.start + pos) * a.Hq + hk * a.G + g;
+  const int tok = cl_row / a.G, pos = tok - gap, g = cl_row % a.G;
+  const size_t qrow = static_cast<size_t>(sq.start + tok) * a.Hq + hk * a.G + g;
   const int wr0 = row0 + 32 * wm < rows ? row0 + 32 * wm : rows - 1;
   const int wr1 = row0 + 32 * wm + 31 < rows ? row0 + 32 * wm + 31 : rows - 1;
-  const int pos_lo = wr0 / a.G, pos_hi = wr1 / a.G;
+  const int pos_lo = wr0 / a.G - gap, pos_hi = wr1 / a.G - gap;
   frag8<IO> q[D / 16], d[D / 16];
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk) {
@@ -131,16 +142,26 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
   const unsigned kstep = static_cast<unsigned>(a.Hk) * D;  // values of a token
   char *const kt = lds, *const vt = lds + TILEB;
   auto load_tile = [&](int kb, int buf) {
-    const size_t base = (static_cast<size_t>(sq.start + kb) * a.Hk + hk) * D;
+    // (a tile with sinks takes its keys one by one, from the sequence's first)
+    const bool mixed = SINK && kb < a.sinks;
+    const size_t base = (static_cast<size_t>(sq.start + (mixed ? 0 : kb + gap)) * a.Hk + hk) * D;
     const IO *const kp = static_cast<const IO *>(a.k) + base, *const vp = static_cast<const IO *>(a.v) + base;
     const int left = k1 - 1 - kb;  // (a key behind the last: any, its score is masked)
     char *const to = lds + buf * 2 * TILEB + 1024 * wv;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int x = sr0 + RPI * i;
-      const unsigned off = (x < left ? x : left) * kstep + (sc ^ TL::f(x)) * TL::VPC;
-      dma16(kp + off, to + 16 * NT * i);
-      dma16(vp + off, to + TILEB + 16 * NT * i);
+      auto bring = [&](auto off) {
+        off += (sc ^ TL::f(x)) * TL::VPC;
+        dma16(kp + off, to + 16 * NT * i);
+        dma16(vp + off, to + TILEB + 16 * NT * i);
+      };
+      if (mixed) {
+        const int j = kb + (x < left ? x : left);
+        bring(static_cast<size_t>(j < a.sinks ? j : j + gap) * kstep);
+      } else {
+        bring((x < left ? x : left) * kstep);
+      }
     }
   };
   f32x16 dq[D / 32];
@@ -157,7 +178,7 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
       const int wk = kb + 32 * (KT * wn + t);
-      if (wk > pos_hi || (a.window > 0 && wk + 31 <= pos_lo - a.window))
+      if (wk > pos_hi || (a.window > 0 && wk + 31 <= pos_lo - a.window && !(SINK && wk < a.sinks)))
         continue;  // nothing visible to the wave
       const bool masked = wk + 31 > pos_lo || (a.window > 0 && wk <= pos_hi - a.window);
       const int rb = row_b + bo + 32 * KT * wn * TL::ROWB, cb = col_b + bo + 32 * KT * wn * TL::ROWB;
@@ -192,10 +213,11 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
         s[i] = fast_exp2(s[i] * a.c - st[0]) * (dp[i] - st[1]);
       if (masked) {
         const int hi_rel = pos - wk - 4 * h, lo_rel = (a.window > 0 ? pos - a.window : -0x40000000) - wk - 4 * h;
+        const int sink_rel = SINK ? a.sinks - wk - 4 * h : 0;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int j = 8 * (i >> 2) + (i & 3);
-          s[i] = (j <= hi_rel && j > lo_rel) ? s[i] : 0.f;
+          s[i] = (j <= hi_rel && (j > lo_rel || (SINK && j < sink_rel))) ? s[i] : 0.f;
         }
       }
 #pragma unroll
@@ -259,7 +281,33 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
 // 1025) and the statistics and first operands of the second half read early
 // (990), all beside 1005 on that card, do not change that; at d = 64 K and V in
 // registers gain 3 %, not enough for a second form.
-template <typename IO, int D, int WK, int WR>
+//
+// Sinks.  The rows that see a sink from behind the window (all later ones) are
+// many for few keys: a launch of its own (DKV_FAR) shares them among far_parts
+// workgroups a 32-key tile and leaves float32 sums, and the workgroup that owns
+// the keys (DKV_SINK) adds them to its window's.  Every sum has a fixed order.
+enum dkv_mode { DKV_PLAIN, DKV_SINK, DKV_FAR };
+// Tile of the DKV_FAR launch: 128 rows where two of them fit shared memory
+// beside the keys (64 would pass through registers and spill).
+constexpr int FAR_KEYS = 32;
+template <typename IO, int D> constexpr int FAR_ROWS = D * sizeof(IO) <= 256 ? 128 : 64;
+// Tiles of TB tokens of the rows of a sequence of len tokens that see a key
+// from key0 on from behind the window, and how many of them a part takes.
+__device__ __forceinline__ int far_tiles(const bwd_args &a, int len, int key0, int TB) {
+  const long n = static_cast<long>(len) - key0 - a.window;
+  return n > 0 ? static_cast<int>((n + TB - 1) / TB) * (a.G / a.gs) : 0;
+}
+// Parts that hold sums for a sink (their workgroups had rows).
+template <typename IO, int D> __device__ __forceinline__ int far_parts_of(const bwd_args &a, int len, int key) {
+  const int n = far_tiles(a, len, key - key % FAR_KEYS, FAR_ROWS<IO, D> / a.gs), per = (n + a.far_parts - 1) / a.far_parts;
+  return n ? (n + per - 1) / per : 0;
+}
+template <int D>
+__device__ __forceinline__ float *far_sum(const bwd_args &a, int part, bool is_v, int n, int key, int hk) {
+  return a.far_sums +
+         (((static_cast<size_t>(2 * part + (is_v ? 1 : 0)) * a.N + n) * a.sinks + key) * a.Hk + hk) * D;
+}
+template <typename IO, int D, int WK, int WR, dkv_mode M>
 __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1)) gdn2_attn_dkv_kernel(bwd_args a) {
   typedef tile<IO, D> TL;
   constexpr int NT = 64 * WK * WR, BK = 32 * WK, BQ = 32 * WR, CPR = TL::CPR, CH = BQ * CPR / NT, RPI = NT / CPR;
@@ -278,23 +326,43 @@ __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1))
   const int wkey = wave % WK, wrow = wave / WK;
   int unit, slot, hk, key0;
   span sq;
-  const int part = blockIdx.x % a.parts;
-  if (!place(a.od, blockIdx.x / a.parts, unit, slot) ||
-      !locate(a, unit, a.od.tiles - 1 - slot, 1, BK, lane, sq, hk, key0))
-    return;
-  const int key_end = key0 + BK < sq.len ? key0 + BK : sq.len;
+  const int parts = M == DKV_FAR ? a.far_parts : a.parts, part = blockIdx.x % parts;
+  if constexpr (M == DKV_FAR) {
+    // a unit a sequence and kv head, a tile for every 32 sinks
+    const int id = blockIdx.x / parts, tiles = (a.sinks + BK - 1) / BK;
+    unit = id / tiles;
+    sq.n = unit / a.Hk;
+    hk = unit % a.Hk;
+    key0 = id % tiles * BK;
+    if (a.cu) {
+      sq = packed_span(a.cu, sq.n, a.T);
+    } else {
+      sq.start = sq.n * a.T;
+      sq.len = a.T;
+    }
+    if (key0 >= sq.len)
+      return;
+  } else {
+    if (!place(a.od, blockIdx.x / parts, unit, slot) ||
+        !locate(a, unit, a.od.tiles - 1 - slot, 1, BK, lane, sq, hk, key0))
+      return;
+  }
+  // keys of the workgroup: all of the sequence's, or its sinks
+  const int last_key = M == DKV_FAR && a.sinks < sq.len ? a.sinks : sq.len;
+  const int key_end = key0 + BK < last_key ? key0 + BK : last_key;
   // Tokens whose rows see a key of the workgroup.  A tile is TB whole tokens
   // of GS heads (GS: the largest divisor of G up to 32; its TB GS rows come
   // first, the rest of the tile's are no rows), so that a thread's rows keep
   // their places in it and only the tile's base moves; G / GS turns over the
   // tokens take all heads.
+  const int tok_0 = M == DKV_FAR ? key0 + a.window : key0;  // (less than len where there are tiles)
   int tok_end = sq.len;
-  if (a.window > 0 && key_end - 1 + static_cast<long>(a.window) < tok_end)
+  if (M != DKV_FAR && a.window > 0 && key_end - 1 + static_cast<long>(a.window) < tok_end)
     tok_end = key_end - 1 + a.window;
   const int GS = a.gs, TB = BQ / GS, nrows = TB * GS;
   const int wk = key0 + 32 * wkey;  // the wave's first key
   const int key = wk + r;           // the lane's
-  const int wk_hi = wk + 31 < sq.len - 1 ? wk + 31 : sq.len - 1;
+  const int wk_hi = wk + 31 < last_key - 1 ? wk + 31 : last_key - 1;
 
   const int sc = tid % CPR, sr0 = tid / CPR;
   const int row_b = TL::row_base(r, h), col_b = TL::col_base(lane), st_b = TL::at(sr0, sc);
@@ -302,7 +370,7 @@ __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1))
 #pragma unroll
   for (int i = 0; i < KCH; ++i) {
     // (a key behind the last: any row, it is not stored)
-    const int x = sr0 + RPI * i, j = key0 + x < sq.len ? key0 + x : sq.len - 1;
+    const int x = sr0 + RPI * i, j = key0 + x < last_key ? key0 + x : last_key - 1;
     const size_t off = (static_cast<size_t>(sq.start + j) * a.Hk + hk) * D + sc * TL::VPC;
     *reinterpret_cast<u32x4 *>(lds + TL::at(x, sc)) =
         *reinterpret_cast<const u32x4 *>(static_cast<const IO *>(a.k) + off);
@@ -327,13 +395,14 @@ __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1))
   const int my_x = tid < nrows ? tid : nrows - 1, my_tok = my_x / GS, my_g = my_x % GS;
   const bool my_ok = tid < nrows;
   const unsigned tstep = static_cast<unsigned>(a.Hq) * D;  // values of a token
-  const int ntok = (tok_end - key0 + TB - 1) / TB, ntiles = ntok * (a.G / GS);
+  const int ntiles = M == DKV_FAR ? far_tiles(a, sq.len, key0, TB) : (tok_end - key0 + TB - 1) / TB * (a.G / GS);
+  const int ntok = ntiles / (a.G / GS);
   // Order of the tiles: a sequence's workgroups run side by side on one die,
   // whose L2 holds a part of its rows, so they walk the tokens in step: without
   // a window from the end down, where all have rows; with one from the first
   // tile whose index is a multiple of the window's tiles.
   int turn = 0;
-  if (a.window > 0) {
+  if (M != DKV_FAR && a.window > 0) {
     const int period = static_cast<int>((static_cast<long>(a.window) + BK - 1) / TB) + 1;
     turn = (period - key0 / TB % period) % period;
     turn = turn < ntok ? turn : 0;
@@ -342,7 +411,7 @@ __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1))
     const int sub = it / ntok;
     int x = it - sub * ntok;
     x = a.window > 0 ? (x + turn < ntok ? x + turn : x + turn - ntok) : ntok - 1 - x;
-    const int t0 = key0 + x * TB;
+    const int t0 = tok_0 + x * TB;
     const size_t base = (static_cast<size_t>(sq.start + t0) * a.Hq + hk * a.G + sub * GS) * D;
     const IO *const qb = static_cast<const IO *>(a.q) + base, *const db = static_cast<const IO *>(a.dout) + base;
     const int left = tok_end - 1 - t0;  // (a token behind the last: any, its weight is 0)
@@ -371,7 +440,9 @@ __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1))
   for (int n = 0; n < D / 32; ++n)
     dk[n] = dv[n] = zero16();
   // this workgroup's share of the tiles
-  const int per = (ntiles + a.parts - 1) / a.parts, it0 = part * per, it1 = it0 + per < ntiles ? it0 + per : ntiles;
+  const int per = (ntiles + parts - 1) / parts, it0 = part * per, it1 = it0 + per < ntiles ? it0 + per : ntiles;
+  if (M == DKV_FAR && it0 >= it1)
+    return;  // (no sums: far_parts_of does not count the part)
   if (it0 < it1)
     load_tile(it0);
   for (int it = it0; it < it1; ++it) {
@@ -402,9 +473,11 @@ __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1))
       continue;
     const int p_lo = __builtin_amdgcn_readfirstlane(s_pos[buf][u0]);
     const int p_hi = __builtin_amdgcn_readfirstlane(s_pos[buf][u0 + 31]);
-    if (p_lo >= tok_end || wk > p_hi || wk >= sq.len || (a.window > 0 && wk_hi <= p_lo - a.window))
+    if (p_lo >= tok_end || wk >= last_key ||
+        (M == DKV_FAR ? wk > p_hi - a.window : wk > p_hi || (a.window > 0 && wk_hi <= p_lo - a.window)))
       continue;  // no row sees a key of the wave
-    const bool masked = wk_hi > p_lo || (a.window > 0 && wk <= p_hi - a.window);
+    // (keys behind the last are not stored)
+    const bool masked = M == DKV_FAR ? wk_hi > p_lo - a.window : wk_hi > p_lo || (a.window > 0 && wk <= p_hi - a.window);
     const int rb = row_b + bo + u0 * TL::ROWB, cb = col_b + bo + u0 * TL::ROWB;
     const int kb = fresh(row_b + 32 * wkey * TL::ROWB);
     f32x16 s = zero16(), dp = zero16();
@@ -450,7 +523,7 @@ __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1))
         const i32x4 ps = *reinterpret_cast<const i32x4 *>(&s_pos[buf][u0 + 8 * g + 4 * h]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const bool vis = key <= ps[i] && (a.window <= 0 || key > ps[i] - a.window);
+          const bool vis = M == DKV_FAR ? key <= ps[i] - a.window : key <= ps[i] && (a.window <= 0 || key > ps[i] - a.window);
           s[4 * g + i] = vis ? s[4 * g + i] : 0.f;
           dp[4 * g + i] = vis ? dp[4 * g + i] : 0.f;
         }
@@ -489,12 +562,40 @@ __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1))
           x[n][4 * g + i] += y[i];
       }
   };
-  auto store = [&](const f32x16(&x)[D / 32], float scale, IO *out) {
-    if (key >= sq.len)
+  auto store = [&](f32x16(&x)[D / 32], float scale, IO *out) {
+    if (key >= last_key)
       return;
     const size_t at = (static_cast<size_t>(sq.start + key) * a.Hk + hk) * D + 4 * h;
+    const bool is_v = wrow != 0;
+    if constexpr (M == DKV_FAR) {
+      float *const sums = far_sum<D>(a, part, is_v, sq.n, key, hk) + 4 * h;
+#pragma unroll
+      for (int n = 0; n < D / 32; ++n)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          io<float>::store4(sums + 32 * n + 8 * g,
+                            f32x4{x[n][4 * g], x[n][4 * g + 1], x[n][4 * g + 2], x[n][4 * g + 3]});
+      return;
+    }
+    if constexpr (M == DKV_SINK) {
+      if (a.parts == 1 && key < a.sinks) {
+        const int np = far_parts_of<IO, D>(a, sq.len, key);
+        for (int p = 0; p < np; ++p) {
+          const float *const sums = far_sum<D>(a, p, is_v, sq.n, key, hk) + 4 * h;
+#pragma unroll
+          for (int n = 0; n < D / 32; ++n)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              const f32x4 y = io<float>::load4(sums + 32 * n + 8 * g);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                x[n][4 * g + i] += y[i];
+            }
+        }
+      }
+    }
     if (a.parts > 1) {
-      float *const sums = a.part_sums + (2 * part + (wrow == 0 ? 0 : 1)) * (static_cast<size_t>(a.Ttot) * a.Hk * D) + at;
+      float *const sums = a.part_sums + (2 * part + (is_v ? 1 : 0)) * (static_cast<size_t>(a.Ttot) * a.Hk * D) + at;
 #pragma unroll
       for (int n = 0; n < D / 32; ++n)
 #pragma unroll
@@ -544,7 +645,7 @@ __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1))
 
 // The parts' sums, in order, to dk and dv: four channels a thread, dk's then
 // dv's.
-template <typename IO, int D> __global__ void __launch_bounds__(256) gdn2_attn_dkv_join_kernel(bwd_args a) {
+template <typename IO, int D, bool SINK> __global__ void __launch_bounds__(256) gdn2_attn_dkv_join_kernel(bwd_args a) {
   const size_t rows = static_cast<size_t>(a.Ttot) * a.Hk * D;
   const size_t at = (static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
   if (at >= 2 * rows)
@@ -557,6 +658,29 @@ template <typename IO, int D> __global__ void __launch_bounds__(256) gdn2_attn_d
 #pragma unroll 4
   for (int p = 0; p < a.parts; ++p)
     x += io<float>::load4(a.part_sums + 2 * p * rows + at);
+  if constexpr (SINK) {
+    const int row = static_cast<int>(e / D), tok = row / a.Hk, hk = row % a.Hk;
+    span sq;
+    if (a.cu) {
+      // the last sequence that starts at or before the token
+      int lo = 0, hi = a.N;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        (a.cu[mid] <= tok ? lo : hi) = mid;
+      }
+      sq = packed_span(a.cu, lo, a.T);
+    } else {
+      sq.n = tok / a.T;
+      sq.start = sq.n * a.T;
+      sq.len = a.T;
+    }
+    const int key = tok - sq.start;
+    if (key >= 0 && key < a.sinks) {
+      const int np = far_parts_of<IO, D>(a, sq.len, key);
+      for (int p = 0; p < np; ++p)
+        x += io<float>::load4(far_sum<D>(a, p, is_v, sq.n, key, hk) + e % D);
+    }
+  }
   io<IO>::store4(static_cast<IO *>(is_v ? a.dv : a.dk) + e, x * (is_v ? 1.f : a.scale));
 }
 
@@ -583,7 +707,19 @@ int attn_bwd_parts(const attn_sizes &z) {
   return p < 1 ? 1 : (p > 16 ? 16 : static_cast<int>(p));
 }
 
-static void fill(bwd_args &a, const attn_sizes &z, const attn_ptrs &p, void *ws) {
+// Workgroups that share the rows behind the window of a 32-sink tile of a
+// sequence and kv head: enough for 1024 in all, at most 64 and at most one for
+// every 512 rows of the call.
+int attn_bwd_far_parts(const attn_sizes &z) {
+  const long long units = static_cast<long long>(z.N) * z.Hk * ((z.sinks + FAR_KEYS - 1) / FAR_KEYS);
+  const long long rows = static_cast<long long>(z.T) * (z.Hq / z.Hk);
+  long long p = (1024 + units - 1) / units;
+  if (p > rows / 512)
+    p = rows / 512;
+  return p < 1 ? 1 : (p > 64 ? 64 : static_cast<int>(p));
+}
+
+static void fill(bwd_args &a, const attn_sizes &z, const attn_ptrs &p, void *ws, int d) {
   a.q = p.q;
   a.k = p.k;
   a.v = p.v;
@@ -606,6 +742,9 @@ static void fill(bwd_args &a, const attn_sizes &z, const attn_ptrs &p, void *ws)
   a.scale = z.scale;
   a.parts = attn_bwd_parts(z);
   a.part_sums = a.parts > 1 ? reinterpret_cast<float *>(static_cast<char *>(ws) + attn_bwd_stat_bytes(z)) : nullptr;
+  a.sinks = z.sinks;
+  a.far_parts = z.sinks ? attn_bwd_far_parts(z) : 0;
+  a.far_sums = z.sinks ? reinterpret_cast<float *>(static_cast<char *>(ws) + attn_bwd_bytes(z, d)) : nullptr;
   a.gs = a.G < 32 ? a.G : 32;
   while (a.G % a.gs)
     --a.gs;
@@ -614,23 +753,44 @@ static void fill(bwd_args &a, const attn_sizes &z, const attn_ptrs &p, void *ws)
 template <typename IO, int D>
 hipError_t launch_attn_bwd_dq(const attn_sizes &z, const attn_ptrs &p, void *ws, hipStream_t st) {
   bwd_args a;
-  fill(a, z, p, ws);
+  fill(a, z, p, ws, D);
   // (few tiles: 4 waves where their tiles fit shared memory; float32, d = 64,
   // 1543 tokens, 4 heads, window 300: 17 us, 25 with 2)
   constexpr int KT = sizeof(IO) == 2 ? 2 : 1, WN = D * sizeof(IO) <= 256 ? 4 : 2;
   const unsigned blocks = plan_tiles(z, z.Hq / z.Hk, 128, a.od);
   if (few_tiles(a.od)) {
     const unsigned few = plan_tiles(z, z.Hq / z.Hk, 32, a.od);
-    hipLaunchKernelGGL((gdn2_attn_dq_kernel<IO, D, 1, WN, 1>), dim3(few), dim3(64 * WN), 0, st, a);
+    if (a.sinks)
+      hipLaunchKernelGGL((gdn2_attn_dq_kernel<IO, D, 1, WN, 1, true>), dim3(few), dim3(64 * WN), 0, st, a);
+    else
+      hipLaunchKernelGGL((gdn2_attn_dq_kernel<IO, D, 1, WN, 1, false>), dim3(few), dim3(64 * WN), 0, st, a);
+  } else if (a.sinks) {
+    hipLaunchKernelGGL((gdn2_attn_dq_kernel<IO, D, 4, 1, KT, true>), dim3(blocks), dim3(256), 0, st, a);
   } else {
-    hipLaunchKernelGGL((gdn2_attn_dq_kernel<IO, D, 4, 1, KT>), dim3(blocks), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((gdn2_attn_dq_kernel<IO, D, 4, 1, KT, false>), dim3(blocks), dim3(256), 0, st, a);
   }
   return hipGetLastError();
 }
 template <typename IO, int D>
+hipError_t launch_attn_bwd_far(const attn_sizes &z, const attn_ptrs &p, void *ws, hipStream_t st) {
+  bwd_args a;
+  fill(a, z, p, ws, D);
+  const unsigned blocks = static_cast<unsigned>(z.N) * z.Hk * ((z.sinks + FAR_KEYS - 1) / FAR_KEYS) * a.far_parts;
+  hipLaunchKernelGGL((gdn2_attn_dkv_kernel<IO, D, FAR_KEYS / 32, FAR_ROWS<IO, D> / 32, DKV_FAR>), dim3(blocks),
+                     dim3(2 * FAR_ROWS<IO, D>), 0, st, a);
+  return hipGetLastError();
+}
+template <typename IO, int D, int WK, int WR>
+static void launch_dkv(const bwd_args &a, unsigned blocks, hipStream_t st) {
+  if (a.sinks)
+    hipLaunchKernelGGL((gdn2_attn_dkv_kernel<IO, D, WK, WR, DKV_SINK>), dim3(blocks), dim3(64 * WK * WR), 0, st, a);
+  else
+    hipLaunchKernelGGL((gdn2_attn_dkv_kernel<IO, D, WK, WR, DKV_PLAIN>), dim3(blocks), dim3(64 * WK * WR), 0, st, a);
+}
+template <typename IO, int D>
 hipError_t launch_attn_bwd_dkv(const attn_sizes &z, const attn_ptrs &p, void *ws, hipStream_t st) {
   bwd_args a;
-  fill(a, z, p, ws);
+  fill(a, z, p, ws, D);
   // Where the tiles do not give every CU two, the longest sequence's first
   // keys, which every row sees, take as long as the call: d = 64 then takes
   // half as many keys and twice the row parts a workgroup.  (bfloat16, 11 packed
@@ -642,20 +802,25 @@ hipError_t launch_attn_bwd_dkv(const attn_sizes &z, const attn_ptrs &p, void *ws
   constexpr int WKH = HALF ? WK / 2 : WK, WRH = D == 64 ? 4 : 2;
   unsigned blocks = plan_tiles(z, 1, 32 * WK, a.od);
   if (!HALF || (a.parts == 1 && static_cast<long long>(a.od.units) * a.od.tiles >= 512)) {
-    hipLaunchKernelGGL((gdn2_attn_dkv_kernel<IO, D, WK, 2>), dim3(blocks * a.parts), dim3(128 * WK), 0, st, a);
+    launch_dkv<IO, D, WK, 2>(a, blocks * a.parts, st);
   } else {
     blocks = plan_tiles(z, 1, 32 * WKH, a.od);
-    hipLaunchKernelGGL((gdn2_attn_dkv_kernel<IO, D, WKH, WRH>), dim3(blocks * a.parts), dim3(64 * WKH * WRH), 0, st, a);
+    launch_dkv<IO, D, WKH, WRH>(a, blocks * a.parts, st);
   }
   if (a.parts > 1) {
     const size_t n = static_cast<size_t>(z.Ttot) * z.Hk * D / 2;  // threads
-    hipLaunchKernelGGL((gdn2_attn_dkv_join_kernel<IO, D>), dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, st, a);
+    const dim3 grid(static_cast<unsigned>((n + 255) / 256));
+    if (a.sinks)
+      hipLaunchKernelGGL((gdn2_attn_dkv_join_kernel<IO, D, true>), grid, dim3(256), 0, st, a);
+    else
+      hipLaunchKernelGGL((gdn2_attn_dkv_join_kernel<IO, D, false>), grid, dim3(256), 0, st, a);
   }
   return hipGetLastError();
 }
 
 #define GDN2_INST_ATTN_BWD(IO, D)                                                                         \
   template hipError_t launch_attn_bwd_dq<IO, D>(const attn_sizes &, const attn_ptrs &, void *, hipStream_t); \
+  template hipError_t launch_attn_bwd_far<IO, D>(const attn_sizes &, const attn_ptrs &, void *, hipStream_t); \
   template hipError_t launch_attn_bwd_dkv<IO, D>(const attn_sizes &, const attn_ptrs &, void *, hipStream_t);
 GDN2_INST_ATTN_BWD(float, 64)
 GDN2_INST_ATTN_BWD(float, 128)

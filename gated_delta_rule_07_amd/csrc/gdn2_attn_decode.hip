@@ -38,7 +38,9 @@ __device__ __forceinline__ float group_max(float x) {
 // Lane l: row (or channel, or key) c = l % 16, group g = l / 16.  An
 // accumulator's register i is row 4g + i; an operand's slot (g, e) is k = 8g + e
 // ("row" order) or 16 (e / 4) + 4g + e % 4 ("acc" order: two accumulators).
-template <typename CT, int D, int TK>
+// SINK: keys are numbered without the gap between the sinks and the window, as
+// in gdn2_attn_fwd_kernel, both parts in whole 16-key tiles.
+template <typename CT, int D, int TK, bool SINK>
 __global__ void __launch_bounds__(256, 3) gdn2_attn_decode_kernel(fwd_args a) {
   constexpr bool F8 = sizeof(CT) == 1;
   typedef bf16_t IO;
@@ -67,6 +69,13 @@ __global__ void __launch_bounds__(256, 3) gdn2_attn_decode_kernel(fwd_args a) {
   int k_hi = kv_len;
   int k_lo = a.window > 0 ? shift - a.window + 1 : 0;
   k_lo = k_lo < 0 ? 0 : k_lo & ~15;
+  int gap = 0;
+  const int s16 = SINK ? (a.sinks + 15) & ~15 : 0;
+  if constexpr (SINK) {
+    gap = k_lo > s16 ? k_lo - s16 : 0;
+    k_lo = 0;
+    k_hi -= gap;
+  }
   int k0 = k_lo, k1 = k_hi;
   if (a.splits > 1) {
     const int nt = k_hi > k_lo ? (k_hi - k_lo + BN - 1) / BN : 0;
@@ -79,7 +88,7 @@ __global__ void __launch_bounds__(256, 3) gdn2_attn_decode_kernel(fwd_args a) {
   const bool row_ok = c < rows;
   const int cl_row = row_ok ? c : rows - 1;
   const int tok = cl_row / a.G, head = hk * a.G + cl_row % a.G;
-  const int pos = shift + tok, pos_lo = shift, pos_hi = shift + a.T - 1;
+  const int pos_lo = shift - gap, pos = pos_lo + tok, pos_hi = pos_lo + a.T - 1;
   const size_t qrow = (static_cast<size_t>(n_seq) * a.T + tok) * a.Hq + head;
 
   frag8<IO> q[NK];
@@ -95,13 +104,16 @@ __global__ void __launch_bounds__(256, 3) gdn2_attn_decode_kernel(fwd_args a) {
   const int pmask = (1 << a.page_shift) - 1;
   char *const vt = lds + wn * TILEB;
   float *const ksc = scales + wn * 2 * SN, *const vsc = ksc + SN;
+  // the key a tile starts with
+  auto tile_key = [&](int wk, int t) {
+    const int j = wk + 16 * t < k1 ? wk + 16 * t : (k1 - 1) & ~15;
+    return SINK && j >= s16 ? j + gap : j;
+  };
   int ent[TK];
   auto load_entries = [&](int wk) {
 #pragma unroll
-    for (int t = 0; t < TK; ++t) {
-      const int j = wk + 16 * t < k1 ? wk + 16 * t : (k1 - 1) & ~15;
-      ent[t] = table[j >> a.page_shift];
-    }
+    for (int t = 0; t < TK; ++t)
+      ent[t] = table[tile_key(wk, t) >> a.page_shift];
   };
   long row[TK];  // the tiles' first rows in the cache
   int bad = 0;   // tiles whose entry is outside it: their keys and values are zeros
@@ -109,7 +121,7 @@ __global__ void __launch_bounds__(256, 3) gdn2_attn_decode_kernel(fwd_args a) {
     bad = 0;
 #pragma unroll
     for (int t = 0; t < TK; ++t) {
-      const int j = wk + 16 * t < k1 ? wk + 16 * t : (k1 - 1) & ~15;
+      const int j = tile_key(wk, t);
       const bool ok = static_cast<unsigned>(ent[t]) < static_cast<unsigned>(a.num_pages);
       bad |= ok ? 0 : 1 << t;
       row[t] = ((static_cast<long>(ok ? ent[t] : 0) * a.Hk + hk) << a.page_shift) + (j & pmask);
@@ -244,6 +256,8 @@ __global__ void __launch_bounds__(256, 3) gdn2_attn_decode_kernel(fwd_args a) {
     // key of register i of tile t: wk + 16 t + 4 g + i
     const int hi_rel = (pos < k1 - 1 ? pos : k1 - 1) - wk - 4 * g;
     const int lo_rel = (a.window > 0 ? pos - a.window : -0x40000000) - wk - 4 * g;
+    const int sink_rel = SINK ? a.sinks - wk - 4 * g : 0;
+    auto visible = [&](int j) { return j <= hi_rel && (j > lo_rel || (SINK && j < sink_rel)); };
     float mx = neg_inf();
 #pragma unroll
     for (int t = 0; t < TK; ++t) {
@@ -252,7 +266,7 @@ __global__ void __launch_bounds__(256, 3) gdn2_attn_decode_kernel(fwd_args a) {
       if (masked) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          s[t][i] = (16 * t + i <= hi_rel && 16 * t + i > lo_rel) ? s[t][i] : neg_inf();
+          s[t][i] = visible(16 * t + i) ? s[t][i] : neg_inf();
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -280,7 +294,7 @@ __global__ void __launch_bounds__(256, 3) gdn2_attn_decode_kernel(fwd_args a) {
         const f32x4 w = *reinterpret_cast<const f32x4 *>(&vsc[16 * t + 4 * g]);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          s[t][i] = (!masked || (16 * t + i <= hi_rel && 16 * t + i > lo_rel)) ? s[t][i] * w[i] : 0.f;
+          s[t][i] = (!masked || visible(16 * t + i)) ? s[t][i] * w[i] : 0.f;
       }
     }
     bool odd = false;
@@ -313,7 +327,7 @@ __global__ void __launch_bounds__(256, 3) gdn2_attn_decode_kernel(fwd_args a) {
             p = 16 * t + i == (j & ~12) ? s[t][i] : p;
         p = __shfl(p, c + 16 * ((j >> 2) & 3), 64);
         const int jr = j - 4 * g;
-        const bool vis = jr <= hi_rel && jr > lo_rel;
+        const bool vis = visible(jr);
 #pragma unroll
         for (int n = 0; n < D / 16; ++n)
 #pragma unroll
@@ -367,7 +381,10 @@ template <typename CT, int D> hipError_t launch_attn_decode(const fwd_args &a, h
   // 136 us for 64 sequences of 4K to 16K keys)
   constexpr int TK = 2;
   const unsigned blocks = 8u * static_cast<unsigned>(a.od.units / a.od.g) * static_cast<unsigned>(a.od.tpr) * a.splits;
-  hipLaunchKernelGGL((gdn2_attn_decode_kernel<CT, D, TK>), dim3(blocks), dim3(256), 0, st, a);
+  if (a.sinks)
+    hipLaunchKernelGGL((gdn2_attn_decode_kernel<CT, D, TK, true>), dim3(blocks), dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL((gdn2_attn_decode_kernel<CT, D, TK, false>), dim3(blocks), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 template hipError_t launch_attn_decode<bf16_t, 64>(const fwd_args &, hipStream_t);

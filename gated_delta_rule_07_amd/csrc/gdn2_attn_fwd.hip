@@ -2,7 +2,7 @@
 // whole packed sequences, and over a paged cache.
 //
 //   s_ij = scale q_i . k_j for the visible keys j (j <= pos(i), and with a
-//   window W, j > pos(i) - W);  o_i = sum_j softmax(s_i)_j v_j;
+//   window W, j > pos(i) - W or, with S sinks, j < S);  o_i = sum_j softmax(s_i)_j v_j;
 //   lse_i = ln sum_j exp(s_ij).  A row that sees no key gives o = 0, lse = -inf.
 //
 // One pass over the keys with the running maximum m and sum l of each row
@@ -37,7 +37,11 @@
 namespace gdn2 {
 namespace attn {
 
-template <typename IO, typename CT, int D, int WM, int WN, int KT, bool PAGED>
+// SINK: the first `sinks` keys of the sequence stay visible behind the window.
+// The workgroup numbers the keys it visits without the gap between the two:
+// the sinks, then the keys from its first row's window on, so that few sinks
+// cost no tile of their own; positions are numbered with them.
+template <typename IO, typename CT, int D, int WM, int WN, int KT, bool PAGED, bool SINK>
 __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
     gdn2_attn_fwd_kernel(fwd_args a) {
   typedef tile<IO, D> TL;
@@ -110,6 +114,13 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
     k_lo = shift + t_lo - a.window + 1;
     k_lo = k_lo < 0 ? 0 : k_lo;
   }
+  // keys behind the sinks are numbered `gap` less than they are
+  int gap = 0;
+  if constexpr (SINK) {
+    gap = k_lo > a.sinks ? k_lo - a.sinks : 0;
+    k_lo = 0;
+    k_hi -= gap;
+  }
   int k0 = k_lo, k1 = k_hi;
   if (a.splits > 1) {
     const int nt = k_hi > k_lo ? (k_hi - k_lo + BN - 1) / BN : 0;
@@ -124,12 +135,12 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
   const bool row_ok = my_row < rows;
   const int cl_row = row_ok ? my_row : rows - 1;
   const int tok = cl_row / a.G, head = hk * a.G + cl_row % a.G;
-  const int pos = shift + tok;
+  const int pos = shift - gap + tok;
   const size_t qrow = static_cast<size_t>(sq.start + tok) * a.Hq + head;
   // positions of the wave's first and last row
   const int wr0 = row0 + 32 * wm < rows ? row0 + 32 * wm : rows - 1;
   const int wr1 = row0 + 32 * wm + 31 < rows ? row0 + 32 * wm + 31 : rows - 1;
-  const int pos_lo = shift + wr0 / a.G, pos_hi = shift + wr1 / a.G;
+  const int pos_lo = shift - gap + wr0 / a.G, pos_hi = shift - gap + wr1 / a.G;
 
   frag8<IO> q[SHARED ? D / 16 : 1];
   const IO *const qp = static_cast<const IO *>(a.q) + qrow * D;
@@ -158,6 +169,7 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
   int ent_b = 0;
   const int32_t *table = PAGED ? a.table + static_cast<size_t>(sq.n) * a.max_pages : nullptr;
   const int pmask = (1 << a.page_shift) - 1;
+  auto key_of = [&](int j) { return SINK && j >= a.sinks ? j + gap : j; };  // of a numbered key
   // Rows of the tile at key kb; one behind the last key stands for that key's
   // row (its score is masked).  Paged: the table's entries are fetched a tile
   // ahead of the rows they lead to.
@@ -166,17 +178,19 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
         const int j = kb + sr0 + ROWS_PER_I * i;
-        ent[i] = table[(j < k1 ? j : k1 - 1) >> a.page_shift];
+        ent[i] = table[key_of(j < k1 ? j : k1 - 1) >> a.page_shift];
       }
       if constexpr (F8) {
         const int j = kb + SN * wn + st % SN;
-        ent_b = table[(j < k1 ? j : k1 - 1) >> a.page_shift];
+        ent_b = table[key_of(j < k1 ? j : k1 - 1) >> a.page_shift];
       }
     }
   };
   const unsigned kstep = static_cast<unsigned>(a.Hk) * D;  // values of a token
   auto load_tile = [&](int kb, int buf) {
-    const size_t base = PAGED ? 0 : (static_cast<size_t>(sq.start + kb) * a.Hk + hk) * D;
+    // (a tile with sinks takes its keys one by one, from the sequence's first)
+    const bool mixed = SINK && kb < a.sinks;
+    const size_t base = PAGED ? 0 : (static_cast<size_t>(sq.start + (mixed ? 0 : kb + gap)) * a.Hk + hk) * D;
     const CT *const kp = static_cast<const CT *>(a.k) + base, *const vp = static_cast<const CT *>(a.v) + base;
     if constexpr (PAGED)
       bad = 0;
@@ -185,6 +199,7 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
       int j = kb + sr0 + ROWS_PER_I * i;
       j = j < k1 ? j : k1 - 1;
       if constexpr (PAGED) {
+        j = key_of(j);
         // (an entry outside the cache stands for zeros, see store_tile)
         const bool ok = static_cast<unsigned>(ent[i]) < static_cast<unsigned>(a.num_pages);
         bad |= ok ? 0 : 1 << i;
@@ -193,21 +208,27 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
         rk[i] = *reinterpret_cast<const u32x4 *>(kp + off);
         rv[i] = *reinterpret_cast<const u32x4 *>(vp + off);
       } else {
-        if constexpr (DMA) {
-          const unsigned off = static_cast<unsigned>(j - kb) * kstep + (sc ^ KV::f(sr0 + ROWS_PER_I * i)) * KV::VPC;
-          char *const to = lds + (buf * 2 * TILEB + 1024 * wv + 16 * NT * i);
-          dma16(kp + off, to);
-          dma16(vp + off, to + TILEB);
-        } else {
-          const unsigned off = static_cast<unsigned>(j - kb) * kstep + sc * KV::VPC;
-          rk[i] = *reinterpret_cast<const u32x4 *>(kp + off);
-          rv[i] = *reinterpret_cast<const u32x4 *>(vp + off);
-        }
+        auto bring = [&](auto off) {
+          if constexpr (DMA) {
+            off += (sc ^ KV::f(sr0 + ROWS_PER_I * i)) * KV::VPC;
+            char *const to = lds + (buf * 2 * TILEB + 1024 * wv + 16 * NT * i);
+            dma16(kp + off, to);
+            dma16(vp + off, to + TILEB);
+          } else {
+            off += sc * KV::VPC;
+            rk[i] = *reinterpret_cast<const u32x4 *>(kp + off);
+            rv[i] = *reinterpret_cast<const u32x4 *>(vp + off);
+          }
+        };
+        if (mixed)
+          bring(static_cast<size_t>(key_of(j)) * kstep);
+        else
+          bring(static_cast<unsigned>(j - kb) * kstep);
       }
     }
     if constexpr (F8) {
       int j = kb + SN * wn + st % SN;
-      j = j < k1 ? j : k1 - 1;
+      j = key_of(j < k1 ? j : k1 - 1);
       const bool ok = static_cast<unsigned>(ent_b) < static_cast<unsigned>(a.num_pages);
       bad |= ok ? 0 : 1 << CH;
       const size_t off = ((static_cast<size_t>(ok ? ent_b : 0) * a.Hk + hk) << a.page_shift) + (j & pmask);
@@ -277,7 +298,8 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
     const float *const ksc = kscale + buf * 2 * SN, *const vsc = vscale + buf * 2 * SN;
     const int wk = kb + SN * wn;  // the wave's first key
     // no rows, or nothing of the tile is visible to the wave
-    if (row0 + 32 * wm >= rows || wk > pos_hi || wk >= k1 || (a.window > 0 && wk + 32 * KT - 1 <= pos_lo - a.window))
+    if (row0 + 32 * wm >= rows || wk > pos_hi || wk >= k1 ||
+        (a.window > 0 && wk + 32 * KT - 1 <= pos_lo - a.window && !(SINK && wk < a.sinks)))
       continue;
     const bool masked = wk + 32 * KT - 1 > pos_lo || wk + 32 * KT > k1 ||
                         (a.window > 0 && wk <= pos_hi - a.window);
@@ -327,16 +349,18 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
         }
     }
     // key of register i: wk + 32 t + 8 (i / 4) + 4 h + i % 4; visible when
-    // j <= pos, j > pos - W and j < k1
+    // j <= pos, j > pos - W (or a sink) and j < k1
     const int hi_rel = (pos < k1 - 1 ? pos : k1 - 1) - wk - 4 * h;
     const int lo_rel = (a.window > 0 ? pos - a.window : -0x40000000) - wk - 4 * h;
+    const int sink_rel = SINK ? a.sinks - wk - 4 * h : 0;
+    auto visible = [&](int j) { return j <= hi_rel && (j > lo_rel || (SINK && j < sink_rel)); };
     if (masked) {
 #pragma unroll
       for (int t = 0; t < KT; ++t)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int j = 32 * t + 8 * (i >> 2) + (i & 3);
-          s[t][i] = (j <= hi_rel && j > lo_rel) ? s[t][i] : neg_inf();
+          s[t][i] = visible(j) ? s[t][i] : neg_inf();
         }
     }
     float mx = s[0][0];
@@ -385,7 +409,7 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int j = 32 * t + 8 * g + i;
-            s[t][4 * g + i] = (!masked || (j <= hi_rel && j > lo_rel)) ? s[t][4 * g + i] * sc4[i] : 0.f;
+            s[t][4 * g + i] = (!masked || visible(j)) ? s[t][4 * g + i] * sc4[i] : 0.f;
           }
         }
     }
@@ -427,7 +451,7 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
             p = (32 * t + 8 * (i >> 2) + (i & 3)) == j - 4 * ((j >> 2) & 1) ? s[t][i] : p;
         p = __shfl(p, r + 32 * ((j >> 2) & 1), 64);
         const int jr = j - 4 * h;
-        const bool vis = jr <= hi_rel && jr > lo_rel;
+        const bool vis = visible(jr);
 #pragma unroll
         for (int n = 0; n < D / 32; ++n)
 #pragma unroll
@@ -597,19 +621,25 @@ int attn_paged_splits(const attn_sizes &z) {
   plan_tiles(z, z.Hq / z.Hk, few ? 32 : 128, od);
   const long long blocks = static_cast<long long>(od.units) * od.tiles;
   long long keys = z.max_keys;
-  if (z.window > 0 && keys > z.window + 128LL)
-    keys = z.window + 128LL;
+  if (z.window > 0 && keys > z.window + z.sinks + 128LL)
+    keys = z.window + z.sinks + 128LL;
   long long s = ((few ? 2048 : 768) + blocks - 1) / blocks;
   if (s > keys / 128)
     s = keys / 128;
   return s < 1 ? 1 : (s > 128 ? 128 : static_cast<int>(s));
 }
 
+template <typename IO, typename CT, int D, int WM, int WN, int KT, bool PAGED, bool SINK>
+static hipError_t launch(fwd_args &a, const attn_sizes &z, hipStream_t st) {
+  const unsigned blocks = plan_tiles(z, a.G, 32 * WM, a.od) * a.splits;
+  hipLaunchKernelGGL((gdn2_attn_fwd_kernel<IO, CT, D, WM, WN, KT, PAGED, SINK>), dim3(blocks), dim3(64 * WM * WN), 0, st,
+                     a);
+  return hipGetLastError();
+}
 template <typename IO, typename CT, int D, int WM, int WN, int KT, bool PAGED>
 static hipError_t go(fwd_args &a, const attn_sizes &z, hipStream_t st) {
-  const unsigned blocks = plan_tiles(z, a.G, 32 * WM, a.od) * a.splits;
-  hipLaunchKernelGGL((gdn2_attn_fwd_kernel<IO, CT, D, WM, WN, KT, PAGED>), dim3(blocks), dim3(64 * WM * WN), 0, st, a);
-  return hipGetLastError();
+  return a.sinks ? launch<IO, CT, D, WM, WN, KT, PAGED, true>(a, z, st)
+                 : launch<IO, CT, D, WM, WN, KT, PAGED, false>(a, z, st);
 }
 
 static void fill(fwd_args &a, const attn_sizes &z, const attn_ptrs &p) {
@@ -634,6 +664,7 @@ static void fill(fwd_args &a, const attn_sizes &z, const attn_ptrs &p) {
   a.num_pages = z.num_pages;
   a.page_shift = z.page_shift;
   a.window = z.window;
+  a.sinks = z.sinks;
   a.splits = 1;
   a.c = z.scale * LOG2E;
 }

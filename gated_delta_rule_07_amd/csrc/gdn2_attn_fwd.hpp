@@ -19,7 +19,7 @@ struct fwd_args {
   int N, T, Hq, Hk, G;
   int Ttot;                  // tokens of q in all
   int max_pages, num_pages, page_shift;
-  int window, splits;
+  int window, sinks, splits;  // sinks: 0 without a window
   float c;                   // scale log2 e
   order od;
 };

@@ -22,7 +22,7 @@ namespace attn {
 struct attn_sizes {
   int N, T, Ttot, Hq, Hk;
   bool packed;
-  int window;
+  int window, sinks;  // sinks: first keys that stay visible behind the window (0 without one)
   float scale;
   int max_pages, num_pages, page_shift;
   long long max_keys;
@@ -60,6 +60,15 @@ inline size_t attn_bwd_bytes(const attn_sizes &z, int d) {
 }
 template <typename IO, int D>
 hipError_t launch_attn_bwd_dq(const attn_sizes &z, const attn_ptrs &p, void *ws, hipStream_t st);
+// With sinks, between the two: sums of dk and dv of the sinks over the rows
+// that see them from behind the window, which launch_attn_bwd_dkv adds; they
+// follow in ws.
+int attn_bwd_far_parts(const attn_sizes &z);
+inline size_t attn_bwd_far_bytes(const attn_sizes &z, int d) {
+  return z.sinks ? static_cast<size_t>(attn_bwd_far_parts(z)) * 2 * z.N * z.sinks * z.Hk * d * 4 : 0;
+}
+template <typename IO, int D>
+hipError_t launch_attn_bwd_far(const attn_sizes &z, const attn_ptrs &p, void *ws, hipStream_t st);
 template <typename IO, int D>
 hipError_t launch_attn_bwd_dkv(const attn_sizes &z, const attn_ptrs &p, void *ws, hipStream_t st);
 

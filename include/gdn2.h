@@ -403,6 +403,8 @@ gdn2_status_t gdn2_decode_step(const void *q, const void *k, const void *v, cons
  *   gdn2_attn_paged                new tokens over the paged cache (decode,
  *                                  chunks of a prompt), next to
  *                                  gdn2_decode_step
+ *   gdn2_attn_sink_fwd / _bwd /    the same attention where a window's layer
+ *   _paged                         keeps its first tokens visible
  * The conventions at the top hold: contiguous token-major device tensors of
  * dtype dt (16-byte aligned), packed sequences by cu_seqlens with B = 1, all
  * work enqueued on `stream`, nothing allocated.  q and o are [B, T, Hq, d],
@@ -542,6 +544,38 @@ gdn2_status_t gdn2_attn_paged(const void *q, const void *k_cache, const void *v_
                               int num_pages, int page_size, int max_pages, int window, float scale, gdn2_dtype_t dt,
                               gdn2_dtype_t cache_dt, void *o, float *lse, void *workspace, size_t workspace_bytes,
                               void *stream);
+
+/* Attention with a sliding window and `sinks` first tokens of every sequence
+ * that stay visible behind it: key j of the same sequence is visible to
+ * position i when j <= i and (j > i - window or j < sinks).  Arguments and
+ * results as for gdn2_attn_fwd, gdn2_attn_bwd and gdn2_attn_paged; sinks >= 0,
+ * without effect where window is 0.  Where the window hides anything (window +
+ * sinks less than the longest sequence) sinks is at most 1024
+ * (GDN2_ERR_UNSUPPORTED).  In the paged form the sinks are the sequence's
+ * first keys; table entries whose page holds neither a sink nor a key of a
+ * query's window are not read, so such pages can be freed and used again. */
+gdn2_status_t gdn2_attn_sink_fwd(const void *q, const void *k, const void *v, const int32_t *cu_seqlens, int B, int T,
+                                 int Hq, int Hk, int d, int num_seqs, int window, int sinks, float scale,
+                                 gdn2_dtype_t dt, void *o, float *lse, void *stream);
+
+/* Bytes of workspace gdn2_attn_sink_bwd needs with any window (num_seqs 0: B
+ * sequences of T tokens; else packed, B = 1 and T tokens in all). */
+size_t gdn2_attn_sink_bwd_workspace_bytes(int B, int T, int Hq, int Hk, int d, int num_seqs, int sinks);
+
+gdn2_status_t gdn2_attn_sink_bwd(const void *q, const void *k, const void *v, const void *o, const float *lse,
+                                 const void *dout, const int32_t *cu_seqlens, int B, int T, int Hq, int Hk, int d,
+                                 int num_seqs, int window, int sinks, float scale, gdn2_dtype_t dt, void *dq, void *dk,
+                                 void *dv, void *workspace, size_t workspace_bytes, void *stream);
+
+size_t gdn2_attn_sink_paged_workspace_bytes(int B, int T, int Hq, int Hk, int d, int num_seqs, int page_size,
+                                            int max_pages, int window, int sinks);
+
+gdn2_status_t gdn2_attn_sink_paged(const void *q, const void *k_cache, const void *v_cache, const uint8_t *k_scale,
+                                   const uint8_t *v_scale, const int32_t *block_table, const int32_t *seq_lens,
+                                   const int32_t *cu_seqlens, int B, int T, int Hq, int Hk, int d, int num_seqs,
+                                   int num_pages, int page_size, int max_pages, int window, int sinks, float scale,
+                                   gdn2_dtype_t dt, gdn2_dtype_t cache_dt, void *o, float *lse, void *workspace,
+                                   size_t workspace_bytes, void *stream);
 
 /* Static text of a status code. */
 const char *gdn2_status_string(gdn2_status_t status);
