@@ -112,6 +112,10 @@ def configure(L: ctypes.CDLL) -> ctypes.CDLL:
     L.gdn2_kv_cache_write.argtypes = [vp] * 3 + [i] * 7 + [vp] * 5
     L.gdn2_kv_cache_read.restype = i
     L.gdn2_kv_cache_read.argtypes = [vp] + [i] * 7 + [vp] * 7
+    i64 = ctypes.c_int64
+    L.gdn2_kv_cache_append.restype = i
+    L.gdn2_kv_cache_append.argtypes = ([vp] * 3 + [i64] * 3 + [vp] * 5 + [i] * 6 + [f] + [i] * 4 + [u32, vp, i64] +
+                                       [vp] * 5)
     L.gdn2_status_string.restype = ctypes.c_char_p
     L.gdn2_status_string.argtypes = [i]
     L.gdn2_last_error.restype = ctypes.c_char_p
@@ -434,5 +438,5 @@ def profile_read(reset: bool = True) -> dict:
 
 
 from .attention import (attn_bwd, attn_bwd_workspace_bytes, attn_fwd, attn_paged,  # noqa: E402,F401
-                        attn_paged_workspace_bytes, kv_cache_read, kv_cache_write, qk_norm_rope, qk_norm_rope_bwd,
-                        rope_frequencies)
+                        attn_paged_workspace_bytes, kv_cache_append, kv_cache_read, kv_cache_write, qk_norm_rope,
+                        qk_norm_rope_bwd, rope_frequencies)

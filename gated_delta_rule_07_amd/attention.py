@@ -323,6 +323,67 @@ def kv_cache_write(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None) ->
           _ptr(v_cache), _ptr(k_scale), _ptr(v_scale))
 
 
+def _tokens(t, name: str, shape, dtype, dev: int) -> int:
+    """Values between two tokens of t [B, T, H, d]: each token's heads are
+    contiguous, the tokens the same distance apart throughout."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}, not {list(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError("libgdn2 takes device tensors")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on another device ({t.device})")
+    B, T, H, d = shape
+    sb, st, sh, sd = t.stride()
+    if sd != 1 or (H > 1 and sh != d):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    if T <= 1:
+        return sb if B > 1 and T == 1 else H * d
+    if B > 1 and sb != T * st:
+        raise ValueError(f"the tokens of {name} must be the same distance apart throughout")
+    return st
+
+
+def kv_cache_append(q, k, v, slots, k_cache, v_cache, freqs, wq=None, wk=None, positions=None, interleaved: bool = False,
+                    norm: bool = True, eps: float = 1e-6, k_scale=None, v_scale=None, out=None):
+    """``qk_norm_rope`` of new tokens and ``kv_cache_write`` of their keys and
+    values in one pass: q [B, T, Hq, d] normed and rotated into ``out`` (which
+    may be q), k [B, T, Hk, d] normed and rotated into ``slots`` (int64, B T
+    values) of k_cache, rounded once, v into those of v_cache.  q, k, v and
+    ``out`` may be views with any distance between tokens (parts of one
+    projection, say), each token's heads contiguous.  A token whose slot is
+    outside the cache (-1) leaves its query only.  Other arguments as in those
+    two; ``freqs`` may be None.  Returns q's output."""
+    dev = _device(slots, freqs, wq, wk, positions, k_cache, v_cache, k_scale, v_scale)
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q, k and v must be [B, T, H, d]")
+    B, T, Hq, d = q.shape
+    Hk, dt = k.shape[2], q.dtype
+    if out is None:
+        out = torch.empty(q.shape, dtype=dt, device=q.device)
+    strides = [_tokens(t, n, (B, T, h, d), dt, dev) for t, n, h in ((q, "q", Hq), (k, "k", Hk), (v, "v", Hk),
+                                                                     (out, "out", Hq))]
+    _like(wq, "wq", (d,), torch.float32)
+    _like(wk, "wk", (d,), torch.float32)
+    _like(positions, "positions", (B, T), torch.int32)
+    if slots.dtype != torch.int64 or slots.numel() != B * T:
+        raise TypeError(f"slots must be {B * T} int64 values")
+    rot = 0
+    if freqs is not None:
+        if freqs.dtype != torch.float64 or freqs.dim() != 1:
+            raise TypeError("freqs must be a 1-D float64 tensor")
+        rot = 2 * freqs.numel()
+    flags = (ROPE_INTERLEAVED if interleaved else 0) | (0 if norm else ROPE_NO_NORM)
+    P, Hc, page, dc, code = _cache(k_cache, v_cache, k_scale, v_scale, dt)
+    if (Hc, dc) != (Hk, d):
+        raise ValueError(f"the cache's rows are [{Hc}, {dc}], the keys' [{Hk}, {d}]")
+    _call(dev, lib().gdn2_kv_cache_append, _ptr(q), _ptr(k), _ptr(v), *strides[:3], _ptr(wq), _ptr(wk), _ptr(freqs),
+          _ptr(positions), _ptr(slots), B, T, Hq, Hk, d, rot, eps, P, page, _dtype_code(q), code, flags, _ptr(out),
+          strides[3], _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale))
+    return out
+
+
 def kv_cache_read(slots, k_cache, v_cache, k_scale=None, v_scale=None, dtype=None, out=None):
     """The keys and values of ``slots`` (int64 [n]), each [n, Hk, d] of
     ``dtype`` (a quantised cache: bfloat16 by default, both exact, but for

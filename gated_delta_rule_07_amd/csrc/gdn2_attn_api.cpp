@@ -571,4 +571,60 @@ gdn2_status_t gdn2_kv_cache_read(const int64_t *slots, int n, int Hk, int d, int
                      k_scale, v_scale, false, stream);
 }
 
+gdn2_status_t gdn2_kv_cache_append(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                                   int64_t v_stride, const float *wq, const float *wk, const double *freqs,
+                                   const int32_t *positions, const int64_t *slots, int B, int T, int Hq, int Hk, int d,
+                                   int rotary_dim, float eps, int num_pages, int page_size, gdn2_dtype_t dt,
+                                   gdn2_dtype_t cache_dt, uint32_t flags, void *q_out, int64_t q_out_stride,
+                                   void *k_cache, void *v_cache, uint8_t *k_scale, uint8_t *v_scale, void *stream) {
+  const char *fn = "gdn2_kv_cache_append";
+  gdn2_status_t st = check_rope(fn, B, T, Hq, Hk, d, rotary_dim, freqs, eps, dt, flags, wq, wk);
+  if (st != GDN2_OK)
+    return st;
+  st = check_cache(fn, num_pages, page_size, dt, cache_dt, k_scale, v_scale);
+  if (st != GDN2_OK)
+    return st;
+  if (static_cast<long long>(B) * T * (static_cast<long long>(Hq) + 2LL * Hk) > MAX_ROWS)
+    return fail(GDN2_ERR_UNSUPPORTED, "%s: too large (at most 2^26 - 1 query, key and value rows)", fn);
+  const int per16 = dt == GDN2_F32 ? 4 : 8;
+  const struct {
+    const char *name;
+    int64_t stride;
+    int heads;
+  } strides[] = {{"q", q_stride, Hq}, {"k", k_stride, Hk}, {"v", v_stride, Hk}, {"q_out", q_out_stride, Hq}};
+  for (const auto &x : strides)
+    if (x.stride < static_cast<int64_t>(x.heads) * d || x.stride > 0xffffffffLL || x.stride % per16 != 0)
+      return fail(GDN2_ERR_INVALID_ARGUMENT,
+                  "%s: token stride %lld of %s (at least %lld values, less than 2^32, a multiple of 16 bytes)", fn,
+                  static_cast<long long>(x.stride), x.name, static_cast<long long>(x.heads) * d);
+  if (T == 0)
+    return ok();
+  st = check_ptrs(fn, {q, k, v, q_out, k_cache, v_cache}, {wq, wk, freqs, positions});
+  if (st != GDN2_OK)
+    return st;
+  if (!slots || (reinterpret_cast<uintptr_t>(slots) & 7u))
+    return fail(GDN2_ERR_INVALID_ARGUMENT, "%s: slots must be an aligned pointer", fn);
+  if (q_out == q && q_out_stride != q_stride)
+    return fail(GDN2_ERR_INVALID_ARGUMENT, "%s: q_out in place of q needs q's stride", fn);
+  const rope_call z = rope_of(q, k, wq, wk, freqs, positions, B, T, Hq, Hk, rotary_dim, eps, flags, q_out, nullptr);
+  cache_call c = {};
+  c.v = const_cast<void *>(v);
+  c.kc = k_cache;
+  c.vc = v_cache;
+  c.ks = k_scale;
+  c.vs = v_scale;
+  c.slots = slots;
+  c.tokens = static_cast<int>(z.tokens);
+  c.Hk = Hk;
+  c.num_pages = num_pages;
+  c.page_shift = page_shift(page_size);
+  const gdn2::attn::append_strides t = {static_cast<long>(q_stride), static_cast<long>(k_stride),
+                                        static_cast<long>(v_stride), static_cast<long>(q_out_stride)};
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e;
+  prof_scope p("kv_cache_append", s);
+  GDN2_CACHE_DISPATCH(e, dt, cache_dt == GDN2_F8E4M3, d, launch_kv_append, z, c, t, s);
+  return launched(fn, e);
+}
+
 }  // extern "C"

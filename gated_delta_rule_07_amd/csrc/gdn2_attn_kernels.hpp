@@ -101,6 +101,14 @@ struct cache_call {
 };
 template <typename IO, typename CT, int D> hipError_t launch_kv_cache(const cache_call &z, bool write, hipStream_t st);
 
+// New tokens: q and k normed and rotated (z; z.k the keys, no z.ok), k and v
+// (c.v) into the slots.  Values between two tokens:
+struct append_strides {
+  long q, k, v, q_out;
+};
+template <typename IO, typename CT, int D>
+hipError_t launch_kv_append(const rope_call &z, const cache_call &c, const append_strides &t, hipStream_t st);
+
 }  // namespace attn
 
 }  // namespace gdn2

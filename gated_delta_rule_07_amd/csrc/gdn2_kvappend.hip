@@ -1,0 +1,136 @@
+// gdn2_kvappend.hip -- new tokens into the paged cache: the norm and rotation of
+// their queries and keys (gdn2_qkrope.hip) and the write of keys and values
+// (gdn2_kvcache.hip) in one pass, for gfx950.
+//
+//   q_out = R(pos) norm(q);  row of k_cache = R(pos) norm(k);  row of v_cache = v
+//
+// In two calls the rotated keys pass through memory once more, rounded to the
+// tensors' type on the way; here a key is formed in float32 and rounded once,
+// to the cache's type.  The bound is memory (every value read and written
+// once), for a decode batch a launch's latency.  A wave takes a token's heads,
+// D / 8 lanes a head (q's, then k's, then v's), as in gdn2_rope_fwd_kernel, so
+// that the sines and cosines are formed once a token and a row's sum and
+// largest magnitude take 3 or 4 lane exchanges.
+#include "gdn2_kvrow.hpp"
+#include "gdn2_rope.hpp"
+
+namespace gdn2 {
+namespace attn {
+
+struct append_args {
+  rope_args r;
+  const void *v;
+  long qs, ks, vs, os;  // values between two tokens of q, k, v and q's output
+  void *kc, *vc;
+  uint8_t *ksc, *vsc;
+  const int64_t *slots;
+  int page_shift;
+  long nslots;
+};
+
+template <typename IO, typename CT, int D> __global__ void __launch_bounds__(256) gdn2_kv_append_kernel(append_args A) {
+  constexpr int LPH = D / 8, HPW = 64 / LPH;
+  constexpr bool F8 = sizeof(CT) == 1;
+  const rope_args &R = A.r;
+  const int lane = threadIdx.x & 63, j = lane % LPH, hh = lane / LPH;
+  const long u = static_cast<long>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (u >= R.tokens * R.parts)
+    return;
+  const long token = u / R.parts;
+  const int part = static_cast<int>(u % R.parts);
+  const int64_t slot = A.slots[token];
+  const bool kept = slot >= 0 && slot < A.nslots;
+  const lane_map m = map_lane<D>(R, j);
+  f32x4 c, s;
+  turn_of(R, m, j, token, c, s);
+  f32x4 wqa = ones(), wqb = ones(), wka = ones(), wkb = ones();
+  if (R.wq) {
+    wqa = io<float>::load4(R.wq + m.a);
+    wqb = io<float>::load4(R.wq + m.b);
+  }
+  if (R.wk) {
+    wka = io<float>::load4(R.wk + m.a);
+    wkb = io<float>::load4(R.wk + m.b);
+  }
+  const int heads = R.Hq + 2 * R.Hk;
+  // every lane stays in the loop (the rows' exchanges need whole rows)
+  for (int h0 = part * HPW; h0 < heads; h0 += R.parts * HPW) {
+    const int hd = h0 + hh, hk = hd < R.Hq + R.Hk ? hd - R.Hq : hd - R.Hq - R.Hk;
+    const bool ok = hd < heads, isq = hd < R.Hq, isv = hd >= R.Hq + R.Hk;
+    const IO *x = isq   ? static_cast<const IO *>(R.q) + token * A.qs + static_cast<long>(hd) * D
+                  : isv ? static_cast<const IO *>(A.v) + token * A.vs + static_cast<long>(hk) * D
+                        : static_cast<const IO *>(R.k) + token * A.ks + static_cast<long>(hk) * D;
+    f32x4 a = {0.f, 0.f, 0.f, 0.f}, b = a;
+    if (ok) {
+      a = io<IO>::load4(x + m.a);
+      b = io<IO>::load4(x + m.b);
+    }
+    if (R.norm) {
+      const float r = 1.f / sqrtf(row_sum<D>(dot4(a, a) + dot4(b, b)) * (1.f / D) + R.eps);
+      if (!isv) {
+        a = a * r * (isq ? wqa : wka);
+        b = b * r * (isq ? wqb : wkb);
+      }
+    }
+    if (m.turned && !isv)
+      rotate(R.interleaved, c, s, 1.f, a, b);
+    u32x2 code = {0u, 0u};
+    uint8_t byte = 0;
+    if constexpr (F8)
+      byte = quantise_row<D>(a, b, code);
+    if (!ok)
+      continue;
+    if (isq) {
+      IO *y = static_cast<IO *>(R.oq) + token * A.os + static_cast<long>(hd) * D;
+      io<IO>::store4(y + m.a, a);
+      io<IO>::store4(y + m.b, b);
+    } else if (kept) {
+      const size_t row = cache_row(slot, R.Hk, hk, A.page_shift);
+      CT *y = static_cast<CT *>(isv ? A.vc : A.kc) + row * D;
+      if constexpr (F8) {
+        *reinterpret_cast<unsigned *>(y + m.a) = code[0];
+        *reinterpret_cast<unsigned *>(y + m.b) = code[1];
+        if (j == 0)
+          (isv ? A.vsc : A.ksc)[row] = byte;
+      } else {
+        io<IO>::store4(y + m.a, a);
+        io<IO>::store4(y + m.b, b);
+      }
+    }
+  }
+}
+
+template <typename IO, typename CT, int D>
+hipError_t launch_kv_append(const rope_call &z, const cache_call &c, const append_strides &t, hipStream_t st) {
+  append_args A;
+  A.r = pack_rope(z);
+  A.r.parts = rope_parts(z.tokens, z.Hq + 2 * z.Hk, D);
+  A.v = c.v;
+  A.qs = t.q;
+  A.ks = t.k;
+  A.vs = t.v;
+  A.os = t.q_out;
+  A.kc = c.kc;
+  A.vc = c.vc;
+  A.ksc = c.ks;
+  A.vsc = c.vs;
+  A.slots = c.slots;
+  A.page_shift = c.page_shift;
+  A.nslots = static_cast<long>(c.num_pages) << c.page_shift;
+  const long waves = z.tokens * A.r.parts;
+  hipLaunchKernelGGL((gdn2_kv_append_kernel<IO, CT, D>), dim3(static_cast<unsigned>((waves + 3) / 4)), dim3(256), 0, st, A);
+  return hipGetLastError();
+}
+
+#define GDN2_INST_APPEND(IO, D)                                                                                  \
+  template hipError_t launch_kv_append<IO, IO, D>(const rope_call &, const cache_call &, const append_strides &, \
+                                                  hipStream_t);                                                  \
+  template hipError_t launch_kv_append<IO, f8_t, D>(const rope_call &, const cache_call &, const append_strides &, \
+                                                    hipStream_t);
+GDN2_INST_APPEND(float, 64)
+GDN2_INST_APPEND(float, 128)
+GDN2_INST_APPEND(bf16_t, 64)
+GDN2_INST_APPEND(bf16_t, 128)
+
+}  // namespace attn
+}  // namespace gdn2

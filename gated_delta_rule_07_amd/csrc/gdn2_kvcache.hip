@@ -18,27 +18,10 @@
 // tokens x 4 kv heads, d = 128, bfloat16 to e4m3: write 19.3 us (102 MB,
 // 5.3 TB/s), read 17.6 us (5.8 TB/s); a batch of 333 tokens x 3 heads, d = 64:
 // 3.5 us each, a launch's own latency.
-#include "gdn2_attn.hpp"
+#include "gdn2_kvrow.hpp"
 
 namespace gdn2 {
 namespace attn {
-
-template <int D> __device__ __forceinline__ float row_max(float x) {
-#pragma unroll
-  for (int s = 1; s < D / 8; s <<= 1)
-    x = fmaxf(x, __shfl_xor(x, s, 64));
-  return x;
-}
-
-// The exponent byte of a row with largest magnitude amax (finite).
-__device__ __forceinline__ int exponent_byte(float amax) {
-  if (amax == 0.f)
-    return 127;
-  int k;
-  const float f = frexpf(amax, &k);                // amax = f 2^k, f in [0.5, 1)
-  const int e = f <= 0.875f ? k - 9 : k - 8;       // 448 = 0.875 * 2^9
-  return (e < -126 ? -126 : e) + 127;
-}
 
 template <typename IO, int D>
 __device__ __forceinline__ void write_row(const IO *x, f8_t *codes, uint8_t *scale, int j, bool ok) {
@@ -47,30 +30,12 @@ __device__ __forceinline__ void write_row(const IO *x, f8_t *codes, uint8_t *sca
     a = io<IO>::load4(x + 8 * j);
     b = io<IO>::load4(x + 8 * j + 4);
   }
-  float m = 0.f;
-  bool odd = false;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    odd = odd || !(fabsf(a[i]) <= 3.4028234663852886e38f) || !(fabsf(b[i]) <= 3.4028234663852886e38f);
-    m = fmaxf(m, fmaxf(fabsf(a[i]), fabsf(b[i])));
-  }
-  m = row_max<D>(odd ? __builtin_inff() : m);
-  const bool bad = m == __builtin_inff();
-  const int byte = bad ? 255 : exponent_byte(m);
-  // 2^-e, a normal number: e is -126 .. 120
-  const float inv = bad ? 0.f : __builtin_bit_cast(float, static_cast<uint32_t>(254 - byte) << 23);
   u32x2 w;
-  int p = 0;
-  p = __builtin_amdgcn_cvt_pk_fp8_f32(bad ? 0.f : a[0] * inv, bad ? 0.f : a[1] * inv, p, false);
-  p = __builtin_amdgcn_cvt_pk_fp8_f32(bad ? 0.f : a[2] * inv, bad ? 0.f : a[3] * inv, p, true);
-  w[0] = p;
-  p = __builtin_amdgcn_cvt_pk_fp8_f32(bad ? 0.f : b[0] * inv, bad ? 0.f : b[1] * inv, p, false);
-  p = __builtin_amdgcn_cvt_pk_fp8_f32(bad ? 0.f : b[2] * inv, bad ? 0.f : b[3] * inv, p, true);
-  w[1] = p;
+  const uint8_t byte = quantise_row<D>(a, b, w);
   if (ok) {
     *reinterpret_cast<u32x2 *>(codes + 8 * j) = w;
     if (j == 0)
-      *scale = static_cast<uint8_t>(byte);
+      *scale = byte;
   }
 }
 template <typename IO, int D>
@@ -116,10 +81,8 @@ __global__ void __launch_bounds__(256) gdn2_kv_cache_kernel(cache_args A) {
   const int64_t slot = in ? A.slots[tok] : -1;
   const bool ok = slot >= 0 && slot < A.nslots;
   size_t at = 0;
-  if (ok) {
-    const size_t page = static_cast<size_t>(slot) >> A.page_shift, off = slot & ((1ll << A.page_shift) - 1);
-    at = ((page * A.Hk + hk) << A.page_shift) + off;
-  }
+  if (ok)
+    at = cache_row(slot, A.Hk, hk, A.page_shift);
   CT *kc = static_cast<CT *>(A.kc) + at * D, *vc = static_cast<CT *>(A.vc) + at * D;
   IO *k = static_cast<IO *>(A.k) + row * D, *v = static_cast<IO *>(A.v) + row * D;
   if constexpr (WRITE) {

@@ -400,6 +400,8 @@ gdn2_status_t gdn2_decode_step(const void *q, const void *k, const void *v, cons
  *                                  prompts), next to gdn2_chunk_fwd / _bwd
  *   gdn2_kv_cache_write / _read    the paged cache, its values as they are or
  *                                  quantised to 8 bits
+ *   gdn2_kv_cache_append           norm, rotation and write of new tokens in
+ *                                  one pass
  *   gdn2_attn_paged                new tokens over the paged cache (decode,
  *                                  chunks of a prompt), next to
  *                                  gdn2_decode_step
@@ -515,6 +517,25 @@ gdn2_status_t gdn2_kv_cache_write(const void *k, const void *v, const int64_t *s
 gdn2_status_t gdn2_kv_cache_read(const int64_t *slots, int n, int Hk, int d, int num_pages, int page_size,
                                  gdn2_dtype_t dt, gdn2_dtype_t cache_dt, const void *k_cache, const void *v_cache,
                                  const uint8_t *k_scale, const uint8_t *v_scale, void *k, void *v, void *stream);
+
+/* New tokens into the cache in one pass: q_out = R(position) norm(q), the
+ * slots' rows of k_cache R(position) norm(k) and of v_cache v, as
+ * gdn2_qk_norm_rope_fwd and gdn2_kv_cache_write would leave them in turn, but
+ * that a key is rounded once, from float32 to the cache's type.  q, q_out are
+ * [B, T, Hq, d], k and v [B, T, Hk, d], each token's heads contiguous and
+ * token i (of B T) at i times the tensor's stride, in values: at least its
+ * heads times d, less than 2^32, a multiple of 16 bytes; so q, k and v may be
+ * parts of one projection's rows.  slots: int64 [B T], as for
+ * gdn2_kv_cache_write (a token whose slot is outside the cache leaves its
+ * query only; no slot twice).  wq, wk, freqs, positions, rotary_dim, eps and
+ * flags as for gdn2_qk_norm_rope_fwd, the cache's arguments as for
+ * gdn2_kv_cache_write.  q_out may be q itself, with its stride. */
+gdn2_status_t gdn2_kv_cache_append(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                                   int64_t v_stride, const float *wq, const float *wk, const double *freqs,
+                                   const int32_t *positions, const int64_t *slots, int B, int T, int Hq, int Hk, int d,
+                                   int rotary_dim, float eps, int num_pages, int page_size, gdn2_dtype_t dt,
+                                   gdn2_dtype_t cache_dt, uint32_t flags, void *q_out, int64_t q_out_stride,
+                                   void *k_cache, void *v_cache, uint8_t *k_scale, uint8_t *v_scale, void *stream);
 
 /* Bytes of workspace gdn2_attn_paged needs: B sequences of T new tokens
  * (num_seqs 0), or num_seqs packed sequences of T new tokens in all (B = 1).
