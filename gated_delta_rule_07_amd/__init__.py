@@ -14,7 +14,8 @@ fallback: without the library or a GPU these functions raise.
 
 and, for the attention layers of a hybrid stack (see ``attention``),
 ``qk_norm_rope``, ``qk_norm_rope_bwd``, ``rope_frequencies``, ``attn_fwd``,
-``attn_bwd``, ``attn_paged``, ``kv_cache_write`` and ``kv_cache_read``.
+``attn_bwd``, ``attn_paged``, ``attn_paged_prefix``, ``kv_cache_append``,
+``kv_cache_write`` and ``kv_cache_read``.
 
 Shapes: q, k, alpha, b [B, T, H, dk]; v, w [B, T, H, dv] (packed sequences:
 B = 1 and ``cu_seqlens`` int32 [N + 1] on the device); states [N, H, dk, dv]
@@ -112,6 +113,10 @@ def configure(L: ctypes.CDLL) -> ctypes.CDLL:
     L.gdn2_kv_cache_write.argtypes = [vp] * 3 + [i] * 7 + [vp] * 5
     L.gdn2_kv_cache_read.restype = i
     L.gdn2_kv_cache_read.argtypes = [vp] + [i] * 7 + [vp] * 7
+    L.gdn2_attn_paged_prefix_workspace_bytes.restype = sz
+    L.gdn2_attn_paged_prefix_workspace_bytes.argtypes = [i] * 10
+    L.gdn2_attn_paged_prefix.restype = i
+    L.gdn2_attn_paged_prefix.argtypes = [vp] * 11 + [i] * 11 + [f, i, i, vp, vp, vp, sz, vp]
     i64 = ctypes.c_int64
     L.gdn2_kv_cache_append.restype = i
     L.gdn2_kv_cache_append.argtypes = ([vp] * 3 + [i64] * 3 + [vp] * 5 + [i] * 6 + [f] + [i] * 4 + [u32, vp, i64] +
@@ -438,5 +443,6 @@ def profile_read(reset: bool = True) -> dict:
 
 
 from .attention import (attn_bwd, attn_bwd_workspace_bytes, attn_fwd, attn_paged,  # noqa: E402,F401
-                        attn_paged_workspace_bytes, kv_cache_append, kv_cache_read, kv_cache_write, qk_norm_rope,
-                        qk_norm_rope_bwd, rope_frequencies)
+                        attn_paged_prefix, attn_paged_prefix_workspace_bytes, attn_paged_workspace_bytes,
+                        kv_cache_append, kv_cache_read, kv_cache_write, qk_norm_rope, qk_norm_rope_bwd,
+                        rope_frequencies)

@@ -12,6 +12,11 @@ recurrence's entry points: argument marshalling for the operators
     kv_cache_write(k, v, slots, k_cache, v_cache, k_scale, v_scale)   # serving
     o, lse = attn_paged(q, k_cache, v_cache, block_table, seq_lens, ...)
     k, v = kv_cache_read(slots, k_cache, v_cache, k_scale, v_scale)
+    q = kv_cache_append(q, k, v, slots, k_cache, v_cache, freqs, wq, wk, positions)   # both steps in one pass
+    o, lse = attn_paged_prefix(q, k_cache, v_cache, prefix_table, prefix_lens, block_table, seq_lens, ...)
+
+Layers whose window keeps first tokens visible: ``sinks`` of ``attn_fwd``,
+``attn_bwd`` and ``attn_paged``.
 
 Shapes: q, o [B, T, Hq, d]; k, v [B, T, Hk, d], d 64 or 128, Hq a multiple of
 Hk; packed sequences have B = 1 and ``cu_seqlens`` int32 [N + 1].  Tensors are
@@ -457,4 +462,61 @@ def attn_paged(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens=None, k_sc
     _call(dev, lib().gdn2_attn_sink_paged, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
           _ptr(block_table), _ptr(seq_lens), _ptr(cu_seqlens), B, T, Hq, Hk, d, ns, P, page, mp, window,
           sinks, d ** -0.5 if scale is None else scale, dt, code, _ptr(out), _ptr(lse), _ptr(ws), ws_bytes)
+    return out, lse
+
+
+def attn_paged_prefix_workspace_bytes(q, k_cache, prefix_table, block_table, cu_seqlens=None) -> int:
+    """Bytes of workspace ``attn_paged_prefix`` needs for these tensors."""
+    B, T, Hq, d = q.shape
+    ns = 0 if cu_seqlens is None else cu_seqlens.numel() - 1
+    return int(lib().gdn2_attn_paged_prefix_workspace_bytes(B, T, Hq, k_cache.shape[1], d, ns, prefix_table.shape[0],
+                                                            k_cache.shape[2], prefix_table.shape[1],
+                                                            block_table.shape[1]))
+
+
+def attn_paged_prefix(q, k_cache, v_cache, prefix_table, prefix_lens, block_table, seq_lens, cu_groups=None,
+                      cu_seqlens=None, k_scale=None, v_scale=None, scale: float | None = None, out=None, lse=None,
+                      want_lse: bool = False, workspace=None):
+    """``attn_paged`` (without a window) for sequences that share a prefix,
+    whose keys are read once for all of them.  Group m is the sequences
+    ``cu_groups[m]`` .. ``cu_groups[m + 1] - 1`` (int32 [M + 1]; None: one group
+    of all) behind the prefix of ``prefix_lens[m]`` keys (int32 [M]) in the
+    pages ``prefix_table[m]`` (int32 [M, max pages]); ``block_table`` and
+    ``seq_lens`` hold what each sequence has of its own, its new tokens
+    included.  Returns (o, lse or None)."""
+    dev = _device(q, k_cache, v_cache, prefix_table, prefix_lens, block_table, seq_lens, cu_groups, cu_seqlens, k_scale,
+                  v_scale)
+    if q.dim() != 4:
+        raise ValueError("q must be [N, T, Hq, d]")
+    B, T, Hq, d = q.shape
+    dt = _dtype_code(q)
+    P, Hk, page, dc, code = _cache(k_cache, v_cache, k_scale, v_scale, q.dtype)
+    if dc != d:
+        raise ValueError(f"the cache's head width {dc} is not q's {d}")
+    ns = _packed(cu_seqlens, B)
+    N = ns if ns else B
+    if block_table.dim() != 2 or prefix_table.dim() != 2:
+        raise ValueError("block_table and prefix_table must be [N, max pages] and [M, max pages]")
+    M, mpp = prefix_table.shape
+    _like(block_table, "block_table", (N, block_table.shape[1]), torch.int32)
+    _like(seq_lens, "seq_lens", (N,), torch.int32)
+    _like(prefix_table, "prefix_table", (M, mpp), torch.int32)
+    _like(prefix_lens, "prefix_lens", (M,), torch.int32)
+    _like(cu_groups, "cu_groups", (M + 1,), torch.int32)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None and want_lse:
+        lse = torch.empty((B, T, Hq), dtype=torch.float32, device=dev)
+    _device(q, out, lse)
+    _like(out, "out", q.shape, q.dtype)
+    _like(lse, "lse", (B, T, Hq), torch.float32)
+    mp = block_table.shape[1]
+    need = 0
+    if workspace is None:
+        need = int(lib().gdn2_attn_paged_prefix_workspace_bytes(B, T, Hq, Hk, d, ns, M, page, mpp, mp))
+    ws, ws_bytes = _workspace(workspace, need, dev)
+    _call(dev, lib().gdn2_attn_paged_prefix, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+          _ptr(prefix_table), _ptr(prefix_lens), _ptr(cu_groups), _ptr(block_table), _ptr(seq_lens), _ptr(cu_seqlens), B,
+          T, Hq, Hk, d, ns, M, P, page, mpp, mp, d ** -0.5 if scale is None else scale, dt, code, _ptr(out), _ptr(lse),
+          _ptr(ws), ws_bytes)
     return out, lse

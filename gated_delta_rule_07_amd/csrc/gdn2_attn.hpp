@@ -289,12 +289,13 @@ struct span {
 // the next sequence's first slot, so no table is needed.  One wave finds the
 // last n whose first slot is <= s, 64 candidates a step.  Every wave of the
 // workgroup calls this with the same arguments.
-__device__ __forceinline__ int find_seq(const int32_t *cu, int N, int G, int BM, long s, int lane) {
+// first(i): cu[i].
+template <typename F> __device__ __forceinline__ int find_seq_by(F first, int N, int G, int BM, long s, int lane) {
   int lo = 0, cnt = N;  // the answer lies in [lo, lo + cnt)
   while (cnt > 1) {
     const int step = (cnt + 63) / 64;
     const int i = lo + lane * step;
-    const bool le = i < lo + cnt && static_cast<long>(cu[i]) * G / BM + i <= s;
+    const bool le = i < lo + cnt && static_cast<long>(first(i)) * G / BM + i <= s;
     const unsigned long long m = __ballot(le);
     const int last = m ? 63 - __builtin_clzll(m) : 0;
     const int end = lo + cnt;
@@ -304,17 +305,23 @@ __device__ __forceinline__ int find_seq(const int32_t *cu, int N, int G, int BM,
   return lo;
 }
 
-// Sequence n's tokens in the tensors of T tokens a call may touch, whatever
-// cu holds.
-__device__ __forceinline__ span packed_span(const int32_t *cu, int n, int T) {
+__device__ __forceinline__ int find_seq(const int32_t *cu, int N, int G, int BM, long s, int lane) {
+  return find_seq_by([cu](int i) { return cu[i]; }, N, G, BM, s, lane);
+}
+
+// Sequence n's tokens (a to b - 1) in the tensors of T tokens a call may touch,
+// whatever cu holds.
+__device__ __forceinline__ span clamped_span(int n, int a, int b, int T) {
   span x;
   x.n = n;
-  int a = cu[n], b = cu[n + 1];
   a = a < 0 ? 0 : (a > T ? T : a);
   b = b > T ? T : b;
   x.start = a;
   x.len = b > a ? b - a : 0;
   return x;
+}
+__device__ __forceinline__ span packed_span(const int32_t *cu, int n, int T) {
+  return clamped_span(n, cu[n], cu[n + 1], T);
 }
 
 // Workgroup order.  Consecutive workgroups go to the 8 dies in turn, each

@@ -16,6 +16,7 @@ using namespace gdn2::host;
 using gdn2::attn::attn_ptrs;
 using gdn2::attn::attn_sizes;
 using gdn2::attn::cache_call;
+using gdn2::attn::prefix_call;
 using gdn2::attn::rope_call;
 
 namespace {
@@ -268,6 +269,32 @@ gdn2_status_t check_paged(const char *fn, int B, int T, int Hq, int Hk, int d, i
   return check_window(fn, window, sinks, z.max_keys + T, z);
 }
 
+// Sizes of a shared-prefix call, without its pointers; x gets its parts.
+gdn2_status_t check_prefix(const char *fn, int B, int T, int Hq, int Hk, int d, int num_seqs, int num_groups,
+                           int page_size, int max_prefix_pages, int max_pages, float scale, gdn2_dtype_t dt,
+                           attn_sizes &z, prefix_call &x) {
+  gdn2_status_t st = check_paged(fn, B, T, Hq, Hk, d, num_seqs, page_size, max_pages, 0, 0, scale, dt, z);
+  if (st != GDN2_OK)
+    return st;
+  if (num_groups <= 0)
+    return fail(GDN2_ERR_INVALID_ARGUMENT, "%s: bad number of groups %d", fn, num_groups);
+  if (max_prefix_pages < 0 || static_cast<long long>(max_prefix_pages) * page_size > (1LL << 28))
+    return fail(GDN2_ERR_UNSUPPORTED, "%s: at most 2^28 keys a prefix (max_prefix_pages=%d)", fn, max_prefix_pages);
+  if (static_cast<long long>(num_groups) * Hk > MAX_UNITS)
+    return fail(GDN2_ERR_UNSUPPORTED, "%s: too large (at most 2^20 - 1 group-heads)", fn);
+  x = {};
+  x.ngroups = num_groups;
+  x.max_pages = max_prefix_pages;
+  if (T > 0) {
+    x.prefix_parts = gdn2::attn::attn_prefix_splits(z, x);
+    x.own_parts = gdn2::attn::attn_paged_splits(z);
+  }
+  return GDN2_OK;
+}
+size_t prefix_bytes(const attn_sizes &z, const prefix_call &x, int d) {
+  return static_cast<size_t>(x.prefix_parts + x.own_parts) * z.Ttot * z.Hq * (d + 1) * sizeof(float);
+}
+
 size_t paged_bytes(const attn_sizes &z, int d) {
   const int s = gdn2::attn::attn_paged_splits(z);
   return s <= 1 ? 0 : static_cast<size_t>(s) * z.Ttot * z.Hq * (d + 1) * sizeof(float);
@@ -391,7 +418,7 @@ gdn2_status_t attn_paged(const char *fn, const void *q, const void *k_cache, con
   }
   if (e == hipSuccess && splits > 1) {
     prof_scope ps("attn_paged_join", s);
-    GDN2_ATTN_DISPATCH(e, dt, d, launch_attn_join, z, p, splits, workspace, s);
+    GDN2_ATTN_DISPATCH(e, dt, d, launch_attn_join, z, p, splits, nullptr, workspace, s);
   }
   return launched(fn, e);
 }
@@ -555,6 +582,84 @@ gdn2_status_t gdn2_attn_sink_paged(const void *q, const void *k_cache, const voi
   return attn_paged("gdn2_attn_sink_paged", q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens, B,
                     T, Hq, Hk, d, num_seqs, num_pages, page_size, max_pages, window, sinks, scale, dt, cache_dt, o, lse,
                     workspace, workspace_bytes, stream);
+}
+
+size_t gdn2_attn_paged_prefix_workspace_bytes(int B, int T, int Hq, int Hk, int d, int num_seqs, int num_groups,
+                                              int page_size, int max_prefix_pages, int max_pages) {
+  attn_sizes z;
+  prefix_call x;
+  if (check_prefix("gdn2_attn_paged_prefix_workspace_bytes", B, T, Hq, Hk, d, num_seqs, num_groups, page_size,
+                   max_prefix_pages, max_pages, 1.f, GDN2_F32, z, x) != GDN2_OK) {
+    (void)ok();
+    return 0;
+  }
+  return prefix_bytes(z, x, d);
+}
+
+gdn2_status_t gdn2_attn_paged_prefix(const void *q, const void *k_cache, const void *v_cache, const uint8_t *k_scale,
+                                     const uint8_t *v_scale, const int32_t *prefix_table, const int32_t *prefix_lens,
+                                     const int32_t *cu_groups, const int32_t *block_table, const int32_t *seq_lens,
+                                     const int32_t *cu_seqlens, int B, int T, int Hq, int Hk, int d, int num_seqs,
+                                     int num_groups, int num_pages, int page_size, int max_prefix_pages, int max_pages,
+                                     float scale, gdn2_dtype_t dt, gdn2_dtype_t cache_dt, void *o, float *lse,
+                                     void *workspace, size_t workspace_bytes, void *stream) {
+  const char *fn = "gdn2_attn_paged_prefix";
+  attn_sizes z;
+  prefix_call x;
+  if ((cu_seqlens != nullptr) != (num_seqs > 0))
+    return fail(GDN2_ERR_INVALID_ARGUMENT, "%s: cu_seqlens goes with num_seqs > 0", fn);
+  gdn2_status_t st = check_prefix(fn, B, T, Hq, Hk, d, num_seqs, num_groups, page_size, max_prefix_pages, max_pages,
+                                  scale, dt, z, x);
+  if (st != GDN2_OK)
+    return st;
+  if (!cu_groups && num_groups != 1)
+    return fail(GDN2_ERR_INVALID_ARGUMENT, "%s: %d groups without cu_groups", fn, num_groups);
+  st = check_cache(fn, num_pages, page_size, dt, cache_dt, k_scale, v_scale);
+  if (st != GDN2_OK)
+    return st;
+  if (T == 0)
+    return ok();
+  // (a table of no pages has no entries: nothing reads it)
+  st = check_ptrs(fn, {q, k_cache, v_cache, max_pages ? block_table : seq_lens, max_prefix_pages ? prefix_table : seq_lens,
+                       prefix_lens, seq_lens, o},
+                  {cu_groups, cu_seqlens, lse, workspace, block_table, prefix_table});
+  if (st != GDN2_OK)
+    return st;
+  const size_t need = prefix_bytes(z, x, d);
+  if (!workspace || workspace_bytes < need)
+    return fail(GDN2_ERR_WORKSPACE_TOO_SMALL, "%s: workspace holds %zu bytes, %zu are needed", fn, workspace_bytes,
+                need);
+  z.num_pages = num_pages;
+  x.table = prefix_table;
+  x.lens = prefix_lens;
+  x.groups = cu_groups;
+  attn_ptrs p = {};
+  p.q = q;
+  p.k = k_cache;
+  p.v = v_cache;
+  p.ks = k_scale;
+  p.vs = v_scale;
+  p.table = block_table;
+  p.seq_lens = seq_lens;
+  p.cu = cu_seqlens;
+  p.o = o;
+  p.lse = lse;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const bool f8 = cache_dt == GDN2_F8E4M3;
+  hipError_t e;
+  {
+    prof_scope ps("attn_prefix", s);
+    GDN2_CACHE_DISPATCH(e, dt, f8, d, launch_attn_prefix, z, p, x, workspace, s);
+  }
+  if (e == hipSuccess) {
+    prof_scope ps("attn_prefix_own", s);
+    GDN2_CACHE_DISPATCH(e, dt, f8, d, launch_attn_own, z, p, x, workspace, s);
+  }
+  if (e == hipSuccess) {
+    prof_scope ps("attn_prefix_join", s);
+    GDN2_ATTN_DISPATCH(e, dt, d, launch_attn_join, z, p, x.prefix_parts + x.own_parts, &x, workspace, s);
+  }
+  return launched(fn, e);
 }
 
 gdn2_status_t gdn2_kv_cache_write(const void *k, const void *v, const int64_t *slots, int n, int Hk, int d,

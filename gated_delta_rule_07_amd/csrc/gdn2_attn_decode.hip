@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(256, 3) gdn2_attn_decode_kernel(fwd_args a) {
     store_row<IO, D>(a, x, L, qrow, split, row_ok, 16 * n + 4 * g);
   }
   if (wn == 0 && g == 0 && row_ok)
-    store_lse(a, M, L, qrow, split);
+    store_lse(a, M, L, qrow, split, pos);
 }
 
 template <typename CT, int D> hipError_t launch_attn_decode(const fwd_args &a, hipStream_t st) {

@@ -37,13 +37,18 @@
 namespace gdn2 {
 namespace attn {
 
-// SINK: the first `sinks` keys of the sequence stay visible behind the window.
+// FWD_SINK: the first `sinks` keys of the sequence stay visible behind the window.
 // The workgroup numbers the keys it visits without the gap between the two:
 // the sinks, then the keys from its first row's window on, so that few sinks
 // cost no tile of their own; positions are numbered with them.
-template <typename IO, typename CT, int D, int WM, int WN, int KT, bool PAGED, bool SINK>
+//
+// FWD_PREFIX: the rows are a group's, all of whose sequences share the keys of one
+// table; every row sees every key.
+enum fwd_mode { FWD_PLAIN, FWD_SINK, FWD_PREFIX };
+template <typename IO, typename CT, int D, int WM, int WN, int KT, bool PAGED, fwd_mode MODE>
 __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
     gdn2_attn_fwd_kernel(fwd_args a) {
+  constexpr bool SINK = MODE == FWD_SINK, PREFIX = MODE == FWD_PREFIX;
   typedef tile<IO, D> TL;
   typedef typename std::conditional<sizeof(CT) == 1, tile8<IO, D>, TL>::type KV;  // a tile of the cache's own type
   // SHARED: the workgroup's waves share a tile, double-buffered, with one
@@ -80,7 +85,13 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
     return;
   span sq;
   int hk, row0;
-  if (a.cu) {
+  if constexpr (PREFIX) {
+    hk = unit;
+    auto first = [&](int i) { return group_start(a, i); };
+    const int n = find_seq_by(first, a.N, a.G, BM, slot, lane);
+    sq = clamped_span(n, first(n), first(n + 1), a.T);
+    row0 = static_cast<int>((slot - (static_cast<long>(first(n)) * a.G / BM + n)) * BM);
+  } else if (a.cu) {
     hk = unit;
     const int n = find_seq(a.cu, a.N, a.G, BM, slot, lane);
     sq = packed_span(a.cu, n, a.T);
@@ -107,7 +118,7 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
   const int t_lo = row0 / a.G;
   const int last_row = row0 + BM - 1 < rows - 1 ? row0 + BM - 1 : rows - 1;
   const int t_hi = last_row / a.G;
-  int k_hi = shift + t_hi + 1;
+  int k_hi = PREFIX ? kv_len : shift + t_hi + 1;
   k_hi = k_hi < 0 ? 0 : k_hi;
   int k_lo = 0;
   if (a.window > 0) {
@@ -135,12 +146,12 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
   const bool row_ok = my_row < rows;
   const int cl_row = row_ok ? my_row : rows - 1;
   const int tok = cl_row / a.G, head = hk * a.G + cl_row % a.G;
-  const int pos = shift - gap + tok;
+  const int pos = PREFIX ? kv_len - 1 : shift - gap + tok;
   const size_t qrow = static_cast<size_t>(sq.start + tok) * a.Hq + head;
   // positions of the wave's first and last row
   const int wr0 = row0 + 32 * wm < rows ? row0 + 32 * wm : rows - 1;
   const int wr1 = row0 + 32 * wm + 31 < rows ? row0 + 32 * wm + 31 : rows - 1;
-  const int pos_lo = shift - gap + wr0 / a.G, pos_hi = shift - gap + wr1 / a.G;
+  const int pos_lo = PREFIX ? pos : shift - gap + wr0 / a.G, pos_hi = PREFIX ? pos : shift - gap + wr1 / a.G;
 
   frag8<IO> q[SHARED ? D / 16 : 1];
   const IO *const qp = static_cast<const IO *>(a.q) + qrow * D;
@@ -513,7 +524,7 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
       }
     }
     if (wn == 0 && h == 0 && row_ok)
-      store_lse(a, M, L, qrow, split);
+      store_lse(a, M, L, qrow, split, pos);
   } else {
 #pragma unroll
     for (int n = 0; n < D / 32; ++n)
@@ -526,14 +537,17 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
         store_row<IO, D>(a, x, l, qrow, split, row_ok, 32 * n + 8 * g + 4 * h);
       }
     if (h == 0 && row_ok)
-      store_lse(a, m, l, qrow, split);
+      store_lse(a, m, l, qrow, split, pos);
   }
 }
 
 // Joins the parts of split keys: W waves per (token, query head), wave w of a
 // row takes the parts w, w + W, ..; weights 2^(lse_s - max lse); the order of
 // the sums is fixed.
-template <typename IO, int D, int W> __global__ void __launch_bounds__(256) gdn2_attn_join_kernel(fwd_args a) {
+// With PREFIX, the first prefix_parts parts hold for the groups' rows alone, and
+// a row that the others mark sees nothing.
+template <typename IO, int D, int W, bool PREFIX>
+__global__ void __launch_bounds__(256) gdn2_attn_join_kernel(fwd_args a) {
   __shared__ float red[W][D + 1];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, w0 = W == 1 ? 0 : wave;
   const size_t rows = static_cast<size_t>(a.Ttot) * a.Hq;
@@ -542,20 +556,38 @@ template <typename IO, int D, int W> __global__ void __launch_bounds__(256) gdn2
     return;
   if (a.cu && row >= static_cast<size_t>(a.cu[a.N] < 0 ? 0 : a.cu[a.N]) * a.Hq)
     return;  // behind the last sequence
+  int s0 = 0;
+  if constexpr (PREFIX) {
+    // (a wave has one row; with a branch for the second comparison the compiler
+    // lost the other value of s0)
+    const int tok = __builtin_amdgcn_readfirstlane(static_cast<int>(row / a.Hq));
+    const int first = group_start(a, 0), end = group_start(a, a.ngroups);
+    s0 = (tok >= first) & (tok < end) ? 0 : a.prefix_parts;
+  }
   float M = neg_inf();
-  for (int s = lane; s < a.splits; s += 64)
+  for (int s = s0 + lane; s < a.splits; s += 64)
     M = fmaxf(M, a.part_lse[s * rows + row]);
 #pragma unroll
   for (int x = 1; x < 64; x <<= 1)
     M = fmaxf(M, __shfl_xor(M, x, 64));
-  const float base = M == neg_inf() ? 0.f : M;
   constexpr int V = D / 64;
+  if (PREFIX && M == __builtin_inff()) {
+    if (w0 == 0) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        static_cast<IO *>(a.o)[row * D + V * lane + i] = io<IO>::from_f(0.f);
+      if (a.lse && lane == 0)
+        a.lse[row] = neg_inf();
+    }
+    return;
+  }
+  const float base = M == neg_inf() ? 0.f : M;
   float acc[V], L = 0.f;
 #pragma unroll
   for (int i = 0; i < V; ++i)
     acc[i] = 0.f;
 #pragma unroll 4
-  for (int s = w0; s < a.splits; s += W) {
+  for (int s = s0 + w0; s < a.splits; s += W) {
     // (a part without keys: weight 0 and zeros; NaN stays NaN)
     const float w = fast_exp2(a.part_lse[s * rows + row] - base);
     const float *p = a.part_o + (s * rows + row) * D + V * lane;
@@ -629,17 +661,17 @@ int attn_paged_splits(const attn_sizes &z) {
   return s < 1 ? 1 : (s > 128 ? 128 : static_cast<int>(s));
 }
 
-template <typename IO, typename CT, int D, int WM, int WN, int KT, bool PAGED, bool SINK>
+template <typename IO, typename CT, int D, int WM, int WN, int KT, bool PAGED, fwd_mode MODE>
 static hipError_t launch(fwd_args &a, const attn_sizes &z, hipStream_t st) {
   const unsigned blocks = plan_tiles(z, a.G, 32 * WM, a.od) * a.splits;
-  hipLaunchKernelGGL((gdn2_attn_fwd_kernel<IO, CT, D, WM, WN, KT, PAGED, SINK>), dim3(blocks), dim3(64 * WM * WN), 0, st,
+  hipLaunchKernelGGL((gdn2_attn_fwd_kernel<IO, CT, D, WM, WN, KT, PAGED, MODE>), dim3(blocks), dim3(64 * WM * WN), 0, st,
                      a);
   return hipGetLastError();
 }
 template <typename IO, typename CT, int D, int WM, int WN, int KT, bool PAGED>
 static hipError_t go(fwd_args &a, const attn_sizes &z, hipStream_t st) {
-  return a.sinks ? launch<IO, CT, D, WM, WN, KT, PAGED, true>(a, z, st)
-                 : launch<IO, CT, D, WM, WN, KT, PAGED, false>(a, z, st);
+  return a.sinks ? launch<IO, CT, D, WM, WN, KT, PAGED, FWD_SINK>(a, z, st)
+                 : launch<IO, CT, D, WM, WN, KT, PAGED, FWD_PLAIN>(a, z, st);
 }
 
 static void fill(fwd_args &a, const attn_sizes &z, const attn_ptrs &p) {
@@ -667,6 +699,17 @@ static void fill(fwd_args &a, const attn_sizes &z, const attn_ptrs &p) {
   a.sinks = z.sinks;
   a.splits = 1;
   a.c = z.scale * LOG2E;
+  a.groups = nullptr;
+  a.ngroups = a.seqs = a.tq = a.prefix_parts = 0;
+  a.mark = false;
+}
+
+// Where part s of a call's parts lies in ws: [parts, Ttot, Hq, D] outputs, then
+// [parts, Ttot, Hq] sums.
+static void parts_at(fwd_args &a, const attn_sizes &z, int D, void *ws, int parts, int s) {
+  const size_t rows = static_cast<size_t>(z.Ttot) * z.Hq;
+  a.part_o = static_cast<float *>(ws) + s * rows * D;
+  a.part_lse = static_cast<float *>(ws) + parts * rows * D + s * rows;
 }
 
 template <typename IO, int D> hipError_t launch_attn_fwd(const attn_sizes &z, const attn_ptrs &p, hipStream_t st) {
@@ -679,17 +722,8 @@ template <typename IO, int D> hipError_t launch_attn_fwd(const attn_sizes &z, co
   return few_tiles(a.od) ? go<IO, IO, D, 1, 4, 1, false>(a, z, st) : go<IO, IO, D, 4, 1, KT, false>(a, z, st);
 }
 
-template <typename IO, typename CT, int D>
-hipError_t launch_attn_paged(const attn_sizes &z, const attn_ptrs &p, int splits, void *ws, hipStream_t st) {
-  fwd_args a;
-  fill(a, z, p);
-  a.splits = splits;
+template <typename IO, typename CT, int D> static hipError_t paged(fwd_args &a, const attn_sizes &z, hipStream_t st) {
   constexpr int KT = sizeof(CT) <= 2 ? 2 : 1;
-  if (splits > 1) {
-    const size_t rows = static_cast<size_t>(z.Ttot) * z.Hq;
-    a.part_o = static_cast<float *>(ws);
-    a.part_lse = a.part_o + rows * D * splits;
-  }
   if constexpr (sizeof(IO) == 2) {
     if (decode_rows(z)) {
       plan_tiles(z, a.G, 16, a.od);
@@ -702,29 +736,99 @@ hipError_t launch_attn_paged(const attn_sizes &z, const attn_ptrs &p, int splits
   return few_rows(z) ? go<IO, CT, D, 1, WN, 1, true>(a, z, st) : go<IO, CT, D, 4, 1, KT, true>(a, z, st);
 }
 
-template <typename IO, int D>
-hipError_t launch_attn_join(const attn_sizes &z, const attn_ptrs &p, int splits, void *ws, hipStream_t st) {
+template <typename IO, typename CT, int D>
+hipError_t launch_attn_paged(const attn_sizes &z, const attn_ptrs &p, int splits, void *ws, hipStream_t st) {
   fwd_args a;
   fill(a, z, p);
   a.splits = splits;
+  if (splits > 1)
+    parts_at(a, z, D, ws, splits, 0);
+  return paged<IO, CT, D>(a, z, st);
+}
+
+static void fill_groups(fwd_args &a, const attn_sizes &z, const prefix_call &x) {
+  a.groups = x.groups;
+  a.ngroups = x.ngroups;
+  a.seqs = z.N;
+  a.tq = z.packed ? 0 : z.T;
+  a.prefix_parts = x.prefix_parts;
+}
+
+// The launch over the prefixes sees the groups as packed sequences of rows.
+static attn_sizes prefix_sizes(const attn_sizes &z, const prefix_call &x) {
+  attn_sizes y = z;
+  y.N = x.ngroups;
+  y.T = z.Ttot;
+  y.packed = true;
+  y.max_pages = x.max_pages;
+  y.max_keys = static_cast<long long>(x.max_pages) << z.page_shift;
+  return y;
+}
+
+int attn_prefix_splits(const attn_sizes &z, const prefix_call &x) { return attn_paged_splits(prefix_sizes(z, x)); }
+
+template <typename IO, typename CT, int D>
+hipError_t launch_attn_prefix(const attn_sizes &z, const attn_ptrs &p, const prefix_call &x, void *ws, hipStream_t st) {
+  const attn_sizes y = prefix_sizes(z, x);
+  fwd_args a;
+  fill(a, y, p);
+  fill_groups(a, z, x);
+  a.table = x.table;
+  a.seq_lens = x.lens;
+  a.splits = x.prefix_parts;
+  parts_at(a, z, D, ws, x.prefix_parts + x.own_parts, 0);
+  constexpr int KT = sizeof(CT) <= 2 ? 2 : 1, WN = D * sizeof(IO) <= 256 ? 4 : 2;
+  return few_rows(y) ? launch<IO, CT, D, 1, WN, 1, true, FWD_PREFIX>(a, y, st)
+                     : launch<IO, CT, D, 4, 1, KT, true, FWD_PREFIX>(a, y, st);
+}
+
+template <typename IO, typename CT, int D>
+hipError_t launch_attn_own(const attn_sizes &z, const attn_ptrs &p, const prefix_call &x, void *ws, hipStream_t st) {
+  fwd_args a;
+  fill(a, z, p);
+  a.splits = x.own_parts;
+  a.mark = true;
+  parts_at(a, z, D, ws, x.prefix_parts + x.own_parts, x.prefix_parts);
+  return paged<IO, CT, D>(a, z, st);
+}
+
+template <typename IO, int D>
+hipError_t launch_attn_join(const attn_sizes &z, const attn_ptrs &p, int splits, const prefix_call *x, void *ws,
+                            hipStream_t st) {
+  fwd_args a;
+  fill(a, z, p);
+  if (x)
+    fill_groups(a, z, *x);
+  a.splits = splits;
+  parts_at(a, z, D, ws, splits, 0);
   const size_t rows = static_cast<size_t>(z.Ttot) * z.Hq;
-  a.part_o = static_cast<float *>(ws);
-  a.part_lse = a.part_o + rows * D * splits;
   // one wave a row where there are rows enough, or few parts
-  if (rows >= 8192 || splits <= 4)
-    hipLaunchKernelGGL((gdn2_attn_join_kernel<IO, D, 1>), dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(256), 0, st, a);
+  const bool one = rows >= 8192 || splits <= 4;
+  const dim3 grid(static_cast<unsigned>(one ? (rows + 3) / 4 : rows));
+  if (one && x)
+    hipLaunchKernelGGL((gdn2_attn_join_kernel<IO, D, 1, true>), grid, dim3(256), 0, st, a);
+  else if (one)
+    hipLaunchKernelGGL((gdn2_attn_join_kernel<IO, D, 1, false>), grid, dim3(256), 0, st, a);
+  else if (x)
+    hipLaunchKernelGGL((gdn2_attn_join_kernel<IO, D, 4, true>), grid, dim3(256), 0, st, a);
   else
-    hipLaunchKernelGGL((gdn2_attn_join_kernel<IO, D, 4>), dim3(static_cast<unsigned>(rows)), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((gdn2_attn_join_kernel<IO, D, 4, false>), grid, dim3(256), 0, st, a);
   return hipGetLastError();
 }
 
-#define GDN2_INST_ATTN(IO, D)                                                                              \
-  template hipError_t launch_attn_fwd<IO, D>(const attn_sizes &, const attn_ptrs &, hipStream_t);          \
-  template hipError_t launch_attn_paged<IO, IO, D>(const attn_sizes &, const attn_ptrs &, int, void *,     \
-                                                   hipStream_t);                                           \
-  template hipError_t launch_attn_paged<IO, f8_t, D>(const attn_sizes &, const attn_ptrs &, int, void *,   \
-                                                     hipStream_t);                                         \
-  template hipError_t launch_attn_join<IO, D>(const attn_sizes &, const attn_ptrs &, int, void *, hipStream_t);
+#define GDN2_INST_PAGED(IO, CT, D)                                                                          \
+  template hipError_t launch_attn_paged<IO, CT, D>(const attn_sizes &, const attn_ptrs &, int, void *,      \
+                                                   hipStream_t);                                            \
+  template hipError_t launch_attn_prefix<IO, CT, D>(const attn_sizes &, const attn_ptrs &,                  \
+                                                    const prefix_call &, void *, hipStream_t);              \
+  template hipError_t launch_attn_own<IO, CT, D>(const attn_sizes &, const attn_ptrs &, const prefix_call &, \
+                                                 void *, hipStream_t);
+#define GDN2_INST_ATTN(IO, D)                                                                               \
+  template hipError_t launch_attn_fwd<IO, D>(const attn_sizes &, const attn_ptrs &, hipStream_t);           \
+  template hipError_t launch_attn_join<IO, D>(const attn_sizes &, const attn_ptrs &, int, const prefix_call *, \
+                                              void *, hipStream_t);                                         \
+  GDN2_INST_PAGED(IO, IO, D)                                                                                \
+  GDN2_INST_PAGED(IO, f8_t, D)
 GDN2_INST_ATTN(float, 64)
 GDN2_INST_ATTN(float, 128)
 GDN2_INST_ATTN(bf16_t, 64)

@@ -15,14 +15,31 @@ struct fwd_args {
   const int32_t *table;      // paged: [N, max_pages]
   const int32_t *seq_lens;   // paged: keys of each sequence
   const uint8_t *ks, *vs;    // paged e4m3: [pages, Hk, page] exponent bytes
-  float *part_o, *part_lse;  // splits > 1: [splits, T total, Hq(, D)]
+  float *part_o, *part_lse;  // where a row leaves parts, not its output: [splits, T total, Hq(, D)]
   int N, T, Hq, Hk, G;
   int Ttot;                  // tokens of q in all
   int max_pages, num_pages, page_shift;
   int window, sinks, splits;  // sinks: 0 without a window
   float c;                   // scale log2 e
   order od;
+  // Shared prefixes.  The launch over the prefixes has the groups for its
+  // sequences: N, table and seq_lens are theirs, T all tokens, and group i is
+  // the sequences groups[i] .. groups[i + 1] - 1 (nullptr: one group of all)
+  // of tq tokens each, or packed by cu.  The launch over the sequences' own
+  // keys marks rows at negative positions, and the join takes the first
+  // prefix_parts parts for the groups' rows alone.
+  const int32_t *groups;
+  int ngroups, seqs, tq, prefix_parts;
+  bool mark;
 };
+
+// The first token of group i, whatever groups and cu hold.
+__device__ __forceinline__ int group_start(const fwd_args &a, int i) {
+  int n = a.groups ? a.groups[i] : (i > 0 ? a.seqs : 0);
+  n = n < 0 ? 0 : (n > a.seqs ? a.seqs : n);
+  const int t = a.cu ? a.cu[n] : n * a.tq;
+  return t < 0 ? 0 : (t > a.Ttot ? a.Ttot : t);
+}
 
 // Infinities and NaN of an operand set to zero; whether there were any.
 __device__ __forceinline__ bool drop_nonfinite(frag8<bf16_t> &x) {
@@ -64,16 +81,18 @@ __device__ __forceinline__ void store_row(const fwd_args &a, f32x4 x, float l, s
   x *= inv;
   if (!ok)
     return;
-  if (a.splits > 1)
+  if (a.part_o)
     io<float>::store4(a.part_o + (static_cast<size_t>(split) * a.Ttot * a.Hq + qrow) * D + ch, x);
   else
     io<IO>::store4(static_cast<IO *>(a.o) + qrow * D + ch, x);
 }
-// ln of the row's sum (with split keys: of the part's, in base 2)
-__device__ __forceinline__ void store_lse(const fwd_args &a, float m, float l, size_t qrow, int split) {
+// ln of the row's sum (of a part's: in base 2).  A row at a negative position
+// is marked, where asked for, by +inf, which no sum gives (a score of +inf
+// makes the sum NaN).
+__device__ __forceinline__ void store_lse(const fwd_args &a, float m, float l, size_t qrow, int split, int pos) {
   const float x = m + log2f(l);
-  if (a.splits > 1)
-    a.part_lse[static_cast<size_t>(split) * a.Ttot * a.Hq + qrow] = x;
+  if (a.part_o)
+    a.part_lse[static_cast<size_t>(split) * a.Ttot * a.Hq + qrow] = a.mark && pos < 0 ? __builtin_inff() : x;
   else if (a.lse)
     a.lse[qrow] = x * LN2;
 }

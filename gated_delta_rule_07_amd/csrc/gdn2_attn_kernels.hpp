@@ -45,8 +45,21 @@ template <typename IO, int D> hipError_t launch_attn_fwd(const attn_sizes &z, co
 int attn_paged_splits(const attn_sizes &z);
 template <typename IO, typename CT, int D>
 hipError_t launch_attn_paged(const attn_sizes &z, const attn_ptrs &p, int splits, void *ws, hipStream_t st);
+// A shared-prefix call's prefixes: the groups' tables, lengths and (nullptr: one
+// group) first sequences, and the parts of the prefixes' and of the own keys.
+struct prefix_call {
+  const int32_t *table, *lens, *groups;
+  int ngroups, max_pages, prefix_parts, own_parts;
+};
+int attn_prefix_splits(const attn_sizes &z, const prefix_call &x);
+// the prefixes' parts of all rows, and the own keys' behind them in ws
+template <typename IO, typename CT, int D>
+hipError_t launch_attn_prefix(const attn_sizes &z, const attn_ptrs &p, const prefix_call &x, void *ws, hipStream_t st);
+template <typename IO, typename CT, int D>
+hipError_t launch_attn_own(const attn_sizes &z, const attn_ptrs &p, const prefix_call &x, void *ws, hipStream_t st);
 template <typename IO, int D>
-hipError_t launch_attn_join(const attn_sizes &z, const attn_ptrs &p, int splits, void *ws, hipStream_t st);
+hipError_t launch_attn_join(const attn_sizes &z, const attn_ptrs &p, int splits, const prefix_call *x, void *ws,
+                            hipStream_t st);
 // Backward: dq, which leaves the rows' statistics in ws, then dk and dv, which
 // read them.  ws holds the statistics and, where attn_bwd_parts workgroups share a key tile's rows,
 // their sums.

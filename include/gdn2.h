@@ -405,6 +405,7 @@ gdn2_status_t gdn2_decode_step(const void *q, const void *k, const void *v, cons
  *   gdn2_attn_paged                new tokens over the paged cache (decode,
  *                                  chunks of a prompt), next to
  *                                  gdn2_decode_step
+ *   gdn2_attn_paged_prefix         the same for sequences that share a prefix
  *   gdn2_attn_sink_fwd / _bwd /    the same attention where a window's layer
  *   _paged                         keeps its first tokens visible
  * The conventions at the top hold: contiguous token-major device tensors of
@@ -565,6 +566,30 @@ gdn2_status_t gdn2_attn_paged(const void *q, const void *k_cache, const void *v_
                               int num_pages, int page_size, int max_pages, int window, float scale, gdn2_dtype_t dt,
                               gdn2_dtype_t cache_dt, void *o, float *lse, void *workspace, size_t workspace_bytes,
                               void *stream);
+
+/* Attention of new tokens over the paged cache where sequences share a prefix
+ * (a system prompt), whose keys are read once for all of them.  The sequences
+ * come in num_groups groups: group m is the sequences cu_groups[m] ..
+ * cu_groups[m+1] - 1 (int32 [num_groups + 1], not falling; NULL with one group:
+ * all of them) behind a prefix of prefix_lens[m] keys (int32; clamped to 0 ..
+ * max_prefix_pages * page_size), key j in row j % page_size of page
+ * prefix_table[m][j / page_size] (int32 [num_groups, max_prefix_pages]).
+ * block_table and seq_lens hold what each sequence has behind its prefix, its
+ * new tokens included, otherwise as for gdn2_attn_paged, as are q, o, lse,
+ * cu_seqlens, B, T and num_seqs.  A query at own position i (seq_lens[n] - L ..
+ * seq_lens[n] - 1) sees the whole prefix and the sequence's own keys j <= i;
+ * one at a negative own position sees nothing.  A sequence before the first
+ * or behind the last group has no prefix.  The workspace is always needed. */
+size_t gdn2_attn_paged_prefix_workspace_bytes(int B, int T, int Hq, int Hk, int d, int num_seqs, int num_groups,
+                                              int page_size, int max_prefix_pages, int max_pages);
+
+gdn2_status_t gdn2_attn_paged_prefix(const void *q, const void *k_cache, const void *v_cache, const uint8_t *k_scale,
+                                     const uint8_t *v_scale, const int32_t *prefix_table, const int32_t *prefix_lens,
+                                     const int32_t *cu_groups, const int32_t *block_table, const int32_t *seq_lens,
+                                     const int32_t *cu_seqlens, int B, int T, int Hq, int Hk, int d, int num_seqs,
+                                     int num_groups, int num_pages, int page_size, int max_prefix_pages, int max_pages,
+                                     float scale, gdn2_dtype_t dt, gdn2_dtype_t cache_dt, void *o, float *lse,
+                                     void *workspace, size_t workspace_bytes, void *stream);
 
 /* Attention with a sliding window and `sinks` first tokens of every sequence
  * that stay visible behind it: key j of the same sequence is visible to
