@@ -28,7 +28,8 @@ ARCH = os.environ.get("GDN2_OFFLOAD_ARCH", "gfx950")
 
 SOURCES = ["gdn2_api.cpp", "gdn2_recurrent.hip", "gdn2_chunk.hip", "gdn2_fused.hip", "gdn2_bwd.hip", "gdn2_segment.hip",
            "gdn2_rule_r1.hip", "gdn2_pad.hip", "gdn2_attn_api.cpp", "gdn2_qkrope.hip", "gdn2_attn_fwd.hip",
-           "gdn2_attn_decode.hip", "gdn2_attn_bwd.hip", "gdn2_kvcache.hip", "gdn2_kvappend.hip"]
+           "gdn2_attn_decode.hip", "gdn2_attn_bwd.hip", "gdn2_kvcache.hip", "gdn2_kvappend.hip",
+           "gdn2_attn_prefix.hip"]
 COMMON = ["-O3", "-fPIC", "-std=c++17", f"--offload-arch={ARCH}",
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
           "-Wall", "-Wno-unused-command-line-argument"]
@@ -41,6 +42,7 @@ COMMON = ["-O3", "-fPIC", "-std=c++17", f"--offload-arch={ARCH}",
 EXTRA = {"gdn2_segment.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
          "gdn2_attn_fwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
          "gdn2_attn_decode.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+         "gdn2_attn_prefix.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
          "gdn2_attn_bwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 # Host-only undefined-behaviour traps for the checked build of the C-ABI files
 # (each flag after -Xarch_host: device code is compiled as in the product).

@@ -218,16 +218,18 @@ __device__ __forceinline__ void dma_wait() { asm volatile("s_waitcnt vmcnt(0)" :
 // applied to the scores and weights, in float32), which both formats hold
 // exactly.
 template <typename T> __device__ __forceinline__ frag8<T> widen8(u32x2 x);
-template <> __device__ __forceinline__ frag8<bf16_t> widen8<bf16_t>(u32x2 x) {
+// (times a power of two)
+__device__ __forceinline__ frag8<bf16_t> widen8_by(u32x2 x, float scale) {
   u32x4 y;
-  y[0] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[0], 1.0f, false));
-  y[1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[0], 1.0f, true));
-  y[2] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[1], 1.0f, false));
-  y[3] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[1], 1.0f, true));
+  y[0] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[0], scale, false));
+  y[1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[0], scale, true));
+  y[2] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[1], scale, false));
+  y[3] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[1], scale, true));
   frag8<bf16_t> f;
   f.v = __builtin_bit_cast(bf16x8, y);
   return f;
 }
+template <> __device__ __forceinline__ frag8<bf16_t> widen8<bf16_t>(u32x2 x) { return widen8_by(x, 1.0f); }
 template <> __device__ __forceinline__ frag8<float> widen8<float>(u32x2 x) {
   const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(x[0], false), b = __builtin_amdgcn_cvt_pk_f32_fp8(x[0], true);
   const f32x2 c = __builtin_amdgcn_cvt_pk_f32_fp8(x[1], false), d = __builtin_amdgcn_cvt_pk_f32_fp8(x[1], true);

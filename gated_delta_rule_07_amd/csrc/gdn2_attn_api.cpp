@@ -285,10 +285,8 @@ gdn2_status_t check_prefix(const char *fn, int B, int T, int Hq, int Hk, int d, 
   x = {};
   x.ngroups = num_groups;
   x.max_pages = max_prefix_pages;
-  if (T > 0) {
-    x.prefix_parts = gdn2::attn::attn_prefix_splits(z, x);
-    x.own_parts = gdn2::attn::attn_paged_splits(z);
-  }
+  if (T > 0)
+    gdn2::attn::attn_prefix_splits(z, x);
   return GDN2_OK;
 }
 size_t prefix_bytes(const attn_sizes &z, const prefix_call &x, int d) {
@@ -650,10 +648,6 @@ gdn2_status_t gdn2_attn_paged_prefix(const void *q, const void *k_cache, const v
   {
     prof_scope ps("attn_prefix", s);
     GDN2_CACHE_DISPATCH(e, dt, f8, d, launch_attn_prefix, z, p, x, workspace, s);
-  }
-  if (e == hipSuccess) {
-    prof_scope ps("attn_prefix_own", s);
-    GDN2_CACHE_DISPATCH(e, dt, f8, d, launch_attn_own, z, p, x, workspace, s);
   }
   if (e == hipSuccess) {
     prof_scope ps("attn_prefix_join", s);

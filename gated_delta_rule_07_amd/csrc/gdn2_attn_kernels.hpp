@@ -51,12 +51,10 @@ struct prefix_call {
   const int32_t *table, *lens, *groups;
   int ngroups, max_pages, prefix_parts, own_parts;
 };
-int attn_prefix_splits(const attn_sizes &z, const prefix_call &x);
-// the prefixes' parts of all rows, and the own keys' behind them in ws
+void attn_prefix_splits(const attn_sizes &z, prefix_call &x);  // sets the numbers of parts
+// all rows' parts to ws: the prefixes', and the own keys' behind them
 template <typename IO, typename CT, int D>
 hipError_t launch_attn_prefix(const attn_sizes &z, const attn_ptrs &p, const prefix_call &x, void *ws, hipStream_t st);
-template <typename IO, typename CT, int D>
-hipError_t launch_attn_own(const attn_sizes &z, const attn_ptrs &p, const prefix_call &x, void *ws, hipStream_t st);
 template <typename IO, int D>
 hipError_t launch_attn_join(const attn_sizes &z, const attn_ptrs &p, int splits, const prefix_call *x, void *ws,
                             hipStream_t st);
