@@ -335,8 +335,6 @@ def _tokens(t, name: str, shape, dtype, dev: int) -> int:
         raise ValueError(f"{name} must have shape {list(shape)}, not {list(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError("libgdn2 takes device tensors")
     if t.get_device() != dev:
         raise ValueError(f"{name} is on another device ({t.device})")
     B, T, H, d = shape
@@ -367,8 +365,8 @@ def kv_cache_append(q, k, v, slots, k_cache, v_cache, freqs, wq=None, wk=None, p
     Hk, dt = k.shape[2], q.dtype
     if out is None:
         out = torch.empty(q.shape, dtype=dt, device=q.device)
-    strides = [_tokens(t, n, (B, T, h, d), dt, dev) for t, n, h in ((q, "q", Hq), (k, "k", Hk), (v, "v", Hk),
-                                                                     (out, "out", Hq))]
+    rows = (B, T, Hk, d)
+    qs, ks, vs = _tokens(q, "q", q.shape, dt, dev), _tokens(k, "k", rows, dt, dev), _tokens(v, "v", rows, dt, dev)
     _like(wq, "wq", (d,), torch.float32)
     _like(wk, "wk", (d,), torch.float32)
     _like(positions, "positions", (B, T), torch.int32)
@@ -383,9 +381,9 @@ def kv_cache_append(q, k, v, slots, k_cache, v_cache, freqs, wq=None, wk=None, p
     P, Hc, page, dc, code = _cache(k_cache, v_cache, k_scale, v_scale, dt)
     if (Hc, dc) != (Hk, d):
         raise ValueError(f"the cache's rows are [{Hc}, {dc}], the keys' [{Hk}, {d}]")
-    _call(dev, lib().gdn2_kv_cache_append, _ptr(q), _ptr(k), _ptr(v), *strides[:3], _ptr(wq), _ptr(wk), _ptr(freqs),
+    _call(dev, lib().gdn2_kv_cache_append, _ptr(q), _ptr(k), _ptr(v), qs, ks, vs, _ptr(wq), _ptr(wk), _ptr(freqs),
           _ptr(positions), _ptr(slots), B, T, Hq, Hk, d, rot, eps, P, page, _dtype_code(q), code, flags, _ptr(out),
-          strides[3], _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale))
+          _tokens(out, "out", q.shape, dt, dev), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale))
     return out
 
 

@@ -708,14 +708,19 @@ int attn_bwd_parts(const attn_sizes &z) {
 }
 
 // Workgroups that share the rows behind the window of a 32-sink tile of a
-// sequence and kv head: enough for 1024 in all, at most 64 and at most one for
-// every 512 rows of the call.
+// sequence and kv head: one a CU, or where sequences are packed, whose lengths
+// differ, four; at most 64 and at most one for every 128 rows of the call.  (8 x
+// 4096 tokens, window 2048, 4 sinks, 16 heads on 4, d = 128: 33 us for 256
+// workgroups, 40 and 48 for 512 and 1024, 134 MB read; 32768 tokens: 57, 252 MB;
+// 11 packed sequences, 9973 tokens, window 500, 33 sinks, d = 64: 35 for 256, 22
+// and 19 for 512 and 1024; 1543 float32 tokens, 7 sinks: 10.3, and 15.1 for 512
+// rows a workgroup.)
 int attn_bwd_far_parts(const attn_sizes &z) {
   const long long units = static_cast<long long>(z.N) * z.Hk * ((z.sinks + FAR_KEYS - 1) / FAR_KEYS);
   const long long rows = static_cast<long long>(z.T) * (z.Hq / z.Hk);
-  long long p = (1024 + units - 1) / units;
-  if (p > rows / 512)
-    p = rows / 512;
+  long long p = ((z.packed ? 1024 : 256) + units - 1) / units;
+  if (p > rows / 128)
+    p = rows / 128;
   return p < 1 ? 1 : (p > 64 ? 64 : static_cast<int>(p));
 }
 
@@ -741,6 +746,16 @@ static void fill(bwd_args &a, const attn_sizes &z, const attn_ptrs &p, void *ws,
   a.c = z.scale * LOG2E;
   a.scale = z.scale;
   a.parts = attn_bwd_parts(z);
+  if (z.sinks) {
+    // Here a window counts (the workspace has room for more): about 2048 rows
+    // of 64 channels, or 1024 of 128, a part.  (4 sinks, windows of 100, 500, 2000:
+    // 4096 tokens, 4 heads on 4, d = 128: 33, 44, 58 us with 1, 1, 2 parts, 57, 62, 72
+    // with 4; 16 heads on 2: 69, 95, 176 with 2, 5, 8, and 103, 195, 541 with one;
+    // 9973 packed tokens, 12 heads on 4, d = 64, window 500: 72 with one, 90 with 2.)
+    const long long keys = z.T < z.window + 128LL ? z.T : z.window + 128LL, rows = keys * a.G;
+    const long long most = (rows * d + 65536) / 131072;
+    a.parts = most < 1 ? 1 : (most < a.parts ? static_cast<int>(most) : a.parts);
+  }
   a.part_sums = a.parts > 1 ? reinterpret_cast<float *>(static_cast<char *>(ws) + attn_bwd_stat_bytes(z)) : nullptr;
   a.sinks = z.sinks;
   a.far_parts = z.sinks ? attn_bwd_far_parts(z) : 0;

@@ -142,11 +142,36 @@ bool decode_rows(const attn_sizes &z) {
 // heads: 136 us at 2048 workgroups, 151 at 1024 and 512; one 1024-token chunk
 // among 23 tokens: 113 us at 768, 125 at 1024, 137 at 2048, where its parts'
 // outputs weigh more.)
+// With sinks, decode's sequences are about as long as their window and sinks,
+// so the parts are chosen for whole rounds over the chip: a round takes its
+// tiles of 128 keys and about three more to begin and end, the join about two.
+// (Window 2048, 4 sinks, 16 heads on 4, e4m3: 64 sequences 32 us with 2 or 3
+// parts, 43 with 8; 200 sequences 93 with 3, 104 with one, 117 with 8; 16
+// sequences 17 with 6 or 9, 25 with 2.)
+static int sink_splits(const attn_sizes &z, long long blocks) {
+  const long long slots = decode_rows(z) ? 768 : 512;
+  long long keys = static_cast<long long>(z.window) + z.sinks + 30 + z.T;
+  keys = keys < z.max_keys ? keys : z.max_keys;
+  const long long tiles = (keys + 127) / 128;
+  long long best = 1, least = (blocks + slots - 1) / slots * (tiles + 3);
+  for (long long s = 2; s <= tiles && s <= 128; ++s) {
+    const long long per = (tiles + s - 1) / s;
+    const long long cost = (blocks * s + slots - 1) / slots * (per + 3) + 2;
+    // (a part without keys is one too many)
+    if (cost < least && (s - 1) * per < tiles) {
+      least = cost;
+      best = s;
+    }
+  }
+  return static_cast<int>(best);
+}
 int attn_paged_splits(const attn_sizes &z) {
   order od;
   const bool few = few_rows(z);
   plan_tiles(z, z.Hq / z.Hk, few ? 32 : 128, od);
   const long long blocks = static_cast<long long>(od.units) * od.tiles;
+  if (z.sinks && few)
+    return sink_splits(z, blocks);
   long long keys = z.max_keys;
   if (z.window > 0 && keys > z.window + z.sinks + 128LL)
     keys = z.window + z.sinks + 128LL;
