@@ -381,9 +381,10 @@ def kv_cache_append(q, k, v, slots, k_cache, v_cache, freqs, wq=None, wk=None, p
     P, Hc, page, dc, code = _cache(k_cache, v_cache, k_scale, v_scale, dt)
     if (Hc, dc) != (Hk, d):
         raise ValueError(f"the cache's rows are [{Hc}, {dc}], the keys' [{Hk}, {d}]")
-    _call(dev, lib().gdn2_kv_cache_append, _ptr(q), _ptr(k), _ptr(v), qs, ks, vs, _ptr(wq), _ptr(wk), _ptr(freqs),
-          _ptr(positions), _ptr(slots), B, T, Hq, Hk, d, rot, eps, P, page, _dtype_code(q), code, flags, _ptr(out),
-          _tokens(out, "out", q.shape, dt, dev), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale))
+    _call(dev, lib().gdn2_kv_cache_append, q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, _ptr(wq), _ptr(wk),
+          _ptr(freqs), _ptr(positions), slots.data_ptr(), B, T, Hq, Hk, d, rot, eps, P, page, _dtype_code(q), code, flags,
+          out.data_ptr(), _tokens(out, "out", q.shape, dt, dev), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale),
+          _ptr(v_scale))
     return out
 
 

@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
 // Sinks.  The rows that see a sink from behind the window (all later ones) are
 // many for few keys: a launch of its own (DKV_FAR) shares them among far_parts
 // workgroups a 32-key tile and leaves float32 sums, and the workgroup that owns
-// the keys (DKV_SINK) adds them to its window's.  Every sum has a fixed order.
+// the keys (DKV_SINK) begins with them.  Every sum has a fixed order.
 enum dkv_mode { DKV_PLAIN, DKV_SINK, DKV_FAR };
 // Tile of the DKV_FAR launch: 128 rows where two of them fit shared memory
 // beside the keys (64 would pass through registers and spill).
@@ -445,6 +445,27 @@ __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1))
     return;  // (no sums: far_parts_of does not count the part)
   if (it0 < it1)
     load_tile(it0);
+  if constexpr (M == DKV_SINK) {
+    // a sink's sums over the far rows: part 0's row parts begin with them
+    if (part == 0 && key < a.sinks && key < last_key) {
+      const int np = far_parts_of<IO, D>(a, sq.len, key);
+      for (int p = wrow; p < np; p += WR) {
+        const float *const sk = far_sum<D>(a, p, false, sq.n, key, hk) + 4 * h;
+        const float *const sv = far_sum<D>(a, p, true, sq.n, key, hk) + 4 * h;
+#pragma unroll
+        for (int n = 0; n < D / 32; ++n)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const f32x4 x = io<float>::load4(sk + 32 * n + 8 * g), y = io<float>::load4(sv + 32 * n + 8 * g);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              dk[n][4 * g + i] += x[i];
+              dv[n][4 * g + i] += y[i];
+            }
+          }
+      }
+    }
+  }
   for (int it = it0; it < it1; ++it) {
     const int buf = NB == 2 ? it & 1 : 0;
     const int bo = buf * 2 * TILEB;
@@ -562,7 +583,7 @@ __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1))
           x[n][4 * g + i] += y[i];
       }
   };
-  auto store = [&](f32x16(&x)[D / 32], float scale, IO *out) {
+  auto store = [&](const f32x16(&x)[D / 32], float scale, IO *out) {
     if (key >= last_key)
       return;
     const size_t at = (static_cast<size_t>(sq.start + key) * a.Hk + hk) * D + 4 * h;
@@ -576,23 +597,6 @@ __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1))
           io<float>::store4(sums + 32 * n + 8 * g,
                             f32x4{x[n][4 * g], x[n][4 * g + 1], x[n][4 * g + 2], x[n][4 * g + 3]});
       return;
-    }
-    if constexpr (M == DKV_SINK) {
-      if (a.parts == 1 && key < a.sinks) {
-        const int np = far_parts_of<IO, D>(a, sq.len, key);
-        for (int p = 0; p < np; ++p) {
-          const float *const sums = far_sum<D>(a, p, is_v, sq.n, key, hk) + 4 * h;
-#pragma unroll
-          for (int n = 0; n < D / 32; ++n)
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              const f32x4 y = io<float>::load4(sums + 32 * n + 8 * g);
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                x[n][4 * g + i] += y[i];
-            }
-        }
-      }
     }
     if (a.parts > 1) {
       float *const sums = a.part_sums + (2 * part + (is_v ? 1 : 0)) * (static_cast<size_t>(a.Ttot) * a.Hk * D) + at;
@@ -645,7 +649,7 @@ __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1))
 
 // The parts' sums, in order, to dk and dv: four channels a thread, dk's then
 // dv's.
-template <typename IO, int D, bool SINK> __global__ void __launch_bounds__(256) gdn2_attn_dkv_join_kernel(bwd_args a) {
+template <typename IO, int D> __global__ void __launch_bounds__(256) gdn2_attn_dkv_join_kernel(bwd_args a) {
   const size_t rows = static_cast<size_t>(a.Ttot) * a.Hk * D;
   const size_t at = (static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
   if (at >= 2 * rows)
@@ -658,29 +662,6 @@ template <typename IO, int D, bool SINK> __global__ void __launch_bounds__(256) 
 #pragma unroll 4
   for (int p = 0; p < a.parts; ++p)
     x += io<float>::load4(a.part_sums + 2 * p * rows + at);
-  if constexpr (SINK) {
-    const int row = static_cast<int>(e / D), tok = row / a.Hk, hk = row % a.Hk;
-    span sq;
-    if (a.cu) {
-      // the last sequence that starts at or before the token
-      int lo = 0, hi = a.N;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        (a.cu[mid] <= tok ? lo : hi) = mid;
-      }
-      sq = packed_span(a.cu, lo, a.T);
-    } else {
-      sq.n = tok / a.T;
-      sq.start = sq.n * a.T;
-      sq.len = a.T;
-    }
-    const int key = tok - sq.start;
-    if (key >= 0 && key < a.sinks) {
-      const int np = far_parts_of<IO, D>(a, sq.len, key);
-      for (int p = 0; p < np; ++p)
-        x += io<float>::load4(far_sum<D>(a, p, is_v, sq.n, key, hk) + e % D);
-    }
-  }
   io<IO>::store4(static_cast<IO *>(is_v ? a.dv : a.dk) + e, x * (is_v ? 1.f : a.scale));
 }
 
@@ -824,11 +805,7 @@ hipError_t launch_attn_bwd_dkv(const attn_sizes &z, const attn_ptrs &p, void *ws
   }
   if (a.parts > 1) {
     const size_t n = static_cast<size_t>(z.Ttot) * z.Hk * D / 2;  // threads
-    const dim3 grid(static_cast<unsigned>((n + 255) / 256));
-    if (a.sinks)
-      hipLaunchKernelGGL((gdn2_attn_dkv_join_kernel<IO, D, true>), grid, dim3(256), 0, st, a);
-    else
-      hipLaunchKernelGGL((gdn2_attn_dkv_join_kernel<IO, D, false>), grid, dim3(256), 0, st, a);
+    hipLaunchKernelGGL((gdn2_attn_dkv_join_kernel<IO, D>), dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, st, a);
   }
   return hipGetLastError();
 }
