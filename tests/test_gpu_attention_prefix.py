@@ -306,3 +306,94 @@ def test_serving_with_a_shared_prompt(g):
         for n in range(N):
             r = plain(q2[n].double(), kk[n].double(), vv[n].double(), 0, 0)
             ref.check_attn({"o": o[n], "lse": lse[n]}, r, BF16, kk.shape[1], d, f"step {t} request {n}")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype,f8", [(BF16, False), (BF16, True), (F32, False), (F32, True)])
+def test_prefix_odd_values_and_entries_many_rows(g, dtype, f8, d):
+    """The same with tiles of 128 rows: entries outside the cache, odd pages behind the length, NaN that one group sees."""
+    page, Hk, N = 16, 2, 90
+    own = [1 + 7 * n % 40 for n in range(N)]
+    print(f"prefix odd, many rows d={d} {dtype} f8={f8}", flush=True)
+    c = Call(g, [300, 190], [0, 50, N], [1] * N, own, 8, Hk, d, page, dtype, f8, seed=21)
+    o0, lse0 = c.run(g)
+    c.check(o0, lse0)
+    c.c.poison(c.c.spare)
+    c.prefix_table[1, 12:] = c.c.spare
+    o, lse = c.run(g)
+    assert torch.equal(o, o0) and torch.equal(lse, lse0)
+    rows = c.c.rows[0]
+    k, v = (x.clone() for x in rows)
+    for p, bad in ((2, -1), (7, 2 ** 31 - 1), (18, c.c.k.shape[0])):
+        c.prefix_table[0, p] = bad
+        k[p * page:(p + 1) * page], v[p * page:(p + 1) * page] = 0.0, 0.0
+    c.c.rows[0] = (k, v)
+    c.check(*c.run(g))
+    c.prefix_table[0, 5] = c.c.spare
+    o, lse = c.run(g)
+    assert o[:50].isnan().all() and torch.equal(o[50:], o0[50:]) and torch.equal(lse[50:], lse0[50:])
+
+
+@pytest.mark.parametrize("power", [-100, 60])
+def test_prefix_scales(g, power):
+    """Quantised rows of very small and large scales, for few rows and many."""
+    page, Hk, d, P = 16, 1, 64, 200
+    for N in (3, 70):
+        print(f"prefix scales 2^{power} N={N}", flush=True)
+        c = Call(g, [P], [0, N], [1] * N, [3] * N, 4, Hk, d, page, BF16, True, seed=22)
+        # every other row of the prefix's values, and its keys one way (scores of size 1 need the other in q)
+        s = c.c.slots(0, P)
+        e = torch.arange(P, device="cuda") % 2 * power
+        c.c.vs[s // page, :, s % page] = (c.c.vs[s // page, :, s % page].int() + e[:, None]).to(torch.uint8)
+        k, v = c.c.rows[0]
+        c.c.rows[0] = (k, v * torch.exp2(e.double())[:, None, None])
+        c.check(*c.run(g))
+
+
+def test_prefix_offsets_past_32_bits(g):
+    """A cache of 5 GiB (bfloat16) and 2.5 GiB (e4m3), prefix and own keys in its last pages."""
+    Hk, page, d, P = 8, 64, 128, 150
+    pages = 5 * (1 << 30) // (Hk * page * d * 2)
+    for cdt in (BF16, F8):
+        kc, vc = (torch.empty((pages, Hk, page, d), dtype=cdt, device="cuda") for _ in range(2))
+        ks, vs = (torch.empty((pages, Hk, page), dtype=torch.uint8, device="cuda") for _ in range(2)) \
+            if cdt == F8 else (None, None)
+        ptab = torch.tensor([[pages - 1, pages - 3, pages - 2]], dtype=torch.int32, device="cuda")
+        for N in (2, 40):
+            tab = (pages - 4 - torch.arange(N, dtype=torch.int32, device="cuda"))[:, None].contiguous()
+            lens = torch.arange(1, N + 1, dtype=torch.int32, device="cuda")
+            t = torch.arange(P, device="cuda")
+            slots = [ptab[0, t // page].long() * page + t % page]
+            slots += [tab[n, 0].long() * page + torch.arange(n + 1, device="cuda") for n in range(N)]
+            rows = []
+            for i, s in enumerate(slots):
+                k, v = (randn(200 + 2 * i + j, (s.numel(), Hk, d), BF16) for j in range(2))
+                g.kv_cache_write(k, v, s, kc, vc, ks, vs)
+                rows.append(tuple(x.double() for x in g.kv_cache_read(s, kc, vc, ks, vs)))
+            q = randn(199, (N, 1, 16, d), BF16)
+            print(f"prefix large cache {cdt} N={N}", flush=True)
+            o, lse = g.attn_paged_prefix(q, kc, vc, ptab, torch.tensor([P], dtype=torch.int32, device="cuda"), tab, lens,
+                                         k_scale=ks, v_scale=vs, want_lse=True)
+            for n in range(N):
+                kk, vv = (torch.cat((rows[0][j], rows[1 + n][j])) for j in range(2))
+                check_rows(o[n], lse[n], q[n], kk, vv, 0, 0, BF16, d, f"seq {n}", cdt == F8)
+        del kc, vc, ks, vs
+        torch.cuda.empty_cache()
+
+
+def test_prefix_two_calls_at_once(g):
+    """Two calls on two streams, each on its own workspace, many times over."""
+    calls = [Call(g, [900], [0, 33], [1] * 33, [1 + 5 * n for n in range(33)], 8, 2, 128, 64, BF16, f8, seed=23 + f8)
+             for f8 in (False, True)]
+    want = [c.run(g, one=True) for c in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    outs = []
+    for i in range(8):
+        for c, s in zip(calls, streams):
+            with torch.cuda.stream(s):
+                outs.append(g.attn_paged_prefix(c.q, c.c.k, c.c.v, c.prefix_table, c.prefix_lens, c.table, c.lens,
+                                                want_lse=True, **c.c.scales()))
+    torch.cuda.synchronize()
+    for i, (o, lse) in enumerate(outs):
+        assert torch.equal(o, want[i % 2][0]) and torch.equal(lse, want[i % 2][1])

@@ -380,3 +380,68 @@ def test_sinks_prompt_then_decode(g):
         r = plain(q[0, t:t + 1].double(), k[0, :t + 1].double(), v[0, :t + 1].double(), window, sinks)
         for x in (o[0], whole[0, t:t + 1]):
             ref.check_attn({"o": x}, r, BF16, t + 1, d, f"step {t}")
+
+
+def test_sinks_offsets_past_32_bits(g):
+    """Tensors of 4 GiB each: one sequence of 2^17 tokens x 128 heads, whose
+    last rows see the first keys; the sinks' gradients are sums over all rows."""
+    H, d, T, window, sinks, n = 128, 128, (1 << 17) + 70, 64, 4, 70
+    gn = torch.Generator(device="cuda")
+    gn.manual_seed(60)
+    q, k, v, do = (torch.randn((1, T, H, d), generator=gn, device="cuda", dtype=BF16) for _ in range(4))
+    print("sinks large tensors: forward", flush=True)
+    o, lse = g.attn_fwd(q, k, v, window=window, sinks=sinks)
+    keys = torch.cat((torch.arange(sinks), torch.arange(T - n - window + 1, T))).cuda()
+    kk, vv = k[0, keys].double(), v[0, keys].double()
+    # those rows and keys as a sequence of their own
+    r = plain(q[0, T - n:].double(), kk, vv, window, sinks)
+    ref.check_attn({"o": o[0, T - n:], "lse": lse[0, T - n:]}, r, BF16, keys.numel(), d, "last rows")
+    print("sinks large tensors: backward", flush=True)
+    gr = g.attn_bwd(q, k, v, o, lse, do, window=window, sinks=sinks)
+    # the sinks' gradients by the formula from the forward's o and lse, a block of rows at a time
+    want = {m: torch.zeros((sinks, H, d), dtype=torch.float64, device="cuda") for m in ("dk", "dv", "dk_abs", "dv_abs")}
+    for t in range(0, T, 1 << 13):
+        rows = slice(t, min(t + (1 << 13), T))
+        qq, dd, oo = (x[0, rows].double() for x in (q, do, o))
+        delta = (dd * oo).sum(-1)
+        pos = torch.arange(T, device="cuda")[rows]
+        for j in range(sinks):
+            p = torch.exp((qq * k[0, j].double()).sum(-1) * d ** -0.5 - lse[0, rows].double())
+            p = torch.where(pos[:, None] >= j, p, 0.0)
+            ds = p * ((dd * v[0, j].double()).sum(-1) - delta) * d ** -0.5
+            want["dv"][j] += (p[..., None] * dd).sum(0)
+            want["dk"][j] += (ds[..., None] * qq).sum(0)
+            want["dv_abs"][j] += (p[..., None] * dd.abs()).sum(0)
+            want["dk_abs"][j] += (ds.abs()[..., None] * qq.abs()).sum(0)
+    for m in ("dk", "dv"):
+        # half a step of the weights as operands and of the output; in float32 a product of 128 terms inside each
+        # weight and a sum of up to 2^17 rows in parts of at most 2^12
+        bound = ref.step(BF16) * want[m].abs() + (1.01 * ref.step(BF16) + 2.0 ** -11) * want[m + "_abs"]
+        ref.check(gr[m][0, :sinks], want[m], bound, m)
+    assert all(torch.isfinite(x).all() for x in gr.values())
+
+
+def test_sinks_two_calls_at_once(g):
+    """Forward and backward of two sizes on two streams, each on its own workspace."""
+    sets = []
+    for i, (T, Hk, d) in enumerate(((500, 2, 128), (900, 1, 64))):
+        x = [randn(70 + 4 * i + j, (1, T, h, d), BF16) for j, h in enumerate((4 * Hk, Hk, Hk, 4 * Hk))]
+        ws = torch.empty(g.attn_bwd_workspace_bytes(1, T, 4 * Hk, Hk, d, BF16, sinks=5), dtype=torch.uint8, device="cuda")
+        sets.append((x, ws))
+
+    def step(x, ws):
+        q, k, v, do = x
+        o, lse = g.attn_fwd(q, k, v, window=40, sinks=5)
+        gr = g.attn_bwd(q, k, v, o, lse, do, window=40, sinks=5, workspace=ws)
+        return [o, lse, gr["dq"], gr["dk"], gr["dv"]]
+    want = [step(*s) for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(6):
+        for s, st in zip(sets, streams):
+            with torch.cuda.stream(st):
+                got.append(step(*s))
+    torch.cuda.synchronize()
+    for i, x in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(x, want[i % 2]))
