@@ -92,7 +92,8 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
   static_assert(BN * CPR % NT == 0, "staging split");
   static_assert(WN == 1 || WN * 32 * D * 4 <= 4 * TILEB, "join space");
   __shared__ __align__(16) char lds[4 * TILEB];  // K and V tiles, double-buffered
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 31, h = lane >> 5;
+  const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);  // (uniform: so is what follows from it)
   const int wm = WN == 1 ? wave : 0, wn = WN == 1 ? 0 : wave;
   int unit, slot, hk, row0;
   span sq;
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
     a.stat[(static_cast<size_t>(hk) * a.Ttot + sq.start) * a.G + cl_row] = st;
   // Tiles come straight from memory: position p of one is chunk (p % CPR) ^ f
   // of row p / CPR.
-  const int sc = tid % CPR, sr0 = tid / CPR, wv = __builtin_amdgcn_readfirstlane(wave);
+  const int sc = tid % CPR, sr0 = tid / CPR;
   const int row_b = TL::row_base(r, h), col_b = TL::col_base(lane);
   const unsigned kstep = static_cast<unsigned>(a.Hk) * D;  // values of a token
   char *const kt = lds, *const vt = lds + TILEB;
@@ -147,7 +148,7 @@ __global__ void __launch_bounds__(64 * WM * WN, (D * sizeof(IO) <= 256 ? 2 : 1))
     const size_t base = (static_cast<size_t>(sq.start + (mixed ? 0 : kb + gap)) * a.Hk + hk) * D;
     const IO *const kp = static_cast<const IO *>(a.k) + base, *const vp = static_cast<const IO *>(a.v) + base;
     const int left = k1 - 1 - kb;  // (a key behind the last: any, its score is masked)
-    char *const to = lds + buf * 2 * TILEB + 1024 * wv;
+    char *const to = lds + buf * 2 * TILEB + 1024 * wave;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int x = sr0 + RPI * i;
@@ -322,7 +323,8 @@ __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1))
   __shared__ __align__(16) char lds[TILES > JOIN ? TILES : JOIN];
   __shared__ __align__(16) float s_lse[NB][BQ], s_delta[NB][BQ];
   __shared__ __align__(16) int s_pos[NB][BQ];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 31, h = lane >> 5;
+  const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);  // (uniform: so is what follows from it)
   const int wkey = wave % WK, wrow = wave / WK;
   int unit, slot, hk, key0;
   span sq;
@@ -379,7 +381,6 @@ __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1))
   }
   // With two buffers a tile comes straight from memory: position p of it is
   // chunk (p % CPR) ^ f of row p / CPR.  With one it passes through registers.
-  const int wv = __builtin_amdgcn_readfirstlane(wave);
   u32x4 rq[NB == 2 ? 1 : CH], rd[NB == 2 ? 1 : CH];
   f32x2 rs = {0.f, 0.f};
   int rp = 0;
@@ -419,7 +420,7 @@ __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1))
     for (int i = 0; i < CH; ++i) {
       const unsigned off = (tok_of[i] < left ? tok_of[i] : left) * tstep + at_of[i];
       if constexpr (NB == 2) {
-        char *const to = qt + (it & 1) * 2 * TILEB + 1024 * wv + 16 * NT * i;
+        char *const to = qt + (it & 1) * 2 * TILEB + 1024 * wave + 16 * NT * i;
         dma16(qb + off, to);
         dma16(db + off, to + TILEB);
       } else {
