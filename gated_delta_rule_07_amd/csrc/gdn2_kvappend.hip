@@ -76,8 +76,10 @@ template <typename IO, typename CT, int D> __global__ void __launch_bounds__(256
       rotate(R.interleaved, c, s, 1.f, a, b);
     u32x2 code = {0u, 0u};
     uint8_t byte = 0;
-    if constexpr (F8)
-      byte = quantise_row<D>(a, b, code);
+    if constexpr (F8) {
+      if (h0 + HPW > R.Hq)  // (the wave's heads are not all queries)
+        byte = quantise_row<D>(a, b, code);
+    }
     if (!ok)
       continue;
     if (isq) {
