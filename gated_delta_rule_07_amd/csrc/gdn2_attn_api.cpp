@@ -137,6 +137,14 @@ gdn2_status_t check_attn(const char *fn, int B, int T, int Hq, int Hk, int d, in
   return GDN2_OK;
 }
 
+// The backward with sinks has a launch of a workgroup at least for every 32
+// sinks of a sequence and kv head, of 256 threads each.
+gdn2_status_t check_far(const char *fn, const attn_sizes &z) {
+  if (static_cast<long long>(z.N) * z.Hk * ((z.sinks + 31) / 32) >= (1LL << 23))
+    return fail(GDN2_ERR_UNSUPPORTED, "%s: too large (at most 2^23 - 1 sequence-heads times 32 sinks)", fn);
+  return GDN2_OK;
+}
+
 gdn2_status_t check_ptrs(const char *fn, std::initializer_list<const void *> need,
                          std::initializer_list<const void *> optional = {}) {
   for (const void *p : need)
@@ -334,6 +342,9 @@ gdn2_status_t attn_bwd(const char *fn, const void *q, const void *k, const void 
     return st;
   if (T == 0)
     return ok();
+  st = check_far(fn, z);
+  if (st != GDN2_OK)
+    return st;
   st = check_ptrs(fn, {q, k, v, o, lse, dout, dq, dk, dv}, {cu_seqlens, workspace});
   if (st != GDN2_OK)
     return st;
@@ -521,7 +532,8 @@ size_t gdn2_attn_sink_bwd_workspace_bytes(int B, int T, int Hq, int Hk, int d, i
   attn_sizes z;
   // (no window hides more than one token's; a call that takes more sinks has none that hides anything)
   if (check_attn("gdn2_attn_sink_bwd_workspace_bytes", B, T, Hq, Hk, d, num_seqs, num_seqs > 0, 1,
-                 sinks > MAX_SINKS ? 0 : sinks, 1.f, GDN2_F32, z) != GDN2_OK) {
+                 sinks > MAX_SINKS ? 0 : sinks, 1.f, GDN2_F32, z) != GDN2_OK ||
+      check_far("gdn2_attn_sink_bwd_workspace_bytes", z) != GDN2_OK) {
     (void)ok();
     return 0;
   }

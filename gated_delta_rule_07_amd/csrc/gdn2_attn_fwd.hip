@@ -29,7 +29,7 @@
 // sequence of 32768 tokens, 16 heads on 4, d = 128, bfloat16: 4.3 to 4.5 ms,
 // 975 to 1020 TFLOP/s (an 8192^3 product: 1212; without tiles straight from
 // memory 4650 us, without read-ahead and with a rescale every tile 4880); 8 x
-// 4096 tokens, window 2048: 480 to 500 us.  Paged, 1024 tokens at 12000 keys among
+// 4096 tokens, window 2048: 480 to 500 us, with 4 sinks 500 to 510.  Paged, 1024 tokens at 12000 keys among
 // 23 single tokens: 105 us with the join's 10 (341 MB: 73 us at a copy's rate).
 #include "gdn2_attn_launch.hpp"
 

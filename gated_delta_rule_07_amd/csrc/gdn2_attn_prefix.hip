@@ -8,14 +8,14 @@
 // taken as one block of rows, whose tiles read the prefix's keys and values
 // once for 128 rows, and not once a sequence.
 //
-// The prefix's part is bound by matrix products (many rows a key), the own
-// keys' by memory, so one launch has the workgroups of both and a CU works on
-// one of either kind at a time.  Measured, 64 sequences behind 32768 keys with
-// up to 1500 of their own, 16 heads on 4, d = 128, bfloat16 (17.6 GFLOP, 169 MB: 36 us
-// at a large copy's rate): 42 us and 6 for the join; in two launches 37 and 28,
-// and 10 for the join of more parts.  41 sequences in three groups, one of 200 new
-// tokens, e4m3: 42 and 9.5 (two launches 62, 23 and 12; 45 of the 62 without the
-// codes widened before shared memory).
+// The prefix's part is bound by matrix products (many rows a key) and by the one
+// tile a workgroup has under way, the own keys' by memory, so one launch has the
+// workgroups of both and a CU works on one of either kind at a time.  Measured,
+// 64 sequences behind 32768 keys with up to 1500 of their own, 16 heads on 4, d =
+// 128, bfloat16 (17.6 GFLOP, 169 MB: 36 us at a large copy's rate), caches cold: 53 us
+// and 7 for the join; the prefix alone 45, the own keys alone 27.  41 sequences in
+// three groups, one of 200 new tokens, e4m3: 45 and 8 (in two launches 62, 23 and
+// 12; 45 of the 62 without the codes widened before shared memory).
 #include "gdn2_attn_decode_body.hpp"
 #include "gdn2_attn_launch.hpp"
 

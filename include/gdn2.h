@@ -596,10 +596,12 @@ gdn2_status_t gdn2_attn_paged_prefix(const void *q, const void *k_cache, const v
  * position i when j <= i and (j > i - window or j < sinks).  Arguments and
  * results as for gdn2_attn_fwd, gdn2_attn_bwd and gdn2_attn_paged; sinks >= 0,
  * without effect where window is 0.  Where the window hides anything (window +
- * sinks less than the longest sequence) sinks is at most 1024
- * (GDN2_ERR_UNSUPPORTED).  In the paged form the sinks are the sequence's
- * first keys; table entries whose page holds neither a sink nor a key of a
- * query's window are not read, so such pages can be freed and used again. */
+ * sinks less than T, in the paged form less than max_pages * page_size + T)
+ * sinks is at most 1024, and the backward takes at most 2^23 - 1 (sequence, kv
+ * head, 32 sinks) triples (GDN2_ERR_UNSUPPORTED).  In the paged form the sinks
+ * are the sequence's first keys; table entries whose page holds neither a sink
+ * nor a key of a query's window are not read, so such pages can be freed and
+ * used again. */
 gdn2_status_t gdn2_attn_sink_fwd(const void *q, const void *k, const void *v, const int32_t *cu_seqlens, int B, int T,
                                  int Hq, int Hk, int d, int num_seqs, int window, int sinks, float scale,
                                  gdn2_dtype_t dt, void *o, float *lse, void *stream);

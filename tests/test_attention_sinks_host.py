@@ -68,6 +68,16 @@ def test_bwd_workspace(L):
     assert L.gdn2_last_error() == b""
 
 
+def test_bwd_most_sinks(L):
+    """A launch for every 32 sinks of a sequence and kv head has to fit a grid."""
+    big = dict(cu=FAKE, B=1, T=1 << 22, Hq=8, Hk=8, N=1 << 16)
+    assert bwd(L, sinks=1024, **big) == 2 and b"32 sinks" in L.gdn2_last_error()
+    assert bwd(L, sinks=480, q=None, **big) == 1 and b"null" in L.gdn2_last_error()
+    assert fwd(L, sinks=1024, q=None, **big) == 1 and b"null" in L.gdn2_last_error()
+    assert L.gdn2_attn_sink_bwd_workspace_bytes(1, 1 << 22, 8, 8, 64, 1 << 16, 1024) == 0
+    assert L.gdn2_attn_sink_bwd_workspace_bytes(1, 1 << 22, 8, 8, 64, 1 << 16, 480) > 0
+
+
 def test_paged_workspace(L):
     w, plain = L.gdn2_attn_sink_paged_workspace_bytes, L.gdn2_attn_paged_workspace_bytes
     assert w(1, 1, 16, 4, 128, 0, 16, 1000, 0, 0) == plain(1, 1, 16, 4, 128, 0, 16, 1000, 0)
