@@ -36,16 +36,28 @@ template <typename IO, typename CT, int D> __global__ void __launch_bounds__(256
   constexpr bool F8 = sizeof(CT) == 1;
   const rope_args &R = A.r;
   const int lane = threadIdx.x & 63, j = lane % LPH, hh = lane / LPH;
-  const long u = static_cast<long>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  if (u >= R.tokens * R.parts)
+  // (a wave is on one token: what follows from it is uniform)
+  const int u = static_cast<int>(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int token = u / R.parts, part = u % R.parts;
+  if (token >= R.tokens)
     return;
-  const long token = u / R.parts;
-  const int part = static_cast<int>(u % R.parts);
   const int64_t slot = A.slots[token];
   const bool kept = slot >= 0 && slot < A.nslots;
   const lane_map m = map_lane<D>(R, j);
-  f32x4 c, s;
-  turn_of(R, m, j, token, c, s);
+  // lane p turns pair p, and a row's lanes fetch their four
+  f32x4 c = ones(), s = ones();
+  if (R.rot > 0) {
+    const double pos = static_cast<double>(R.positions ? R.positions[token] : token % R.T);
+    const int p = lane % (D / 2);
+    float cs = 1.f, sn = 0.f;
+    if (2 * p < R.rot)
+      turn(pos, R.freqs[p], cs, sn);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c[i] = __shfl(cs, 4 * j + i, 64);
+      s[i] = __shfl(sn, 4 * j + i, 64);
+    }
+  }
   f32x4 wqa = ones(), wqb = ones(), wka = ones(), wkb = ones();
   if (R.wq) {
     wqa = io<float>::load4(R.wq + m.a);
@@ -55,38 +67,54 @@ template <typename IO, typename CT, int D> __global__ void __launch_bounds__(256
     wka = io<float>::load4(R.wk + m.a);
     wkb = io<float>::load4(R.wk + m.b);
   }
+  const IO *const qt = static_cast<const IO *>(R.q) + token * A.qs, *const kt = static_cast<const IO *>(R.k) + token * A.ks;
+  const IO *const vt = static_cast<const IO *>(A.v) + token * A.vs;
+  IO *const ot = static_cast<IO *>(R.oq) + token * A.os;
   const int heads = R.Hq + 2 * R.Hk;
-  // every lane stays in the loop (the rows' exchanges need whole rows)
+  auto normed = [&](f32x4 &a, f32x4 &b, const f32x4 &wa, const f32x4 &wb) {
+    const float r = 1.f / sqrtf(row_sum<D>(dot4(a, a) + dot4(b, b)) * (1.f / D) + R.eps);
+    a = a * r * wa;
+    b = b * r * wb;
+  };
+  // (heads of a token: less than 2^32 values)
   for (int h0 = part * HPW; h0 < heads; h0 += R.parts * HPW) {
-    const int hd = h0 + hh, hk = hd < R.Hq + R.Hk ? hd - R.Hq : hd - R.Hq - R.Hk;
+    const int hd = h0 + hh;
+    if (h0 + HPW <= R.Hq) {
+      const unsigned at = static_cast<unsigned>(hd) * D;
+      f32x4 a = io<IO>::load4(qt + at + m.a), b = io<IO>::load4(qt + at + m.b);
+      if (R.norm)
+        normed(a, b, wqa, wqb);
+      if (m.turned)
+        rotate(R.interleaved, c, s, 1.f, a, b);
+      io<IO>::store4(ot + at + m.a, a);
+      io<IO>::store4(ot + at + m.b, b);
+      continue;
+    }
+    // keys and values among them; every lane stays (the rows' exchanges need
+    // whole rows)
+    const int hk = hd < R.Hq + R.Hk ? hd - R.Hq : hd - R.Hq - R.Hk;
     const bool ok = hd < heads, isq = hd < R.Hq, isv = hd >= R.Hq + R.Hk;
-    const IO *x = isq   ? static_cast<const IO *>(R.q) + token * A.qs + static_cast<long>(hd) * D
-                  : isv ? static_cast<const IO *>(A.v) + token * A.vs + static_cast<long>(hk) * D
-                        : static_cast<const IO *>(R.k) + token * A.ks + static_cast<long>(hk) * D;
+    const IO *x = (isq ? qt : isv ? vt : kt) + static_cast<unsigned>(isq ? hd : hk) * D;
     f32x4 a = {0.f, 0.f, 0.f, 0.f}, b = a;
     if (ok) {
       a = io<IO>::load4(x + m.a);
       b = io<IO>::load4(x + m.b);
     }
-    if (R.norm) {
-      const float r = 1.f / sqrtf(row_sum<D>(dot4(a, a) + dot4(b, b)) * (1.f / D) + R.eps);
-      if (!isv) {
-        a = a * r * (isq ? wqa : wka);
-        b = b * r * (isq ? wqb : wkb);
-      }
-    }
-    if (m.turned && !isv)
+    const f32x4 va = a, vb = b;
+    if (R.norm)
+      normed(a, b, isq ? wqa : wka, isq ? wqb : wkb);
+    if (m.turned)
       rotate(R.interleaved, c, s, 1.f, a, b);
+    a = isv ? va : a;
+    b = isv ? vb : b;
     u32x2 code = {0u, 0u};
     uint8_t byte = 0;
-    if constexpr (F8) {
-      if (h0 + HPW > R.Hq)  // (the wave's heads are not all queries)
-        byte = quantise_row<D>(a, b, code);
-    }
+    if constexpr (F8)
+      byte = quantise_row<D>(a, b, code);
     if (!ok)
       continue;
     if (isq) {
-      IO *y = static_cast<IO *>(R.oq) + token * A.os + static_cast<long>(hd) * D;
+      IO *y = ot + static_cast<unsigned>(hd) * D;
       io<IO>::store4(y + m.a, a);
       io<IO>::store4(y + m.b, b);
     } else if (kept) {

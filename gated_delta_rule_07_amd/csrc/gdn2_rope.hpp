@@ -38,6 +38,14 @@ template <int D> __device__ __forceinline__ lane_map map_lane(const rope_args &A
   return m;
 }
 
+// cosine and sine of pos * freq, the angle reduced to a fraction of a turn in
+// 64 bits
+__device__ __forceinline__ void turn(double pos, double freq, float &cs, float &sn) {
+  const double t = pos * freq * 0.15915494309189533577;  // turns
+  const float f = static_cast<float>(t - __builtin_rint(t));
+  sincospif(2.f * f, &sn, &cs);
+}
+
 __device__ __forceinline__ void turn_of(const rope_args &A, const lane_map &m, int j, long token, f32x4 &c, f32x4 &s) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -49,10 +57,8 @@ __device__ __forceinline__ void turn_of(const rope_args &A, const lane_map &m, i
   const double pos = A.positions ? static_cast<double>(A.positions[token]) : static_cast<double>(token % A.T);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const double t = pos * A.freqs[4 * j + i] * 0.15915494309189533577;  // turns
-    const float f = static_cast<float>(t - __builtin_rint(t));
     float sn, cs;
-    sincospif(2.f * f, &sn, &cs);
+    turn(pos, A.freqs[4 * j + i], cs, sn);
     c[i] = cs;
     s[i] = sn;
   }
