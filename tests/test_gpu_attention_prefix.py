@@ -397,3 +397,33 @@ def test_prefix_two_calls_at_once(g):
     torch.cuda.synchronize()
     for i, (o, lse) in enumerate(outs):
         assert torch.equal(o, want[i % 2][0]) and torch.equal(lse, want[i % 2][1])
+
+
+@pytest.mark.parametrize("dtype,f8", [(BF16, False), (BF16, True), (F32, False), (F32, True)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefix_tile_shapes_together(g, d, dtype, f8):
+    """Every pair of the prefixes' and the own keys' tiles (32 or 128 rows; 16, 32 or 128)."""
+    print(f"prefix tile shapes d={d} {dtype} f8={f8}", flush=True)
+    # 32 rows over the prefixes (more groups than rows would need), 128 over the own keys
+    c = Call(g, [90, 0, 40, 7, 200], [0, 0, 1, 1, 2, 2], [40, 40], [60, 41], 2, 2, d, 32, dtype, f8, seed=31)
+    c.check(*c.run(g))
+    # 32 and 32 (packed), 32 and 16
+    for packed in (True, False):
+        c = Call(g, [130, 60, 5], [0, 1, 2, 3], [2] * 3, [33, 2, 150], 8, 2, d, 16, dtype, f8, seed=32, packed=packed)
+        c.check(*c.run(g))
+    # 128 and 16, 128 and 32 (packed), 128 and 128
+    for T, packed in ((1, False), (1, True), (20, False), (20, True)):
+        c = Call(g, [333], [0, 48], [T] * 48, [T + n % 30 for n in range(48)], 8, 2, d, 64, dtype, f8, seed=33, packed=packed)
+        c.check(*c.run(g, one=True))
+
+
+def test_prefix_scale_and_defaults(g):
+    """A scale of its own, and outputs and workspace that the call makes."""
+    c = Call(g, [100], [0, 9], [1] * 9, [1 + n for n in range(9)], 4, 2, 64, 16, F32, False, seed=34)
+    c.q.mul_(0.3 * 8)  # scale 0.3 on the same scores as 1 / 8 on these
+    o, lse = c.run(g)
+    q = c.q / (0.3 * 8)
+    o2, lse2 = g.attn_paged_prefix(q, c.c.k, c.c.v, c.prefix_table, c.prefix_lens, c.table, c.lens, scale=0.3, want_lse=True)
+    o3, none = g.attn_paged_prefix(q, c.c.k, c.c.v, c.prefix_table, c.prefix_lens, c.table, c.lens, scale=0.3)
+    assert none is None and torch.equal(o2, o3)
+    assert (o2 - o).abs().max() < 1e-5 and (lse2 - lse).abs().max() < 1e-5

@@ -445,3 +445,53 @@ def test_sinks_two_calls_at_once(g):
     torch.cuda.synchronize()
     for i, x in enumerate(got):
         assert all(torch.equal(a, b) for a, b in zip(x, want[i % 2]))
+
+
+def test_sinks_scale_and_defaults(g):
+    q, k, v = (randn(90 + i, (1, 200, h, 64), F32) for i, h in enumerate((4, 2, 2)))
+    o, lse = g.attn_fwd(q * (0.3 * 8), k, v, window=30, sinks=3)
+    o2, lse2 = g.attn_fwd(q, k, v, window=30, sinks=3, scale=0.3)
+    o3, none = g.attn_fwd(q, k, v, window=30, sinks=3, scale=0.3, want_lse=False)
+    assert none is None and torch.equal(o2, o3)
+    assert (o2 - o).abs().max() < 1e-5 and (lse2 - lse).abs().max() < 1e-5
+
+
+@pytest.mark.parametrize("f8", [False, True])
+def test_sinks_decode_in_a_graph(g, f8):
+    """A captured decode step replayed while the sequences grow past their window, its workspace shared with another graph."""
+    Hq, Hk, d, page, window, sinks = 8, 2, 128, 16, 40, 3
+    c = Paged(g, [200, 37, 90], Hk, d, page, BF16, f8, seed=91)
+    q = randn(92, (3, 1, Hq, d), BF16)
+    table = c.table.cuda()
+    lens = torch.tensor([100, 10, 43], dtype=torch.int32, device="cuda")
+    ws = torch.empty(max(1, g.attn_paged_workspace_bytes(q, c.k, table, None, window, sinks),
+                         g.attn_paged_workspace_bytes(q, c.k, table)), dtype=torch.uint8, device="cuda")
+    outs = [torch.empty_like(q) for _ in range(2)]
+    lses = [torch.empty((3, 1, Hq), device="cuda") for _ in range(2)]
+    calls = [dict(window=window, sinks=sinks), dict()]
+
+    def step(i):
+        g.attn_paged(q, c.k, c.v, table, lens, out=outs[i], lse=lses[i], workspace=ws, **c.scales(), **calls[i])
+    graphs = []
+    for i in range(2):
+        step(i)
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            step(i)
+    for t in range(4):
+        lens.add_(9)
+        want = []
+        for i in range(2):
+            step(i)
+            want.append((outs[i].clone(), lses[i].clone()))
+        for i in (0, 1, 0):
+            outs[i].zero_()
+            ws.fill_(t)
+            graphs[i].replay()
+            torch.cuda.synchronize()
+            assert torch.equal(outs[i], want[i][0]) and torch.equal(lses[i], want[i][1]), (t, i)
+        for i, n in enumerate(lens.tolist()):
+            n = min(n, c.lk[i])
+            if lens[i] <= c.lk[i]:
+                check_rows(outs[0][i], lses[0][i], q[i], c.rows[i][0][:n], c.rows[i][1][:n], window, sinks, BF16, d,
+                           f"step {t} sequence {i}", f8)

@@ -251,3 +251,19 @@ def test_append_in_a_graph_and_on_streams(g):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(t, w) for t, w in zip(held, want)), i
+
+
+@pytest.mark.parametrize("dtype,f8", [(BF16, False), (F32, True)])
+def test_append_without_norm_and_rotation(g, dtype, f8):
+    """Neither norm nor rotation: the write, from any distance between tokens."""
+    gn = gen(74)
+    x = randn(gn, (2, 9, 8, 64), dtype)
+    q, k, v = x[:, :, :4], x[:, :, 4:6], x[:, :, 6:]
+    slots = torch.arange(18, device="cuda") * 2
+    (kc, vc), (ks, vs) = cache(4, 2, 16, 64, dtype, f8)
+    (kc2, vc2), (ks2, vs2) = cache(4, 2, 16, 64, dtype, f8)
+    o = g.kv_cache_append(q, k, v, slots, kc, vc, None, norm=False, k_scale=ks, v_scale=vs)
+    g.kv_cache_write(k.contiguous(), v.contiguous(), slots, kc2, vc2, k_scale=ks2, v_scale=vs2)
+    assert torch.equal(o, q)
+    assert torch.equal(kc.view(torch.uint8), kc2.view(torch.uint8)) and torch.equal(vc.view(torch.uint8), vc2.view(torch.uint8))
+    assert not f8 or (torch.equal(ks, ks2) and torch.equal(vs, vs2))
