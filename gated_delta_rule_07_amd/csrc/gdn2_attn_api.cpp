@@ -402,7 +402,8 @@ gdn2_status_t attn_paged(const char *fn, const void *q, const void *k_cache, con
                   {cu_seqlens, lse, workspace, block_table});
   if (st != GDN2_OK)
     return st;
-  const size_t need = paged_bytes(z, d);
+  const int splits = dt == GDN2_BF16 && gdn2::attn::attn_decode_wide(z) ? 1 : gdn2::attn::attn_paged_splits(z);
+  const size_t need = splits > 1 ? paged_bytes(z, d) : 0;
   if (need && (!workspace || workspace_bytes < need))
     return fail(GDN2_ERR_WORKSPACE_TOO_SMALL, "%s: workspace holds %zu bytes, %zu are needed", fn, workspace_bytes,
                 need);
@@ -418,7 +419,6 @@ gdn2_status_t attn_paged(const char *fn, const void *q, const void *k_cache, con
   p.cu = cu_seqlens;
   p.o = o;
   p.lse = lse;
-  const int splits = gdn2::attn::attn_paged_splits(z);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e;
   {

@@ -23,9 +23,9 @@
 namespace gdn2 {
 namespace attn {
 
-template <typename CT, int D, int TK, bool SINK>
-__global__ void __launch_bounds__(256, 3) gdn2_attn_decode_kernel(fwd_args a) {
-  typedef decode_body<CT, D, TK, SINK> F;
+template <typename CT, int D, int TK, bool SINK, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES, 3) gdn2_attn_decode_kernel(fwd_args a) {
+  typedef decode_body<CT, D, TK, SINK, WAVES> F;
   __shared__ __align__(16) char lds[F::BYTES];
   F::run(a, blockIdx.x, lds);
 }
@@ -35,10 +35,13 @@ template <typename CT, int D> hipError_t launch_attn_decode(const fwd_args &a, h
   // 136 us for 64 sequences of 4K to 16K keys)
   constexpr int TK = 2;
   const unsigned blocks = 8u * static_cast<unsigned>(a.od.units / a.od.g) * static_cast<unsigned>(a.od.tpr) * a.splits;
-  if (a.sinks)
-    hipLaunchKernelGGL((gdn2_attn_decode_kernel<CT, D, TK, true>), dim3(blocks), dim3(256), 0, st, a);
+  if (a.sinks && a.wide)
+    hipLaunchKernelGGL((gdn2_attn_decode_kernel<CT, D, TK, true, WIDE_WAVES>), dim3(blocks), dim3(64 * WIDE_WAVES), 0,
+                       st, a);
+  else if (a.sinks)
+    hipLaunchKernelGGL((gdn2_attn_decode_kernel<CT, D, TK, true, 4>), dim3(blocks), dim3(256), 0, st, a);
   else
-    hipLaunchKernelGGL((gdn2_attn_decode_kernel<CT, D, TK, false>), dim3(blocks), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((gdn2_attn_decode_kernel<CT, D, TK, false, 4>), dim3(blocks), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 template hipError_t launch_attn_decode<bf16_t, 64>(const fwd_args &, hipStream_t);

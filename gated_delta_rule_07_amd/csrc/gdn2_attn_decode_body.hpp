@@ -25,16 +25,16 @@ __device__ __forceinline__ float group_max(float x) {
 // ("row" order) or 16 (e / 4) + 4g + e % 4 ("acc" order: two accumulators).
 // SINK: keys are numbered without the gap between the sinks and the window, as
 // in gdn2_attn_fwd_kernel, both parts in whole 16-key tiles.
-template <typename CT, int D, int TK, bool SINK> struct decode_body {
+template <typename CT, int D, int TK, bool SINK, int WAVES = 4> struct decode_body {
   static constexpr bool F8 = sizeof(CT) == 1;
   typedef bf16_t IO;
   typedef typename std::conditional<F8, tile8<IO, D>, tile<IO, D>>::type KV;
-  static constexpr int WN = 4, SN = 16 * TK, BN = SN * WN;
+  static constexpr int WN = WAVES, SN = 16 * TK, BN = SN * WN;
   static constexpr int ROWB = KV::ROWB, TILEB = SN * ROWB, LV = 16 * ROWB / 1024;  // loads of a 16-key tile of V
   static constexpr int LK = LV, NK = D / 32;                  // of K; products along the channels
   static constexpr int OLD = D + 4, JOIN = WN * 16 * (OLD * 4 + 8);
   static constexpr int LDSB = WN * TILEB > JOIN ? WN * TILEB : JOIN, SCALESB = F8 ? 2 * WN * SN * 4 : 0;
-  static constexpr int THREADS = 256, BYTES = LDSB + SCALESB;
+  static constexpr int THREADS = 64 * WN, BYTES = LDSB + SCALESB;
 
   // One workgroup's part of a call; lds: BYTES of its shared memory.
   static __device__ __forceinline__ void run(const fwd_args &a, int block, char *const lds) {

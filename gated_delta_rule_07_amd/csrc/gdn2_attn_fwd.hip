@@ -136,42 +136,58 @@ bool decode_rows(const attn_sizes &z) {
   return !z.packed && static_cast<long long>(z.T) * (z.Hq / z.Hk) <= 16;
 }
 
-// Parts along the keys of a paged call: enough workgroups that sequences of
-// different lengths even out over the CUs, no part of the longest possible
-// sequence under 128 keys, at most 128 parts.  (Decode of 64 sequences x 4 kv
-// heads: 136 us at 2048 workgroups, 151 at 1024 and 512; one 1024-token chunk
-// among 23 tokens: 113 us at 768, 125 at 1024, 137 at 2048, where its parts'
-// outputs weigh more.)
 // With sinks, decode's sequences are about as long as their window and sinks,
 // so the parts are chosen for whole rounds over the chip: a round takes its
 // tiles of 128 keys and about three more to begin and end, the join about two.
 // (Window 2048, 4 sinks, 16 heads on 4, e4m3: 64 sequences 32 us with 2 or 3
 // parts, 43 with 8; 200 sequences 93 with 3, 104 with one, 117 with 8; 16
-// sequences 17 with 6 or 9, 25 with 2.)
-static int sink_splits(const attn_sizes &z, long long blocks) {
-  const long long slots = decode_rows(z) ? 768 : 512;
+// sequences 17 with 6 or 9, 25 with 2.)  In bfloat16, workgroups of 12 waves (one a
+// CU, tiles of 384 keys) need no parts and no join, where one round of them is
+// enough.  (Window 500, 8 to 64 sequences: 11 to 14 us, in parts 14 to 16; window
+// 2048, 64 sequences 31 and 35, 32 sequences 23 and 23, 16 sequences over a bfloat16
+// cache 31 and 23, 100 sequences 52 and 47.)
+struct sink_plan {
+  int parts;
+  bool wide;
+};
+static sink_plan plan_sinks(const attn_sizes &z, long long blocks) {
+  const bool dec = decode_rows(z);
+  const long long slots = dec ? 768 : 512;
   long long keys = static_cast<long long>(z.window) + z.sinks + 30 + z.T;
   keys = keys < z.max_keys ? keys : z.max_keys;
   const long long tiles = (keys + 127) / 128;
-  long long best = 1, least = (blocks + slots - 1) / slots * (tiles + 3);
+  sink_plan p = {1, false};
+  long long least = (blocks + slots - 1) / slots * (tiles + 3);
   for (long long s = 2; s <= tiles && s <= 128; ++s) {
     const long long per = (tiles + s - 1) / s;
     const long long cost = (blocks * s + slots - 1) / slots * (per + 3) + 2;
     // (a part without keys is one too many)
     if (cost < least && (s - 1) * per < tiles) {
       least = cost;
-      best = s;
+      p.parts = static_cast<int>(s);
     }
   }
-  return static_cast<int>(best);
+  p.wide = dec && blocks <= 256 && (tiles + 2) / 3 + 3 < least;
+  return p;
 }
-int attn_paged_splits(const attn_sizes &z) {
+static long long paged_blocks(const attn_sizes &z) {
   order od;
+  plan_tiles(z, z.Hq / z.Hk, few_rows(z) ? 32 : 128, od);
+  return static_cast<long long>(od.units) * od.tiles;
+}
+bool attn_decode_wide(const attn_sizes &z) { return z.sinks && decode_rows(z) && plan_sinks(z, paged_blocks(z)).wide; }
+
+// Parts along the keys of a paged call: enough workgroups that sequences of
+// different lengths even out over the CUs, no part of the longest possible
+// sequence under 128 keys, at most 128 parts.  (Decode of 64 sequences x 4 kv
+// heads: 136 us at 2048 workgroups, 151 at 1024 and 512; one 1024-token chunk
+// among 23 tokens: 113 us at 768, 125 at 1024, 137 at 2048, where its parts'
+// outputs weigh more.)
+int attn_paged_splits(const attn_sizes &z) {
   const bool few = few_rows(z);
-  plan_tiles(z, z.Hq / z.Hk, few ? 32 : 128, od);
-  const long long blocks = static_cast<long long>(od.units) * od.tiles;
+  const long long blocks = paged_blocks(z);
   if (z.sinks && few)
-    return sink_splits(z, blocks);
+    return plan_sinks(z, blocks).parts;
   long long keys = z.max_keys;
   if (z.window > 0 && keys > z.window + z.sinks + 128LL)
     keys = z.window + z.sinks + 128LL;
@@ -202,6 +218,7 @@ template <typename IO, typename CT, int D> hipError_t launch_paged(fwd_args &a, 
   if constexpr (sizeof(IO) == 2) {
     if (decode_rows(z)) {
       plan_tiles(z, a.G, 16, a.od);
+      a.wide = attn_decode_wide(z);
       return launch_attn_decode<CT, D>(a, st);
     }
   }

@@ -31,7 +31,9 @@ struct fwd_args {
   const int32_t *groups;
   int ngroups, seqs, tq, prefix_parts;
   bool mark;
+  bool wide;  // decode: WIDE_WAVES waves a workgroup and no parts, where they serve the call best
 };
+constexpr int WIDE_WAVES = 12;
 
 // The first token of group i, whatever groups and cu hold.
 __device__ __forceinline__ int group_start(const fwd_args &a, int i) {

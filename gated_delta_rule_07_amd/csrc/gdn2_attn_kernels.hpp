@@ -43,6 +43,9 @@ template <typename IO, int D> hipError_t launch_attn_fwd(const attn_sizes &z, co
 // ws, [splits, Ttot, Hq, D] and [splits, Ttot, Hq] float32, and the join
 // writes o and lse
 int attn_paged_splits(const attn_sizes &z);
+// Whether a bfloat16 call takes wide workgroups instead (splits 1, whatever
+// attn_paged_splits says).
+bool attn_decode_wide(const attn_sizes &z);
 template <typename IO, typename CT, int D>
 hipError_t launch_attn_paged(const attn_sizes &z, const attn_ptrs &p, int splits, void *ws, hipStream_t st);
 // A shared-prefix call's prefixes: the groups' tables, lengths and (nullptr: one

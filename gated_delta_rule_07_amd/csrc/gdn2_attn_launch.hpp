@@ -53,7 +53,7 @@ inline void fill(fwd_args &a, const attn_sizes &z, const attn_ptrs &p) {
   a.c = z.scale * LOG2E;
   a.groups = nullptr;
   a.ngroups = a.seqs = a.tq = a.prefix_parts = 0;
-  a.mark = false;
+  a.mark = a.wide = false;
 }
 
 // Where part s of a call's parts lies in ws: [parts, Ttot, Hq, D] outputs, then

@@ -495,3 +495,25 @@ def test_sinks_decode_in_a_graph(g, f8):
             if lens[i] <= c.lk[i]:
                 check_rows(outs[0][i], lses[0][i], q[i], c.rows[i][0][:n], c.rows[i][1][:n], window, sinks, BF16, d,
                            f"step {t} sequence {i}", f8)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("f8", [False, True])
+def test_sinks_decode_workgroups(g, f8, d):
+    """Decode's workgroups of 12 waves, of 4 with keys in parts, and of 4 where there are many sequences."""
+    Hk, page = 2, 32
+    for N, T, top, window, sinks in ((6, 1, 900, 500, 4), (6, 2, 400, 30, 37), (3, 1, 4000, 2000, 20), (3, 4, 3000, 1500, 5),
+                                     (140, 1, 300, 64, 5), (140, 3, 200, 130, 40)):
+        print(f"sinks decode N={N} T={T} window={window} sinks={sinks} d={d} f8={f8}", flush=True)
+        lk = [max(0, top - 37 * n % (top + 1)) for n in range(N)]
+        lk[1] = 0
+        c = Paged(g, lk, Hk, d, page, BF16, f8, seed=N + T)
+        c.poison(c.spare)
+        for i, n in enumerate(lk):
+            c.table[i, -(-sinks // page):max(0, n - T + 1 - window) // page] = c.spare
+        q = randn(N, (N, T, 4 * Hk, d), BF16)
+        assert (g.attn_paged_workspace_bytes(q, c.k, c.table, None, window, sinks) > 0) == (window > 200)
+        o, lse = g.attn_paged(q, *c.args(), window=window, sinks=sinks, want_lse=True, **c.scales())
+        torch.cuda.synchronize()
+        for i, n in enumerate(lk):
+            check_rows(o[i], lse[i], q[i], *c.rows[i], window, sinks, BF16, d, f"keys {n}", f8)
