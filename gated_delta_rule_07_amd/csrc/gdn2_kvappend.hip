@@ -11,9 +11,9 @@
 // D / 8 lanes a head (q's, then k's, then v's), as in gdn2_rope_fwd_kernel, so
 // that the sines and cosines are formed once a token and a row's sum and
 // largest magnitude take 3 or 4 lane exchanges.  Measured, 32768 tokens x (16 + 4 +
-// 4) heads, d = 128, bfloat16: into e4m3 84 us (370 MB, 4.4 TB/s; the two calls it
-// stands for 88), into bfloat16 81 us (403 MB, 5 TB/s); a large copy runs at 4.7
-// TB/s.  32 tokens (a decode step): 4.6 us, a launch's own latency.
+// 4) heads, d = 128, bfloat16: into e4m3 81 us (370 MB, 4.6 TB/s; the two calls it
+// stands for 88), into bfloat16 80 us (403 MB, 5 TB/s); a large copy runs at 4.7
+// TB/s.  32 tokens (a decode step): 4.2 us, a launch's own latency.
 #include "gdn2_kvrow.hpp"
 #include "gdn2_rope.hpp"
 
