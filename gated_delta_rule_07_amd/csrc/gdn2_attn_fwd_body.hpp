@@ -191,12 +191,14 @@ template <typename IO, typename CT, int D, int WM, int WN, int KT, bool PAGED, f
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
         int j = kb + sr0 + ROWS_PER_I * i;
-        j = j < k1 ? j : k1 - 1;
+        const bool in = j < k1;
+        j = in ? j : k1 - 1;
         if constexpr (PAGED) {
           j = key_of(j);
-          // (an entry outside the cache stands for zeros, see store_tile)
+          // (an entry outside the cache stands for zeros, see store_tile; so do a
+          // prefix's rows behind the last key, whose weights are 0 for every row)
           const bool ok = static_cast<unsigned>(ent[i]) < static_cast<unsigned>(a.num_pages);
-          bad |= ok ? 0 : 1 << i;
+          bad |= ok && (in || !PREFIX) ? 0 : 1 << i;
           const size_t off = (((static_cast<size_t>(ok ? ent[i] : 0) * a.Hk + hk) << a.page_shift) + (j & pmask)) * D +
                              sc * VPC;
           if constexpr (DMA) {
@@ -470,7 +472,7 @@ template <typename IO, typename CT, int D, int WM, int WN, int KT, bool PAGED, f
           const frag8<IO> p = pack8<IO>(s[g / PER / 2], g / PER & 1);
 #pragma unroll
           for (int x = 0; x < GV; ++x) {
-            if (masked)
+            if (!PREFIX && masked)
               odd |= drop_nonfinite(vf[g & 1][x]);
             mma(o[g % PER * GV + x], vf[g & 1][x], p);
           }
@@ -479,8 +481,8 @@ template <typename IO, typename CT, int D, int WM, int WN, int KT, bool PAGED, f
       }
       // 0 times an infinity would reach rows that do not see its key: in a
       // masked tile such values are left out of the product above and added
-      // here for the rows that do see them.
-      if (masked && __any(odd)) {
+      // here for the rows that do see them.  (A prefix's keys are seen by all rows.)
+      if (!PREFIX && masked && __any(odd)) {
         for (int j = 0; j < 32 * KT; ++j) {
           float p = 0.f;  // weight of key j, kept by half (j / 4) % 2
 #pragma unroll
