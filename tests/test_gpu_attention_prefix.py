@@ -427,3 +427,37 @@ def test_prefix_scale_and_defaults(g):
     o3, none = g.attn_paged_prefix(q, c.c.k, c.c.v, c.prefix_table, c.prefix_lens, c.table, c.lens, scale=0.3)
     assert none is None and torch.equal(o2, o3)
     assert (o2 - o).abs().max() < 1e-5 and (lse2 - lse).abs().max() < 1e-5
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("N", [3, 40])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefix_ends_inside_pages(g, d, N, f8, dtype):
+    """Prefixes that end inside a tile and a page, of every page size and shape of the
+    rows: what the page holds behind the last key does not reach a row, and an infinite
+    value of the last key reaches all of its group's."""
+    for page, pre in ((16, [70, 1, 250]), (32, [33, 520, 31]), (256, [65, 300, 1030])):
+        c = Call(g, pre, [0, N // 3, N - 1, N], [1] * N, [n % 7 for n in range(N)], 8, 2, d, page, dtype, f8, seed=page + N)
+        c.check(*c.run(g))
+        for m, n in enumerate(pre):
+            slot, end = int(c.c.slots(m, n)[-1]), n % page
+            p = slot // page
+            if end:
+                if f8:
+                    c.c.ks[p, :, end:], c.c.vs[p, :, end:] = 255, 255
+                else:
+                    c.c.k[p, :, end:], c.c.v[p, :, end:] = math.nan, math.nan
+        o0, lse0 = c.run(g)
+        c.check(o0, lse0)
+        if not f8:
+            p = int(c.c.slots(1, pre[1])[-1])
+            c.c.v[p // page, 1, p % page, 3] = math.inf
+            o, lse = c.run(g)
+            t0, t1 = N // 3, N - 1
+            assert torch.equal(lse, lse0) and torch.equal(o[:t0], o0[:t0]) and torch.equal(o[t1:], o0[t1:])
+            # (a sequence without own keys has its token at position -1: it sees nothing)
+            seen = [math.inf if n % 7 else 0. for n in range(t0, t1)]
+            assert (o[t0:t1, 0, 4:, 3] == torch.tensor(seen, device="cuda")[:, None]).all(), (page, d)
+            o[t0:t1, :, 4:, 3] = o0[t0:t1, :, 4:, 3]
+            assert torch.equal(o, o0), (page, d)
