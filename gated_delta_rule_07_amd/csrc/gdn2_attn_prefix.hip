@@ -12,10 +12,11 @@
 // tile a workgroup has under way, the own keys' by memory, so one launch has the
 // workgroups of both and a CU works on one of either kind at a time.  Measured,
 // 64 sequences behind 32768 keys with up to 1500 of their own, 16 heads on 4, d =
-// 128, bfloat16 (17.6 GFLOP, 169 MB: 36 us at a large copy's rate), caches cold: 53 us
-// and 7 for the join; the prefix alone 45, the own keys alone 27.  41 sequences in
-// three groups, one of 200 new tokens, e4m3: 45 and 8 (in two launches 62, 23 and
-// 12; 45 of the 62 without the codes widened before shared memory).
+// 128, bfloat16 (17.6 GFLOP, 169 MB: 36 us at a large copy's rate), caches cold: 51 us
+// and 7 for the join; the prefix alone 36, the own keys alone 29.  41 sequences in
+// three groups, one of 200 new tokens, e4m3: 44 and 8, the prefixes alone 38 (in
+// two launches the prefixes' took 45 us, and 62 with the codes widened behind
+// shared memory).
 #include "gdn2_attn_decode_body.hpp"
 #include "gdn2_attn_launch.hpp"
 
@@ -51,10 +52,10 @@ static attn_sizes prefix_sizes(const attn_sizes &z, const prefix_call &x) {
 // may not be there), the own keys' the other twice over; no part of the longest
 // possible sequence under 128 keys, at most 128 parts.  More parts cost the
 // join, fewer leave CUs without products.  Measured, us with the join, 16 heads
-// on 4, d = 128, prefix of 32768 keys, up to 1500 own: 64 sequences 48 (32 parts)
-// against 65, 54 and 60 with 16, 48 and 64; 256 sequences 160 (8 parts) against
-// 178 with 16 and 221 with 64; three groups, 240 rows a head, 9000 keys: 51 with
-// 12, 57 with 6, 60 with 24.
+// on 4, d = 128, prefix of 32768 keys, up to 1500 own: 64 sequences 58 (32 parts)
+// against 59, 63 and 68 with 24, 48 and 64; 256 sequences 149 (8 parts) against
+// 162, 158 and 173 with 6, 12 and 16; three groups, 960 rows a kv head, 9000 keys:
+// 51 with 9 and 12, 54 with 6, 57 with 19.
 static int at_most(long long s, long long keys) {
   if (s > keys / 128)
     s = keys / 128;
