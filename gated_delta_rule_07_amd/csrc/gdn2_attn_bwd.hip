@@ -33,7 +33,9 @@ struct bwd_args {
   int N, T, Ttot, Hq, Hk, G, window;
   int sinks;         // first keys visible behind the window (0: none, or no window)
   int far_parts;     // workgroups that share the rows which see a sink from behind the window
-  float *far_sums;   // sinks > 0: [far_parts, 2, N, sinks, Hk, D], their sums of dk / scale and dv
+  float *far_sums;   // sinks > 0: [far_parts, 2, far_rows, Hk, D], their sums of dk / scale and dv
+  size_t far_rows;   // a row for every sink of every sequence, or (far_by_token) for every token
+  bool far_by_token;
   float c, scale;
   int gs;            // heads of a row tile of the dk, dv kernel
   int parts;         // workgroups that share a key tile's rows (dk, dv kernel)
@@ -304,9 +306,9 @@ template <typename IO, int D> __device__ __forceinline__ int far_parts_of(const 
   return n ? (n + per - 1) / per : 0;
 }
 template <int D>
-__device__ __forceinline__ float *far_sum(const bwd_args &a, int part, bool is_v, int n, int key, int hk) {
-  return a.far_sums +
-         (((static_cast<size_t>(2 * part + (is_v ? 1 : 0)) * a.N + n) * a.sinks + key) * a.Hk + hk) * D;
+__device__ __forceinline__ float *far_sum(const bwd_args &a, int part, bool is_v, const span &sq, int key, int hk) {
+  const size_t row = (a.far_by_token ? sq.start : static_cast<size_t>(sq.n) * a.sinks) + key;
+  return a.far_sums + ((static_cast<size_t>(2 * part + (is_v ? 1 : 0)) * a.far_rows + row) * a.Hk + hk) * D;
 }
 template <typename IO, int D, int WK, int WR, dkv_mode M>
 __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1)) gdn2_attn_dkv_kernel(bwd_args a) {
@@ -451,8 +453,8 @@ __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1))
     if (part == 0 && key < a.sinks && key < last_key) {
       const int np = far_parts_of<IO, D>(a, sq.len, key);
       for (int p = wrow; p < np; p += WR) {
-        const float *const sk = far_sum<D>(a, p, false, sq.n, key, hk) + 4 * h;
-        const float *const sv = far_sum<D>(a, p, true, sq.n, key, hk) + 4 * h;
+        const float *const sk = far_sum<D>(a, p, false, sq, key, hk) + 4 * h;
+        const float *const sv = far_sum<D>(a, p, true, sq, key, hk) + 4 * h;
 #pragma unroll
         for (int n = 0; n < D / 32; ++n)
 #pragma unroll
@@ -590,7 +592,7 @@ __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1))
     const size_t at = (static_cast<size_t>(sq.start + key) * a.Hk + hk) * D + 4 * h;
     const bool is_v = wrow != 0;
     if constexpr (M == DKV_FAR) {
-      float *const sums = far_sum<D>(a, part, is_v, sq.n, key, hk) + 4 * h;
+      float *const sums = far_sum<D>(a, part, is_v, sq, key, hk) + 4 * h;
 #pragma unroll
       for (int n = 0; n < D / 32; ++n)
 #pragma unroll
@@ -741,6 +743,8 @@ static void fill(bwd_args &a, const attn_sizes &z, const attn_ptrs &p, void *ws,
   a.part_sums = a.parts > 1 ? reinterpret_cast<float *>(static_cast<char *>(ws) + attn_bwd_stat_bytes(z)) : nullptr;
   a.sinks = z.sinks;
   a.far_parts = z.sinks ? attn_bwd_far_parts(z) : 0;
+  a.far_rows = attn_bwd_far_rows(z);
+  a.far_by_token = attn_bwd_far_by_token(z);
   a.far_sums = z.sinks ? reinterpret_cast<float *>(static_cast<char *>(ws) + attn_bwd_bytes(z, d)) : nullptr;
   a.gs = a.G < 32 ? a.G : 32;
   while (a.G % a.gs)

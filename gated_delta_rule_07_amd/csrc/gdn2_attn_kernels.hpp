@@ -78,8 +78,14 @@ hipError_t launch_attn_bwd_dq(const attn_sizes &z, const attn_ptrs &p, void *ws,
 // that see them from behind the window, which launch_attn_bwd_dkv adds; they
 // follow in ws.
 int attn_bwd_far_parts(const attn_sizes &z);
+// Where the sequences' sinks are more than the call's tokens (packed sequences,
+// most of them shorter), a part has a row for every token, else for every sink.
+inline bool attn_bwd_far_by_token(const attn_sizes &z) { return static_cast<long long>(z.N) * z.sinks > z.Ttot; }
+inline size_t attn_bwd_far_rows(const attn_sizes &z) {
+  return attn_bwd_far_by_token(z) ? static_cast<size_t>(z.Ttot) : static_cast<size_t>(z.N) * z.sinks;
+}
 inline size_t attn_bwd_far_bytes(const attn_sizes &z, int d) {
-  return z.sinks ? static_cast<size_t>(attn_bwd_far_parts(z)) * 2 * z.N * z.sinks * z.Hk * d * 4 : 0;
+  return z.sinks ? static_cast<size_t>(attn_bwd_far_parts(z)) * 2 * attn_bwd_far_rows(z) * z.Hk * d * 4 : 0;
 }
 template <typename IO, int D>
 hipError_t launch_attn_bwd_far(const attn_sizes &z, const attn_ptrs &p, void *ws, hipStream_t st);
