@@ -262,7 +262,7 @@ def attn_bwd_workspace_bytes(B: int, T: int, Hq: int, Hk: int, d: int, dtype: to
                              sinks: int = 0, num_seqs: int = 0) -> int:
     """Bytes of workspace ``attn_bwd`` needs (B = 1 and the total T when
     packed, with sinks also ``num_seqs``; the same for either dtype and any
-    window)."""
+    window; one that hides nothing needs no more than with ``sinks`` 0)."""
     return int(lib().gdn2_attn_sink_bwd_workspace_bytes(B, T, Hq, Hk, d, num_seqs, _sinks(sinks)))
 
 
@@ -284,7 +284,11 @@ def attn_bwd(q, k, v, o, lse, dout, cu_seqlens=None, window: int = 0, scale: flo
             out[name] = torch.empty_like(like)
         _like(out[name], name, like.shape, q.dtype)
     _device(q, *out.values())
-    need = 0 if workspace is not None else attn_bwd_workspace_bytes(B, T, Hq, Hk, d, q.dtype, sinks, ns)
+    need = 0
+    if workspace is None:
+        # (sinks have no part in a call whose window hides nothing: any number goes, and needs no room)
+        hides = 0 < window and window + sinks < T
+        need = attn_bwd_workspace_bytes(B, T, Hq, Hk, d, q.dtype, sinks if hides else 0, ns)
     ws, ws_bytes = _workspace(workspace, need, dev)
     _call(dev, lib().gdn2_attn_sink_bwd, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(cu_seqlens), B, T,
           Hq, Hk, d, ns, window, sinks, d ** -0.5 if scale is None else scale, _dtype_code(q), _ptr(out["dq"]),

@@ -607,7 +607,9 @@ gdn2_status_t gdn2_attn_sink_fwd(const void *q, const void *k, const void *v, co
                                  gdn2_dtype_t dt, void *o, float *lse, void *stream);
 
 /* Bytes of workspace gdn2_attn_sink_bwd needs with any window (num_seqs 0: B
- * sequences of T tokens; else packed, B = 1 and T tokens in all). */
+ * sequences of T tokens; else packed, B = 1 and T tokens in all); 0 for sizes
+ * that a window which hides anything is refused for.  A call whose window hides
+ * nothing needs gdn2_attn_bwd_workspace_bytes, whatever its sinks. */
 size_t gdn2_attn_sink_bwd_workspace_bytes(int B, int T, int Hq, int Hk, int d, int num_seqs, int sinks);
 
 gdn2_status_t gdn2_attn_sink_bwd(const void *q, const void *k, const void *v, const void *o, const float *lse,

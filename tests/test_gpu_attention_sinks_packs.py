@@ -32,3 +32,20 @@ def test_workspace_of_more_sinks_than_tokens(g):
     big = torch.full((2 * need,), 0xff, dtype=torch.uint8, device="cuda")
     again = g.attn_bwd(q, k, v, o, lse, do, workspace=big, **kw)
     assert all(torch.equal(got[n], again[n]) for n in ("dq", "dk", "dv"))
+
+
+@pytest.mark.parametrize("window", [0, 1024, 5000])
+def test_sinks_where_the_window_hides_nothing(g, window):
+    """Sinks have no part then, also where a window that hides would be refused for their number
+    (2^23 sequence-heads times 32 sinks): the backward finds its own workspace."""
+    N, T, Hk, d, sinks = 1 << 16, 2048, 8, 64, 1024
+    print(f"sinks that hide nothing window={window}", flush=True)
+    assert g.attn_bwd_workspace_bytes(1, T, Hk, Hk, d, BF16, sinks=sinks, num_seqs=N) == 0
+    cu = torch.full((N + 1,), T, dtype=torch.int32, device="cuda")
+    cu[:3] = torch.tensor([0, 1500, 1503], dtype=torch.int32, device="cuda")
+    q, k, v, do = (randn(80 + i, (1, T, Hk, d), BF16) for i in range(4))
+    o, lse = g.attn_fwd(q, k, v, cu, window=window, sinks=sinks)
+    o0, lse0 = g.attn_fwd(q, k, v, cu)
+    assert torch.equal(o, o0) and torch.equal(lse, lse0)
+    got, want = g.attn_bwd(q, k, v, o, lse, do, cu, window=window, sinks=sinks), g.attn_bwd(q, k, v, o, lse, do, cu)
+    assert all(torch.equal(got[n], want[n]) for n in ("dq", "dk", "dv"))
