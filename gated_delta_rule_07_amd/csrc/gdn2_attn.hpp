@@ -17,6 +17,7 @@
 #pragma once
 
 #include "gdn2_attn_kernels.hpp"
+#include "gdn2_attn_order.hpp"
 #include "gdn2_device.hpp"
 
 namespace gdn2 {
@@ -326,35 +327,6 @@ __device__ __forceinline__ span packed_span(const int32_t *cu, int n, int T) {
   return clamped_span(n, cu[n], cu[n + 1], T);
 }
 
-// Workgroup order.  Consecutive workgroups go to the 8 dies in turn, each
-// with its own L2: the tiles of one unit (a sequence's kv head, which reads
-// the same keys and values) are kept on one die, or, with fewer than 8 (or
-// an odd number of) units, dealt out over 8 / gcd dies.  Later tiles see more
-// keys, so each die starts with its last ones.  A unit of fewer tiles than 8 / gcd
-// leaves dies without work: units that are no multiple of 8 and have few tiles
-// run on a part of the chip (decode of 2048 keys each, e4m3: 1024 sequences on one kv
-// head 106 us, 1025 452; 172 sequences on three kv heads 71, 171 240).
-struct order {
-  int units, tiles, g, tpr;  // g = gcd(units, 8), tpr = ceil(tiles / (8 / g))
-};
-__device__ __forceinline__ bool place(const order &od, int id, int &unit, int &tile_i) {
-  const int x = id & 7, idx = id >> 3, r = 8 / od.g;
-  const int u = idx / od.tpr, t = (od.tpr - 1 - idx % od.tpr) * r + x / od.g;
-  unit = u * od.g + x % od.g;
-  tile_i = t;
-  return unit < od.units && t < od.tiles;
-}
-// Fills the order of tiles of BM rows (GR rows a token) and returns the
-// number of workgroups.
-inline unsigned plan_tiles(const attn_sizes &z, int GR, int BM, order &od) {
-  const long long rows = static_cast<long long>(z.T) * GR;
-  od.tiles = static_cast<int>(z.packed ? rows / BM + z.N : (rows + BM - 1) / BM);
-  od.units = z.packed ? z.Hk : z.N * z.Hk;
-  od.g = od.units % 8 == 0 ? 8 : od.units % 4 == 0 ? 4 : od.units % 2 == 0 ? 2 : 1;
-  const int r = 8 / od.g;
-  od.tpr = (od.tiles + r - 1) / r;
-  return 8u * static_cast<unsigned>(od.units / od.g) * static_cast<unsigned>(od.tpr);
-}
 // Fewer 128-row tiles than CUs: such calls take 32-row tiles whose keys the
 // waves split.  (float32, 5 sequences, 1543 tokens, 4 heads: 54 tiles, forward
 // and backward 118 us with 128 rows, 69 with 32; bfloat16, 11 sequences, 9973

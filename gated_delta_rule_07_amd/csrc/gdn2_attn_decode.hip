@@ -34,7 +34,7 @@ template <typename CT, int D> hipError_t launch_attn_decode(const fwd_args &a, h
   // (32 keys a wave and tile; 64 of e4m3 leave two waves a SIMD: 166 against
   // 136 us for 64 sequences of 4K to 16K keys)
   constexpr int TK = 2;
-  const unsigned blocks = 8u * static_cast<unsigned>(a.od.units / a.od.g) * static_cast<unsigned>(a.od.tpr) * a.splits;
+  const unsigned blocks = workgroups(a.od) * a.splits;
   if (a.sinks && a.wide)
     hipLaunchKernelGGL((gdn2_attn_decode_kernel<CT, D, TK, true, WIDE_WAVES>), dim3(blocks), dim3(64 * WIDE_WAVES), 0,
                        st, a);
