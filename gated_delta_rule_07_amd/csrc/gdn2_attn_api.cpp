@@ -290,6 +290,9 @@ gdn2_status_t check_prefix(const char *fn, int B, int T, int Hq, int Hk, int d, 
     return fail(GDN2_ERR_UNSUPPORTED, "%s: at most 2^28 keys a prefix (max_prefix_pages=%d)", fn, max_prefix_pages);
   if (static_cast<long long>(num_groups) * Hk > MAX_UNITS)
     return fail(GDN2_ERR_UNSUPPORTED, "%s: too large (at most 2^20 - 1 group-heads)", fn);
+  // (the join always runs, four rows a workgroup of 256 work-items, in 32 bits with the last one filled up)
+  if (static_cast<long long>(z.Ttot) * Hq > MAX_ROWS - 3)
+    return fail(GDN2_ERR_UNSUPPORTED, "%s: too large (at most 2^26 - 4 query rows)", fn);
   x = {};
   x.ngroups = num_groups;
   x.max_pages = max_prefix_pages;

@@ -579,7 +579,8 @@ gdn2_status_t gdn2_attn_paged(const void *q, const void *k_cache, const void *v_
  * cu_seqlens, B, T and num_seqs.  A query at own position i (seq_lens[n] - L ..
  * seq_lens[n] - 1) sees the whole prefix and the sequence's own keys j <= i;
  * one at a negative own position sees nothing.  A sequence before the first
- * or behind the last group has no prefix.  The workspace is always needed. */
+ * or behind the last group has no prefix.  The workspace is always needed.  At
+ * most 2^26 - 4 (token, query head) rows a call. */
 size_t gdn2_attn_paged_prefix_workspace_bytes(int B, int T, int Hq, int Hk, int d, int num_seqs, int num_groups,
                                               int page_size, int max_prefix_pages, int max_pages);
 
