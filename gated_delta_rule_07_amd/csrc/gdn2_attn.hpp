@@ -292,13 +292,14 @@ struct span {
 // the next sequence's first slot, so no table is needed.  One wave finds the
 // last n whose first slot is <= s, 64 candidates a step.  Every wave of the
 // workgroup calls this with the same arguments.
-// first(i): cu[i].
-template <typename F> __device__ __forceinline__ int find_seq_by(F first, int N, int G, int BM, long s, int lane) {
+// holds(i): true for the numbers up to one, and false behind it; the last one of
+// 0 .. N - 1 (0 if there is none).
+template <typename P> __device__ __forceinline__ int find_last(P holds, int N, int lane) {
   int lo = 0, cnt = N;  // the answer lies in [lo, lo + cnt)
   while (cnt > 1) {
     const int step = (cnt + 63) / 64;
     const int i = lo + lane * step;
-    const bool le = i < lo + cnt && static_cast<long>(first(i)) * G / BM + i <= s;
+    const bool le = i < lo + cnt && holds(i);
     const unsigned long long m = __ballot(le);
     const int last = m ? 63 - __builtin_clzll(m) : 0;
     const int end = lo + cnt;
@@ -306,6 +307,10 @@ template <typename F> __device__ __forceinline__ int find_seq_by(F first, int N,
     cnt = step < end - lo ? step : end - lo;
   }
   return lo;
+}
+// first(i): cu[i].
+template <typename F> __device__ __forceinline__ int find_seq_by(F first, int N, int G, int BM, long s, int lane) {
+  return find_last([=](int i) { return static_cast<long>(first(i)) * G / BM + i <= s; }, N, lane);
 }
 
 __device__ __forceinline__ int find_seq(const int32_t *cu, int N, int G, int BM, long s, int lane) {

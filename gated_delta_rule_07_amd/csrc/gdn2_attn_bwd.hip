@@ -32,8 +32,11 @@ struct bwd_args {
   const int32_t *cu;
   int N, T, Ttot, Hq, Hk, G, window;
   int sinks;         // first keys visible behind the window (0: none, or no window)
-  int far_parts;     // workgroups that share the rows which see a sink from behind the window
-  float *far_sums;   // sinks > 0: [far_parts, 2, far_rows, Hk, D], their sums of dk / scale and dv
+  int far_parts;     // workgroups that share the rows which see a sink from behind the window, a sequence
+  int far_extra;     // packed: so many more, one for every far_step tokens
+  int far_step;
+  float *far_sums;   // sinks > 0: [far_parts, 2, far_rows, Hk, D], their sums of dk / scale and dv, then
+                     // [far_extra, 2, sinks, Hk, D]
   size_t far_rows;   // a row for every sink of every sequence, or (far_by_token) for every token
   bool far_by_token;
   float c, scale;
@@ -300,15 +303,29 @@ __device__ __forceinline__ int far_tiles(const bwd_args &a, int len, int key0, i
   const long n = static_cast<long>(len) - key0 - a.window;
   return n > 0 ? static_cast<int>((n + TB - 1) / TB) * (a.G / a.gs) : 0;
 }
+// The workgroups that share a sequence's far rows: far_parts, and number e of the
+// far_extra where token far_step (e + 1) - 1 of the call is the sequence's, so that a
+// long one among short ones has nearly all of them.
+__device__ __forceinline__ int far_share(const bwd_args &a, const span &sq) {
+  return a.far_parts + (a.far_extra ? (sq.start + sq.len) / a.far_step - sq.start / a.far_step : 0);
+}
 // Parts that hold sums for a sink (their workgroups had rows).
-template <typename IO, int D> __device__ __forceinline__ int far_parts_of(const bwd_args &a, int len, int key) {
-  const int n = far_tiles(a, len, key - key % FAR_KEYS, FAR_ROWS<IO, D> / a.gs), per = (n + a.far_parts - 1) / a.far_parts;
+template <typename IO, int D> __device__ __forceinline__ int far_parts_of(const bwd_args &a, const span &sq, int key) {
+  const int n = far_tiles(a, sq.len, key - key % FAR_KEYS, FAR_ROWS<IO, D> / a.gs), share = far_share(a, sq);
+  const int per = (n + share - 1) / share;
   return n ? (n + per - 1) / per : 0;
 }
 template <int D>
 __device__ __forceinline__ float *far_sum(const bwd_args &a, int part, bool is_v, const span &sq, int key, int hk) {
-  const size_t row = (a.far_by_token ? sq.start : static_cast<size_t>(sq.n) * a.sinks) + key;
-  return a.far_sums + ((static_cast<size_t>(2 * part + (is_v ? 1 : 0)) * a.far_rows + row) * a.Hk + hk) * D;
+  const int v = is_v ? 1 : 0;
+  size_t row;
+  if (part < a.far_parts) {
+    row = (2 * part + v) * a.far_rows + (a.far_by_token ? sq.start : static_cast<size_t>(sq.n) * a.sinks) + key;
+  } else {
+    const int e = sq.start / a.far_step + part - a.far_parts;
+    row = 2 * a.far_parts * a.far_rows + static_cast<size_t>(2 * e + v) * a.sinks + key;
+  }
+  return a.far_sums + (row * a.Hk + hk) * D;
 }
 template <typename IO, int D, int WK, int WR, dkv_mode M>
 __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1)) gdn2_attn_dkv_kernel(bwd_args a) {
@@ -330,22 +347,37 @@ __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1))
   const int wkey = wave % WK, wrow = wave / WK;
   int unit, slot, hk, key0;
   span sq;
-  const int parts = M == DKV_FAR ? a.far_parts : a.parts, part = blockIdx.x % parts;
+  int parts = a.parts, part = blockIdx.x % parts;
   if constexpr (M == DKV_FAR) {
-    // a unit a sequence and kv head, a tile for every 32 sinks
-    const int id = blockIdx.x / parts, tiles = (a.sinks + BK - 1) / BK;
-    unit = id / tiles;
-    sq.n = unit / a.Hk;
-    hk = unit % a.Hk;
-    key0 = id % tiles * BK;
-    if (a.cu) {
-      sq = packed_span(a.cu, sq.n, a.T);
+    // a unit a sequence and kv head, a tile for every 32 sinks; behind all sequences'
+    // parts, those that long sequences have in addition
+    const int tiles = (a.sinks + BK - 1) / BK, block = blockIdx.x, first = a.N * a.Hk * tiles * a.far_parts;
+    if (block < first) {
+      const int id = block / a.far_parts;
+      part = block % a.far_parts;
+      unit = id / tiles;
+      sq.n = unit / a.Hk;
+      hk = unit % a.Hk;
+      key0 = id % tiles * BK;
+      if (a.cu) {
+        sq = packed_span(a.cu, sq.n, a.T);
+      } else {
+        sq.start = sq.n * a.T;
+        sq.len = a.T;
+      }
     } else {
-      sq.start = sq.n * a.T;
-      sq.len = a.T;
+      const int id = (block - first) / a.far_extra, e = (block - first) % a.far_extra;
+      hk = id / tiles;
+      key0 = id % tiles * BK;
+      const int last = e * a.far_step + a.far_step - 1;
+      sq = packed_span(a.cu, find_last([&](int i) { return a.cu[i] <= last; }, a.N, lane), a.T);
+      part = a.far_parts + e - sq.start / a.far_step;
+      if (part < a.far_parts || part >= far_share(a, sq))
+        return;
     }
     if (key0 >= sq.len)
       return;
+    parts = far_share(a, sq);
   } else {
     if (!place(a.od, blockIdx.x / parts, unit, slot) ||
         !locate(a, unit, a.od.tiles - 1 - slot, 1, BK, lane, sq, hk, key0))
@@ -451,7 +483,7 @@ __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1))
   if constexpr (M == DKV_SINK) {
     // a sink's sums over the far rows: part 0's row parts begin with them
     if (part == 0 && key < a.sinks && key < last_key) {
-      const int np = far_parts_of<IO, D>(a, sq.len, key);
+      const int np = far_parts_of<IO, D>(a, sq, key);
       for (int p = wrow; p < np; p += WR) {
         const float *const sk = far_sum<D>(a, p, false, sq, key, hk) + 4 * h;
         const float *const sv = far_sum<D>(a, p, true, sq, key, hk) + 4 * h;
@@ -699,14 +731,22 @@ int attn_bwd_parts(const attn_sizes &z) {
 // 11 packed sequences, 9973 tokens, window 500, 33 sinks, d = 64: 35 for 256, 22
 // and 19 for 512 and 1024; 1543 float32 tokens, 7 sinks: 10.3, and 15.1 for 512
 // rows a workgroup.)
-int attn_bwd_far_parts(const attn_sizes &z) {
-  const long long units = static_cast<long long>(z.N) * z.Hk * ((z.sinks + FAR_KEYS - 1) / FAR_KEYS);
+//
+// Packed sequences may be one long one and many short ones, which leave their parts
+// without rows: what one sequence alone would have in addition (far_extra) is
+// dealt out by the tokens.  (16 heads on 4, d = 128, window 2048, 4 sinks: one of 30000
+// tokens before 255 of 10: 82 us, behind them 60, alone 54, and 2030 with the same parts for
+// all; one of 16384 before 63 of 256: 49, alone 29, and 279.)
+static int far_parts_for(const attn_sizes &z, int N) {
+  const long long units = static_cast<long long>(N) * z.Hk * ((z.sinks + FAR_KEYS - 1) / FAR_KEYS);
   const long long rows = static_cast<long long>(z.T) * (z.Hq / z.Hk);
   long long p = ((z.packed ? 1024 : 256) + units - 1) / units;
   if (p > rows / 128)
     p = rows / 128;
   return p < 1 ? 1 : (p > 64 ? 64 : static_cast<int>(p));
 }
+int attn_bwd_far_parts(const attn_sizes &z) { return far_parts_for(z, z.N); }
+int attn_bwd_far_extra(const attn_sizes &z) { return z.packed ? far_parts_for(z, 1) - far_parts_for(z, z.N) : 0; }
 
 static void fill(bwd_args &a, const attn_sizes &z, const attn_ptrs &p, void *ws, int d) {
   a.q = p.q;
@@ -743,6 +783,8 @@ static void fill(bwd_args &a, const attn_sizes &z, const attn_ptrs &p, void *ws,
   a.part_sums = a.parts > 1 ? reinterpret_cast<float *>(static_cast<char *>(ws) + attn_bwd_stat_bytes(z)) : nullptr;
   a.sinks = z.sinks;
   a.far_parts = z.sinks ? attn_bwd_far_parts(z) : 0;
+  a.far_extra = z.sinks ? attn_bwd_far_extra(z) : 0;
+  a.far_step = a.far_extra ? (z.T + a.far_extra - 1) / a.far_extra : 1;
   a.far_rows = attn_bwd_far_rows(z);
   a.far_by_token = attn_bwd_far_by_token(z);
   a.far_sums = z.sinks ? reinterpret_cast<float *>(static_cast<char *>(ws) + attn_bwd_bytes(z, d)) : nullptr;
@@ -776,7 +818,8 @@ template <typename IO, int D>
 hipError_t launch_attn_bwd_far(const attn_sizes &z, const attn_ptrs &p, void *ws, hipStream_t st) {
   bwd_args a;
   fill(a, z, p, ws, D);
-  const unsigned blocks = static_cast<unsigned>(z.N) * z.Hk * ((z.sinks + FAR_KEYS - 1) / FAR_KEYS) * a.far_parts;
+  const unsigned tiles = static_cast<unsigned>(z.Hk) * ((z.sinks + FAR_KEYS - 1) / FAR_KEYS);
+  const unsigned blocks = tiles * (static_cast<unsigned>(z.N) * a.far_parts + a.far_extra);
   hipLaunchKernelGGL((gdn2_attn_dkv_kernel<IO, D, FAR_KEYS / 32, FAR_ROWS<IO, D> / 32, DKV_FAR>), dim3(blocks),
                      dim3(2 * FAR_ROWS<IO, D>), 0, st, a);
   return hipGetLastError();

@@ -84,8 +84,13 @@ inline bool attn_bwd_far_by_token(const attn_sizes &z) { return static_cast<long
 inline size_t attn_bwd_far_rows(const attn_sizes &z) {
   return attn_bwd_far_by_token(z) ? static_cast<size_t>(z.Ttot) : static_cast<size_t>(z.N) * z.sinks;
 }
+// Packed sequences share as many parts more by their tokens.
+int attn_bwd_far_extra(const attn_sizes &z);
 inline size_t attn_bwd_far_bytes(const attn_sizes &z, int d) {
-  return z.sinks ? static_cast<size_t>(attn_bwd_far_parts(z)) * 2 * attn_bwd_far_rows(z) * z.Hk * d * 4 : 0;
+  if (!z.sinks)
+    return 0;
+  const size_t rows = attn_bwd_far_parts(z) * attn_bwd_far_rows(z) + static_cast<size_t>(attn_bwd_far_extra(z)) * z.sinks;
+  return rows * 2 * z.Hk * d * 4;
 }
 template <typename IO, int D>
 hipError_t launch_attn_bwd_far(const attn_sizes &z, const attn_ptrs &p, void *ws, hipStream_t st);

@@ -49,3 +49,38 @@ def test_sinks_where_the_window_hides_nothing(g, window):
     assert torch.equal(o, o0) and torch.equal(lse, lse0)
     got, want = g.attn_bwd(q, k, v, o, lse, do, cu, window=window, sinks=sinks), g.attn_bwd(q, k, v, o, lse, do, cu)
     assert all(torch.equal(got[n], want[n]) for n in ("dq", "dk", "dv"))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [64, 128])
+def test_long_sequence_among_short_ones(g, d, dtype):
+    """A long sequence's far rows go to more workgroups than its neighbours', wherever it stands."""
+    short = [9, 0, 40, 1, 130, 3] * 10
+    long = 2500 if dtype == BF16 else 1300
+    for lens in ([long] + short, short + [long], short[:31] + [long] + short[31:], [long // 2] + short + [long // 2, 0, 5]):
+        run(g, lens, 8, 2, d, dtype, 100, 4, seed=len(lens), tail=33)
+    # more than 32 sinks, and more of them than tokens
+    run(g, short + [long] + short, 3, 1, d, dtype, 64, 50, seed=5)
+    run(g, [1] * 200 + [long] + short, 4, 2, d, dtype, 37, 40, seed=6, tail=3)
+
+
+def test_long_sequence_among_short_ones_many_heads(g):
+    """Heads of a group in several turns over the tokens (a tile has at most 32 of them)."""
+    run(g, [5, 0, 30] * 20 + [900, 2], 96, 2, 64, BF16, 50, 7, seed=9)
+    run(g, [5, 700] + [8] * 50, 66, 2, 64, BF16, 20, 3, seed=10)
+
+
+def test_long_sequence_workspace_and_bits(g):
+    """The workspace is all that is written, whatever it held before, and runs repeat their bits."""
+    lens, Hq, Hk, d = [4] * 150 + [3000] + [7] * 50, 8, 2, 64
+    T, kw = sum(lens), dict(cu_seqlens=cu_of(lens), window=128, sinks=33)
+    print("long sequence's workspace", flush=True)
+    q, k, v, do = (randn(90 + i, (1, T, h, d), BF16) for i, h in enumerate((Hq, Hk, Hk, Hq)))
+    o, lse = g.attn_fwd(q, k, v, **kw)
+    need = g.attn_bwd_workspace_bytes(1, T, Hq, Hk, d, BF16, sinks=33, num_seqs=len(lens))
+    room = torch.full((need + 4096,), 0xff, dtype=torch.uint8, device="cuda")
+    got = g.attn_bwd(q, k, v, o, lse, do, workspace=room[:need], **kw)
+    assert (room[need:] == 0xff).all()
+    for _ in range(4):
+        again = g.attn_bwd(q, k, v, o, lse, do, workspace=room[:need], **kw)
+        assert all(torch.equal(got[n], again[n]) for n in ("dq", "dk", "dv"))
