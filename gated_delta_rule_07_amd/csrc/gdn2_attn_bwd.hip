@@ -296,6 +296,7 @@ enum dkv_mode { DKV_PLAIN, DKV_SINK, DKV_FAR };
 // Tile of the DKV_FAR launch: 128 rows where two of them fit shared memory
 // beside the keys (64 would pass through registers and spill).
 constexpr int FAR_KEYS = 32;
+constexpr int FAR_TILES = 16;  // of a workgroup beyond a sequence's far_parts
 template <typename IO, int D> constexpr int FAR_ROWS = D * sizeof(IO) <= 256 ? 128 : 64;
 // Tiles of TB tokens of the rows of a sequence of len tokens that see a key
 // from key0 on from behind the window, and how many of them a part takes.
@@ -303,15 +304,22 @@ __device__ __forceinline__ int far_tiles(const bwd_args &a, int len, int key0, i
   const long n = static_cast<long>(len) - key0 - a.window;
   return n > 0 ? static_cast<int>((n + TB - 1) / TB) * (a.G / a.gs) : 0;
 }
-// The workgroups that share a sequence's far rows: far_parts, and number e of the
-// far_extra where token far_step (e + 1) - 1 of the call is the sequence's, so that a
-// long one among short ones has nearly all of them.
-__device__ __forceinline__ int far_share(const bwd_args &a, const span &sq) {
-  return a.far_parts + (a.far_extra ? (sq.start + sq.len) / a.far_step - sq.start / a.far_step : 0);
+// The workgroups that share the n far tiles of a sequence's keys: far_parts, and
+// number e of the far_extra where token far_step (e + 1) - 1 of the call is the
+// sequence's, so that a long one among short ones has nearly all of them; but those
+// only while a workgroup has FAR_TILES, since the keys' owner adds the parts one by one.
+__device__ __forceinline__ int far_share(const bwd_args &a, const span &sq, int n) {
+  int share = a.far_parts;
+  if (a.far_extra) {
+    const int more = share + (sq.start + sq.len) / a.far_step - sq.start / a.far_step, most = (n + FAR_TILES - 1) / FAR_TILES;
+    const int x = more < most ? more : most;
+    share = x > share ? x : share;
+  }
+  return share;
 }
 // Parts that hold sums for a sink (their workgroups had rows).
 template <typename IO, int D> __device__ __forceinline__ int far_parts_of(const bwd_args &a, const span &sq, int key) {
-  const int n = far_tiles(a, sq.len, key - key % FAR_KEYS, FAR_ROWS<IO, D> / a.gs), share = far_share(a, sq);
+  const int n = far_tiles(a, sq.len, key - key % FAR_KEYS, FAR_ROWS<IO, D> / a.gs), share = far_share(a, sq, n);
   const int per = (n + share - 1) / share;
   return n ? (n + per - 1) / per : 0;
 }
@@ -372,12 +380,14 @@ __global__ void __launch_bounds__(64 * WK * WR, (D * sizeof(IO) <= 256 ? 2 : 1))
       const int last = e * a.far_step + a.far_step - 1;
       sq = packed_span(a.cu, find_last([&](int i) { return a.cu[i] <= last; }, a.N, lane), a.T);
       part = a.far_parts + e - sq.start / a.far_step;
-      if (part < a.far_parts || part >= far_share(a, sq))
+      if (part < a.far_parts)
         return;
     }
     if (key0 >= sq.len)
       return;
-    parts = far_share(a, sq);
+    parts = far_share(a, sq, far_tiles(a, sq.len, key0, BQ / a.gs));
+    if (part >= parts)
+      return;
   } else {
     if (!place(a.od, blockIdx.x / parts, unit, slot) ||
         !locate(a, unit, a.od.tiles - 1 - slot, 1, BK, lane, sq, hk, key0))
@@ -735,8 +745,9 @@ int attn_bwd_parts(const attn_sizes &z) {
 // Packed sequences may be one long one and many short ones, which leave their parts
 // without rows: what one sequence alone would have in addition (far_extra) is
 // dealt out by the tokens.  (16 heads on 4, d = 128, window 2048, 4 sinks: one of 30000
-// tokens before 255 of 10: 82 us, behind them 60, alone 54, and 2030 with the same parts for
-// all; one of 16384 before 63 of 256: 49, alone 29, and 279.)
+// tokens before 255 of 10: 82 to 87 us, behind them 60 to 63, alone 54, and 2030 with the same parts for
+// all; one of 16384 before 63 of 256: 49 to 53, alone 29, and 279.  All of them whatever the rows: 6
+// sequences of up to 2833 tokens, 163 sinks, 2 heads on one, d = 64: dk and dv 50, not 30.)
 static int far_parts_for(const attn_sizes &z, int N) {
   const long long units = static_cast<long long>(N) * z.Hk * ((z.sinks + FAR_KEYS - 1) / FAR_KEYS);
   const long long rows = static_cast<long long>(z.T) * (z.Hq / z.Hk);
@@ -748,7 +759,7 @@ static int far_parts_for(const attn_sizes &z, int N) {
 int attn_bwd_far_parts(const attn_sizes &z) { return far_parts_for(z, z.N); }
 int attn_bwd_far_extra(const attn_sizes &z) { return z.packed ? far_parts_for(z, 1) - far_parts_for(z, z.N) : 0; }
 
-static void fill(bwd_args &a, const attn_sizes &z, const attn_ptrs &p, void *ws, int d) {
+static void fill(bwd_args &a, const attn_sizes &z, const attn_ptrs &p, void *ws, int d, int far_tile) {
   a.q = p.q;
   a.k = p.k;
   a.v = p.v;
@@ -784,19 +795,23 @@ static void fill(bwd_args &a, const attn_sizes &z, const attn_ptrs &p, void *ws,
   a.sinks = z.sinks;
   a.far_parts = z.sinks ? attn_bwd_far_parts(z) : 0;
   a.far_extra = z.sinks ? attn_bwd_far_extra(z) : 0;
-  a.far_step = a.far_extra ? (z.T + a.far_extra - 1) / a.far_extra : 1;
   a.far_rows = attn_bwd_far_rows(z);
   a.far_by_token = attn_bwd_far_by_token(z);
   a.far_sums = z.sinks ? reinterpret_cast<float *>(static_cast<char *>(ws) + attn_bwd_bytes(z, d)) : nullptr;
   a.gs = a.G < 32 ? a.G : 32;
   while (a.G % a.gs)
     --a.gs;
+  // (none where even one sequence of all tokens would take none)
+  const int tb = far_tile / a.gs;
+  if ((z.T - z.window + tb - 1) / tb * (a.G / a.gs) <= FAR_TILES * a.far_parts)
+    a.far_extra = 0;
+  a.far_step = a.far_extra ? (z.T + a.far_extra - 1) / a.far_extra : 1;
 }
 
 template <typename IO, int D>
 hipError_t launch_attn_bwd_dq(const attn_sizes &z, const attn_ptrs &p, void *ws, hipStream_t st) {
   bwd_args a;
-  fill(a, z, p, ws, D);
+  fill(a, z, p, ws, D, FAR_ROWS<IO, D>);
   // (few tiles: 4 waves where their tiles fit shared memory; float32, d = 64,
   // 1543 tokens, 4 heads, window 300: 17 us, 25 with 2)
   constexpr int KT = sizeof(IO) == 2 ? 2 : 1, WN = D * sizeof(IO) <= 256 ? 4 : 2;
@@ -817,7 +832,7 @@ hipError_t launch_attn_bwd_dq(const attn_sizes &z, const attn_ptrs &p, void *ws,
 template <typename IO, int D>
 hipError_t launch_attn_bwd_far(const attn_sizes &z, const attn_ptrs &p, void *ws, hipStream_t st) {
   bwd_args a;
-  fill(a, z, p, ws, D);
+  fill(a, z, p, ws, D, FAR_ROWS<IO, D>);
   const unsigned tiles = static_cast<unsigned>(z.Hk) * ((z.sinks + FAR_KEYS - 1) / FAR_KEYS);
   const unsigned blocks = tiles * (static_cast<unsigned>(z.N) * a.far_parts + a.far_extra);
   hipLaunchKernelGGL((gdn2_attn_dkv_kernel<IO, D, FAR_KEYS / 32, FAR_ROWS<IO, D> / 32, DKV_FAR>), dim3(blocks),
@@ -834,7 +849,7 @@ static void launch_dkv(const bwd_args &a, unsigned blocks, hipStream_t st) {
 template <typename IO, int D>
 hipError_t launch_attn_bwd_dkv(const attn_sizes &z, const attn_ptrs &p, void *ws, hipStream_t st) {
   bwd_args a;
-  fill(a, z, p, ws, D);
+  fill(a, z, p, ws, D, FAR_ROWS<IO, D>);
   // Where the tiles do not give every CU two, the longest sequence's first
   // keys, which every row sees, take as long as the call: d = 64 then takes
   // half as many keys and twice the row parts a workgroup.  (bfloat16, 11 packed
