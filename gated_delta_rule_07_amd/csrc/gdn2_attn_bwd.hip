@@ -14,7 +14,9 @@
 // five, and in exchange every sum has a fixed order (the same bits every run)
 // and no float32 copy of dq passes through memory.  The query rows are the
 // (token, head of the group) pairs of a kv head, so the sum over the heads
-// that share a key row is part of the same product.
+// that share a key row is part of the same product.  delta is formed from the
+// stored o, for bfloat16 rounded (half a step a value): a float32 o would have to be
+// kept from the forward, twice o's bytes.  p and ds are rounded as operands (pack8).
 //
 // Measured, 8 x 4096 tokens, 16 heads on 4, d = 128, window 2048, bfloat16 (206
 // GFLOP a product; an 8192^3 product runs at 1212 TFLOP/s): dq 590 to 610 us
@@ -801,9 +803,10 @@ static void fill(bwd_args &a, const attn_sizes &z, const attn_ptrs &p, void *ws,
   a.gs = a.G < 32 ? a.G : 32;
   while (a.G % a.gs)
     --a.gs;
-  // (none where even one sequence of all tokens would take none)
+  // (none where even one sequence of all tokens would leave far_parts less than 2
+  // FAR_TILES each: workgroups that find nothing to do cost 1 us of the packed d = 64 case)
   const int tb = far_tile / a.gs;
-  if ((z.T - z.window + tb - 1) / tb * (a.G / a.gs) <= FAR_TILES * a.far_parts)
+  if ((z.T - z.window + tb - 1) / tb * (a.G / a.gs) <= 2 * FAR_TILES * a.far_parts)
     a.far_extra = 0;
   a.far_step = a.far_extra ? (z.T + a.far_extra - 1) / a.far_extra : 1;
 }

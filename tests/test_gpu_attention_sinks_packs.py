@@ -3,6 +3,7 @@ against plain float64 forms (bounds as in test_gpu_attention_sinks)."""
 import pytest
 import torch
 
+from test_attention_sinks_limits import far_parts
 from test_gpu_attention_sinks import BF16, F32, cu_of, g, randn, run  # noqa: F401 (g: the fixture)
 
 pytestmark = pytest.mark.gpu
@@ -84,3 +85,57 @@ def test_long_sequence_workspace_and_bits(g):
     for _ in range(4):
         again = g.attn_bwd(q, k, v, o, lse, do, workspace=room[:need], **kw)
         assert all(torch.equal(got[n], again[n]) for n in ("dq", "dk", "dv"))
+
+
+# over 512 sequences of few tokens: each has one workgroup for a kv head's far rows, 16 tiles of
+# which are left to a long one's before it has more by its tokens
+MANY = ([0] * 7 + [3, 0, 1]) * 52
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [64, 128])
+def test_long_sequence_among_hundreds(g, d, dtype):
+    """The far rows of one or two long sequences in parts that they alone have, wherever they stand."""
+    long = 2500
+    assert len(MANY) * 2 >= 1024 and (long - 100) * 4 // 128 > 32
+    for lens in ([long] + MANY, MANY + [long], MANY[:301] + [long] + MANY[301:], [long] + MANY + [1900]):
+        run(g, lens, 8, 2, d, dtype, 100, 4, seed=len(lens), tail=21)
+    # more than 32 sinks, and more of them than tokens
+    run(g, MANY[:200] + [long] + MANY[200:], 8, 2, d, dtype, 64, 50, seed=7)
+    run(g, MANY + [long, 0, 0], 4, 1, d, dtype, 30, 130, seed=8, tail=2)
+
+
+def test_long_sequence_among_hundreds_many_heads(g):
+    """The same with heads of a group in several turns over the tokens."""
+    run(g, MANY[:99] + [1100] + MANY, 66, 2, 64, BF16, 20, 3, seed=11)
+
+
+def test_long_sequence_among_hundreds_workspace_and_bits(g):
+    """The workspace is all that is written, whatever it held before; runs and replays repeat their bits."""
+    lens, Hq, Hk, d = MANY[:250] + [3000] + MANY[250:], 8, 2, 64
+    T, kw = sum(lens), dict(cu_seqlens=cu_of(lens), window=128, sinks=33)
+    print("long sequence among hundreds, workspace", flush=True)
+    q, k, v, do = (randn(95 + i, (1, T, h, d), BF16) for i, h in enumerate((Hq, Hk, Hk, Hq)))
+    o, lse = g.attn_fwd(q, k, v, **kw)
+    need = g.attn_bwd_workspace_bytes(1, T, Hq, Hk, d, BF16, sinks=33, num_seqs=len(lens))
+    room = torch.full((need + 4096,), 0xff, dtype=torch.uint8, device="cuda")
+    want = g.attn_bwd(q, k, v, o, lse, do, workspace=room[:need], **kw)
+    assert (room[need:] == 0xff).all()
+    # (its end holds the parts by tokens: the long sequence's are among them)
+    each, one = (far_parts(T, n, Hk, Hq // Hk, 33) for n in (len(lens), 1))
+    more = (one - each) * 33 * 2 * Hk * d * 4
+    assert each == 1 and (room[need - more:need] != 0xff).any()
+    want = {n: x.clone() for n, x in want.items()}
+    gr = {n: torch.empty_like(x) for n, x in want.items()}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g.attn_bwd(q, k, v, o, lse, do, workspace=room[:need], out=gr, **kw)
+    for i in range(3):
+        again = g.attn_bwd(q, k, v, o, lse, do, workspace=room[:need], **kw)
+        assert all(torch.equal(want[n], again[n]) for n in want)
+        room.fill_(i)
+        for x in gr.values():
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(want[n], gr[n]) for n in want), i
