@@ -240,8 +240,9 @@ def attn_fwd(q, k, v, cu_seqlens=None, window: int = 0, scale: float | None = No
              want_lse: bool = True, sinks: int = 0):
     """Causal attention over whole sequences, with ``window`` > 0 over each
     token's last ``window`` keys (itself included) and its sequence's first
-    ``sinks`` keys (at most 1024).  ``scale`` defaults to d^-0.5.  Returns (o, lse): lse float32 [B, T, Hq] is what the backward
-    needs (None when ``want_lse`` is False and none is given)."""
+    ``sinks`` keys (at most 1024).  ``scale`` defaults to d^-0.5.  Returns
+    (o, lse): lse float32 [B, T, Hq] is what the backward needs (None when
+    ``want_lse`` is False and none is given)."""
     window, sinks = _window(window), _sinks(sinks)
     dev = _device(q, k, v, cu_seqlens)
     B, T, Hq, Hk, d = _heads(q, k, (v, "v"))
@@ -270,7 +271,8 @@ def attn_bwd(q, k, v, o, lse, dout, cu_seqlens=None, window: int = 0, scale: flo
              out=None, sinks: int = 0):
     """Backward of ``attn_fwd``: from its o and lse on the same inputs and
     dL/do, a dict with dq, dk, dv.  ``out`` may hold preallocated tensors
-    under those names."""
+    under those names.  Every 32 sinks read the rows behind the window once
+    more."""
     window, sinks = _window(window), _sinks(sinks)
     dev = _device(q, k, v, o, lse, dout, cu_seqlens)
     B, T, Hq, Hk, d = _heads(q, k, (v, "v"))
@@ -416,7 +418,8 @@ def kv_cache_read(slots, k_cache, v_cache, k_scale=None, v_scale=None, dtype=Non
 
 
 def attn_paged_workspace_bytes(q, k_cache, block_table, cu_seqlens=None, window: int = 0, sinks: int = 0) -> int:
-    """Bytes of workspace ``attn_paged`` needs for these tensors (0: none)."""
+    """Bytes of workspace ``attn_paged`` needs for these tensors (0: none); in
+    bfloat16 with sinks a call may do with less."""
     B, T, Hq, d = q.shape
     ns = 0 if cu_seqlens is None else cu_seqlens.numel() - 1
     return int(lib().gdn2_attn_sink_paged_workspace_bytes(B, T, Hq, k_cache.shape[1], d, ns, k_cache.shape[2],
@@ -480,10 +483,10 @@ def attn_paged_prefix_workspace_bytes(q, k_cache, prefix_table, block_table, cu_
 def attn_paged_prefix(q, k_cache, v_cache, prefix_table, prefix_lens, block_table, seq_lens, cu_groups=None,
                       cu_seqlens=None, k_scale=None, v_scale=None, scale: float | None = None, out=None, lse=None,
                       want_lse: bool = False, workspace=None):
-    """``attn_paged`` (without a window) for sequences that share a prefix,
-    whose keys are read once for all of them.  Group m is the sequences
-    ``cu_groups[m]`` .. ``cu_groups[m + 1] - 1`` (int32 [M + 1]; None: one group
-    of all) behind the prefix of ``prefix_lens[m]`` keys (int32 [M]) in the
+    """``attn_paged`` (without a window or sinks: for layers of full attention)
+    for sequences that share a prefix, whose keys are read once for all of
+    them.  Group m is the sequences ``cu_groups[m]`` .. ``cu_groups[m + 1] - 1``
+    (int32 [M + 1]; None: one group of all) behind the prefix of ``prefix_lens[m]`` keys (int32 [M]) in the
     pages ``prefix_table[m]`` (int32 [M, max pages]); ``block_table`` and
     ``seq_lens`` hold what each sequence has of its own, its new tokens
     included.  Returns (o, lse or None)."""

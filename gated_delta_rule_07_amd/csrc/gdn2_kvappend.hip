@@ -11,9 +11,12 @@
 // D / 8 lanes a head (q's, then k's, then v's), as in gdn2_rope_fwd_kernel, so
 // that the sines and cosines are formed once a token and a row's sum and
 // largest magnitude take 3 or 4 lane exchanges.  Measured, 32768 tokens x (16 + 4 +
-// 4) heads, d = 128, bfloat16: into e4m3 81 us (370 MB, 4.6 TB/s; the two calls it
-// stands for 88), into bfloat16 80 us (403 MB, 5 TB/s); a large copy runs at 4.7
-// TB/s.  32 tokens (a decode step): 4.2 us, a launch's own latency.
+// 4) heads, d = 128, bfloat16, three sets of inputs in turn, shuffled slots: into e4m3
+// 76 to 81 us (370 MB, 4.6 to 4.9 TB/s) where the two calls it stands for take 84 to 90
+// on the same cards (61 to 64 and 22 to 23), into bfloat16 78 to 80 (403 MB, 5.1 TB/s)
+// and 94 to 98 (62 to 65 and 29); q, k and v as parts of one projection add 1 to 3, and
+// copying them out for the two calls 83.  A large copy runs at 4.7 TB/s.  32 tokens (a
+// decode step): 4.2 us, a launch's own latency.
 #include "gdn2_kvrow.hpp"
 #include "gdn2_rope.hpp"
 

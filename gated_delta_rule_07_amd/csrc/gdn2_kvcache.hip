@@ -16,7 +16,8 @@
 // row, 8 values (16 bytes of bfloat16) each, so a row's maximum takes 3 or 4
 // lane exchanges and every access of a wave is whole rows.  Measured, 32768
 // tokens x 4 kv heads, d = 128, bfloat16 to e4m3: write 19.3 us (102 MB,
-// 5.3 TB/s), read 17.6 us (5.8 TB/s); a batch of 333 tokens x 3 heads, d = 64:
+// 5.3 TB/s; 22 to 23 where three sets of inputs take turns, so that none is still
+// in a cache), read 17.6 us (5.8 TB/s); a batch of 333 tokens x 3 heads, d = 64:
 // 3.5 us each, a launch's own latency.
 #include "gdn2_kvrow.hpp"
 

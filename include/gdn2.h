@@ -502,7 +502,8 @@ gdn2_status_t gdn2_attn_bwd(const void *q, const void *k, const void *v, const v
  * (127 for a row of zeros), and the codes are x * 2^-e rounded to nearest
  * even: code * 2^e is exact in float32, and in bfloat16 for e >= -124 or rows
  * that were bfloat16 (else, largest magnitude up to 448 * 2^-125, the smallest
- * codes may lie under its smallest subnormal and are rounded once).  A row
+ * codes may lie under its smallest subnormal and are rounded once; a magnitude
+ * from 248 * 2^120, 3.3e38, on rounds to 2^128, an infinity in both).  A row
  * holding an infinity or NaN gets the byte 255 and stands for NaN throughout.
  *
  * gdn2_kv_cache_write stores n tokens' keys and values, [n, Hk, d], into
@@ -602,7 +603,8 @@ gdn2_status_t gdn2_attn_paged_prefix(const void *q, const void *k_cache, const v
  * head, 32 sinks) triples (GDN2_ERR_UNSUPPORTED).  In the paged form the sinks
  * are the sequence's first keys; table entries whose page holds neither a sink
  * nor a key of a query's window are not read, so such pages can be freed and
- * used again. */
+ * used again.  The backward reads the rows behind the window once more for
+ * every 32 sinks. */
 gdn2_status_t gdn2_attn_sink_fwd(const void *q, const void *k, const void *v, const int32_t *cu_seqlens, int B, int T,
                                  int Hq, int Hk, int d, int num_seqs, int window, int sinks, float scale,
                                  gdn2_dtype_t dt, void *o, float *lse, void *stream);
@@ -618,6 +620,8 @@ gdn2_status_t gdn2_attn_sink_bwd(const void *q, const void *k, const void *v, co
                                  int num_seqs, int window, int sinks, float scale, gdn2_dtype_t dt, void *dq, void *dk,
                                  void *dv, void *workspace, size_t workspace_bytes, void *stream);
 
+/* As gdn2_attn_paged_workspace_bytes, for either dtype; in bfloat16 a call of
+ * few rows may need none of it. */
 size_t gdn2_attn_sink_paged_workspace_bytes(int B, int T, int Hq, int Hk, int d, int num_seqs, int page_size,
                                             int max_pages, int window, int sinks);
 
