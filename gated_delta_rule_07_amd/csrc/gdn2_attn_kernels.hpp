@@ -84,7 +84,7 @@ inline bool attn_bwd_far_by_token(const attn_sizes &z) { return static_cast<long
 inline size_t attn_bwd_far_rows(const attn_sizes &z) {
   return attn_bwd_far_by_token(z) ? static_cast<size_t>(z.Ttot) : static_cast<size_t>(z.N) * z.sinks;
 }
-// Packed sequences share as many parts more by their tokens.
+// Parts beyond those that packed sequences share out by their tokens.
 int attn_bwd_far_extra(const attn_sizes &z);
 inline size_t attn_bwd_far_bytes(const attn_sizes &z, int d) {
   if (!z.sinks)
